@@ -5,3 +5,4 @@ this package is its Python binding.  Build it with ``build.build()``.
 """
 from ._lib import (BUFFER_NAMES, Buffers, Config, DQError, KVCache, TensorCfg, kv_sizes, load,  # noqa: F401
                    make_config, symbol_probs)
+from .pages import PagePool, PagesConfig, make_pages_config, pages_sizes  # noqa: F401

@@ -37,7 +37,7 @@ def sources():
 
 def _deps():
     return sources() + [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".h", ".cuh"))] + \
-        [os.path.join(INCLUDE, "dq.h")]
+        [os.path.join(INCLUDE, f) for f in os.listdir(INCLUDE)]
 
 
 def up_to_date(lib: str = LIB) -> bool:

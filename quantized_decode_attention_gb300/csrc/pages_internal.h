@@ -1,0 +1,87 @@
+// Internal declarations of the paged cache: geometry, kernel arguments, launchers.
+#pragma once
+
+#include <cstddef>
+#include <cstdint>
+
+#include "dq_pages.h"
+
+namespace dq {
+
+// Bits of the status word beside those of dq_internal.h that the paged cache shares
+// (1 non-finite input, 2 timeout).
+enum : unsigned {
+    PST_NONFINITE = 1u,
+    PST_TIMEOUT = 2u,
+    PST_FULL = 64u,    // resize: too few free pages
+    PST_ARG = 128u,    // a row, length or count out of range, or a row named twice
+    PST_TABLE = 256u,  // a page number out of range
+    PST_SHARED = 512u  // an append to a page that several rows hold
+};
+
+// Pool geometry and pointers, passed to every kernel by value.
+struct PagesView {
+    int n_layers, n_pages, P, Hkv, Hq, G, d, max_seqs, M;
+    int bf16;             // dtype: 1 bf16, 0 fp16
+    int blk;              // tokens per block, min(P, 64)
+    int page_bytes;       // of one KV head
+    int sum_bytes;
+    int k_exp, v_exp;
+    uint8_t *pages;       // the layer's first page (append .. select), or the pool's
+    uint8_t *summary;
+    int *table, *seq_len, *refs;
+    unsigned *status;
+};
+
+// Which rows and new tokens a call is about.
+struct PagesRows {
+    const int *rows, *cu;
+    int n_rows, n_tok, max_new;
+};
+
+// The int part of the workspace: [0] copies or moves of the last plan, [1] live pages
+// below which moves end, then three lists of n_pages.
+constexpr int PAGES_WS_HEAD = 16;
+
+struct PagesStoreArgs {
+    PagesView p;
+    PagesRows r;
+    const uint16_t *k, *v;
+    long long kt, kh, vt, vh;
+};
+struct PagesReadArgs {
+    PagesView p;
+    PagesRows r;
+    uint16_t *k, *v;
+};
+struct PagesAttnArgs {
+    PagesView p;
+    PagesRows r;
+    const uint16_t *q;
+    long long qt, qh;
+    uint16_t *out;
+    float *lse;
+    const int *sel;
+    int n_sel;
+    float scale_log2;     // sm_scale 2^k_exp log2(e)
+    float out_scale;      // 2^v_exp
+};
+struct PagesSelectArgs {
+    PagesView p;
+    PagesRows r;
+    const uint16_t *q;
+    long long qt, qh;
+    int *sel;
+    int n_sel, keep_first, keep_last;
+};
+
+// launchers (return cudaError_t as int)
+int launch_pages_resize(const PagesView &p, const int *rows, const int *lens, int n, int *ws, int num_sms, void *stream);
+int launch_pages_fork(const PagesView &p, const int *src, const int *dst, int n, void *stream);
+int launch_pages_compact(const PagesView &p, int *ws, int num_sms, void *stream);
+int launch_pages_append(const PagesStoreArgs &a, void *stream);
+int launch_pages_read(const PagesReadArgs &a, void *stream);
+int launch_pages_attention(const PagesAttnArgs &a, void *stream);
+int launch_pages_select(const PagesSelectArgs &a, void *stream);
+
+}  // namespace dq
