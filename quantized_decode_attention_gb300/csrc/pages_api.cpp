@@ -130,7 +130,7 @@ dq_status dq_pages_sizes(const dq_pages_config *cfg, size_t bytes[DQ_PAGES_NUM_B
     bytes[3] = static_cast<size_t>(cfg->max_seqs) * 4;
     bytes[4] = static_cast<size_t>(cfg->n_pages) * 4;
     bytes[5] = 16;
-    bytes[6] = (dq::PAGES_WS_HEAD + 3 * static_cast<size_t>(cfg->n_pages)) * 4;
+    bytes[6] = dq::pages_ws_bytes(cfg->n_pages);
     return ok();
 }
 
@@ -222,7 +222,10 @@ dq_status dq_pages_attention(const dq_pages_config *cfg, const dq_pages_buffers 
     a.n_sel = sel ? n_sel : 0;
     a.scale_log2 = static_cast<float>(std::ldexp(static_cast<double>(sm_scale) * 1.4426950408889634074, cfg->k_exp));
     a.out_scale = std::ldexp(1.0f, cfg->v_exp);
-    return launched(dq::launch_pages_attention(a, stream), "attention launch");
+    uint8_t *ws = static_cast<uint8_t *>(bufs->workspace) + dq::pages_ws_lists(cfg->n_pages);
+    a.tickets = reinterpret_cast<int *>(ws);
+    a.records = reinterpret_cast<float *>(ws + dq::PAGES_MAX_CTAS * 4);
+    return launched(dq::launch_pages_attention(a, device_sms(), stream), "attention launch");
 }
 
 dq_status dq_pages_select(const dq_pages_config *cfg, const dq_pages_buffers *bufs, int layer, const void *q,

@@ -2,7 +2,32 @@
 //
 // For a query at position x, with z_j = sm_scale q . k_j over the visible keys j <= x:
 //   m = max z_j, l = sum exp(z_j - m), out = sum exp(z_j - m) v_j / l, lse = m + log l
-// in one pass: a running m, l and accumulator, rescaled when m grows.
+// in one pass over the pages.
+//
+// Work.  A unit is 8 NT query rows (token, query head of the group) of one row and KV
+// head; it walks the row's tokens in tiles of 16 (a tile lies in one page whatever the
+// page size).  All units' tiles, in order, are cut into equal shares, one for each warp
+// of one CTA per SM, so that ragged lengths and small batches fill the card alike.  A
+// warp that holds all of a unit writes its output; parts of a unit meet in shared
+// memory, and parts in several CTAs in the workspace, where the last CTA to arrive
+// adds them up in CTA order (so that the result does not depend on timing; nobody waits).
+//
+// A tile.  Codes and scales come straight to registers, 16 bytes a lane, two tiles ahead
+// of their use: with 16 warps that keeps some 55 KB in flight per SM, which is what
+// HBM's latency asks for, without shared memory or barriers.  The page layout is made
+// for it: a lane's 16 bytes are its own operands.  Codes become binary16 by one
+// conversion and one multiplication by the scale, both exact (2 + 4 significant bits,
+// multiples of 2^-10 below 2^12).  Both products run on mma.sync m16n8k16 with
+// the cache as the 16-row operand: K [16 tokens x 16 channels] . Q^T and
+// V^T [16 channels x 16 tokens] . P, in which 8 query rows fill the n of 8.
+// Lane (g, t) = (lane / 4, lane % 4) holds, of D / 4 channels at t D / 4, tokens g and
+// g + 8 of K; of D / 8 channels at g D / 8, token pairs t and t + 4 of V.
+//
+// Rounding.  Queries are scaled by a power of two to at most 2^14 and are exact in
+// binary16 down to 2^-38 of their row's largest.  Weights exp2(z - m + 7) are rounded to
+// binary16 for P . V (11 bits; 8 bits of slack for m, which is raised only when a logit
+// passes it by 2^8, and 7 bits up so that weights below binary16's normal range are
+// those under 2^-21); sums, logits and accumulators are fp32.
 #include <cuda_runtime.h>
 
 #include "pages.cuh"
@@ -10,104 +35,547 @@
 namespace dq {
 namespace {
 
-constexpr int AT_THREADS = 128, AT_ROWS = 8, AT_CH = 32;
 constexpr float LN2 = 0.69314718055994530942f;
+constexpr float SLACK = 8.f, LIFT = 7.f;   // log2 units
+constexpr int MIN_TILES = 32;              // tiles that make a CTA worth its merge
 
-// One CTA per (8 query rows of a row and KV head); a query row is a (token, query head
-// of the group).  Keys and values of up to 32 tokens at a time are expanded to fp32.
+// ---- one tile in registers ---------------------------------------------------------------
 template <int D>
-__global__ void __launch_bounds__(AT_THREADS) attn_simple(PagesAttnArgs a) {
-    __shared__ float kf[AT_CH][D + 1], vf[AT_CH][D];
-    __shared__ float qf[AT_ROWS][D], pr[AT_ROWS][AT_CH], al[AT_ROWS], ls[AT_ROWS], ms[AT_ROWS];
+struct Tile {
+    uint32_t k[2][D / 32], v[2][D / 32];  // tokens g, g + 8; pairs t, t + 4
+    uint32_t ks[2], vs[2];
+    int pos;                              // position of the first token, -1: nothing to do
+};
+
+template <int N>
+__device__ __forceinline__ void ld_words(const uint8_t *p, uint32_t (&w)[N]) {
+    if (N == 4) {
+        asm("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];\n" : "=r"(w[0]), "=r"(w[1]), "=r"(w[N > 2 ? 2 : 0]), "=r"(w[N > 3 ? 3 : 0]) : "l"(p));
+    } else {
+        asm("ld.global.nc.L1::no_allocate.v2.u32 {%0,%1}, [%2];\n" : "=r"(w[0]), "=r"(w[1]) : "l"(p));
+    }
+}
+
+// Tile at token `off` of a page (a multiple of 16).
+template <int D>
+__device__ __forceinline__ void load_tile(Tile<D> &x, const uint8_t *page, int off, int b) {
     using B = PageBlock<D>;
-    const PagesView &p = a.p;
-    const PageRow r = page_row(p, a.r, blockIdx.y);
-    const int head = blockIdx.z, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int m0 = blockIdx.x * AT_ROWS, rows = r.n * p.G;
-    if (m0 >= rows) return;
-    for (int i = tid; i < AT_ROWS * D; i += AT_THREADS) {
-        const int m = m0 + i / D;
-        float x = 0.f;
-        if (m < rows) x = from16(a.q[(static_cast<long long>(r.q0) + m / p.G) * a.qt + (head * p.G + m % p.G) * a.qh + i % D], p.bf16);
-        qf[i / D][i % D] = x;
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    const uint8_t *blk = page + (off / b) * B::size(b);
+    const int o = off % b;
+    const uint8_t *kc = blk + (o + g) * (D / 2) + t * (D / 8);
+    ld_words(kc, x.k[0]);
+    ld_words(kc + 4 * D, x.k[1]);
+    const uint8_t *vc = blk + B::vc(b) + o * (D / 2) + ((D == 128 ? g : g >> 1) * 4 + t) * 16 + (D == 128 ? 0 : (g & 1) * 8);
+    ld_words(vc, x.v[0]);
+    ld_words(vc + 4 * D, x.v[1]);
+    const uint8_t *ks = blk + B::ks(b) + (o + g) * (D / 16) + t * (D / 64);
+    const uint8_t *vs = blk + B::vs(b) + o * (D / 16) + ((D == 128 ? g : g >> 1) * 4 + t) * 2;
+    if (D == 128) {
+        x.ks[0] = *reinterpret_cast<const uint16_t *>(ks);
+        x.ks[1] = *reinterpret_cast<const uint16_t *>(ks + D / 2);
+    } else {
+        x.ks[0] = *ks;
+        x.ks[1] = *(ks + D / 2);
     }
-    if (tid < AT_ROWS) {
-        ms[tid] = -INFINITY;
-        ls[tid] = 0.f;
+    x.vs[0] = *reinterpret_cast<const uint16_t *>(vs);
+    x.vs[1] = *reinterpret_cast<const uint16_t *>(vs + D / 2);
+}
+
+__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("mul.rn.f16x2 %0, %1, %2;\n" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;\n" : "=r"(y) : "r"(x));
+    return y;
+}
+__device__ __forceinline__ uint32_t half2_of(float a, float b) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;\n" : "=r"(r) : "f"(b), "f"(a));
+    return r;
+}
+
+// ---- a warp's state over a unit: lane (g, t) holds query rows 2t and 2t + 1 of each n tile ----
+template <int D, int NT>
+struct State {
+    uint32_t q[NT][D / 16][2];
+    float f[NT][2];            // logit units: sm_scale log2(e) 2^k_exp, and the row's power of two
+    int pos[NT][2];            // positions of the rows
+    float m[NT][2], l[NT][2];  // m the same in every lane of a row; l this lane's part
+    float acc[NT][D / 16][4];  // [channel g D/8 + 2 mi (+ 1: 2, 3)][row 2t (+ 1: 1, 3)]
+
+    __device__ __forceinline__ void reset() {
+#pragma unroll
+        for (int n = 0; n < NT; n++) {
+            m[n][0] = m[n][1] = -INFINITY;
+            l[n][0] = l[n][1] = 0.f;
+#pragma unroll
+            for (int i = 0; i < D / 16; i++) acc[n][i][0] = acc[n][i][1] = acc[n][i][2] = acc[n][i][3] = 0.f;
+        }
     }
-    float acc[AT_ROWS];
+
+    // Queries of rows row0 .. row0 + 8 NT of the unit's (token, head) rows.
+    __device__ __forceinline__ void load_q(const PagesAttnArgs &a, const PageRow &r, int head, int row0) {
+        const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+        const int rows = r.n * a.p.G;
 #pragma unroll
-    for (int i = 0; i < AT_ROWS; i++) acc[i] = 0.f;
-    const int ch = p.P < AT_CH ? p.P : AT_CH;
-    const int entries = a.sel ? a.n_sel : (r.len + p.P - 1) / p.P;
-    for (int e = 0; e < entries; e++) {
-        const int ord = a.sel ? a.sel[(static_cast<long long>(blockIdx.y) * p.Hkv + head) * a.n_sel + e] : e;
-        if (ord < 0 || ord >= p.M || ord * p.P >= r.len) continue;
-        const int id = page_of(p, r.row, ord);
-        if (id < 0) continue;
-        const uint8_t *page = page_ptr(p, id, head);
-        for (int s0 = 0; s0 < p.P && ord * p.P + s0 < r.len; s0 += ch) {
-            __syncthreads();
-            const int pos0 = ord * p.P + s0;
-            for (int i = tid; i < AT_CH * (D / 16); i += AT_THREADS) {
-                const int t = i / (D / 16), c = i % (D / 16), tp = s0 + t, tb = tp % p.blk;
-                const bool in = t < ch && pos0 + t < r.len;
-                const uint8_t *blk = page + (tp / p.blk) * B::size(p.blk);
-                const float ks = in ? e4m3_to_float(blk[B::ks(p.blk) + tb * (D / 16) + c]) : 0.f;
-                const float vs = in ? e4m3_to_float(blk[B::vs(p.blk) + B::vscale(tb, c)]) : 0.f;
-                const uint8_t *kc = blk + tb * (D / 2) + 8 * c, *vc = blk + B::vc(p.blk) + B::vcode(tb, c);
-                for (int x = 0; x < 16; x++) {
-                    kf[t][16 * c + x] = in ? e2m1_to_float((kc[x >> 1] >> (4 * (x & 1))) & 15u) * ks : 0.f;
-                    vf[t][16 * c + x] = in ? e2m1_to_float((vc[x] >> (4 * (tp & 1))) & 15u) * vs : 0.f;
+        for (int n = 0; n < NT; n++) {
+            const int row = row0 + 8 * n + g;
+            float x[D / 4];
+            float top = 0.f;
+            if (row < rows) {
+                const int tok = row / a.p.G;
+                const uint16_t *src = a.q + (static_cast<long long>(r.q0) + tok) * a.qt + (head * a.p.G + row - tok * a.p.G) * a.qh + t * (D / 4);
+#pragma unroll
+                for (int i = 0; i < D / 32; i++) {
+                    const uint4 w = *reinterpret_cast<const uint4 *>(src + 8 * i);
+                    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                    for (int j = 0; j < 4; j++) {
+                        x[8 * i + 2 * j] = from16(static_cast<uint16_t>(u[j] & 0xffffu), a.p.bf16);
+                        x[8 * i + 2 * j + 1] = from16(static_cast<uint16_t>(u[j] >> 16), a.p.bf16);
+                    }
                 }
+            } else {
+#pragma unroll
+                for (int i = 0; i < D / 4; i++) x[i] = 0.f;
             }
-            __syncthreads();
-            // warp w: query rows 2w and 2w + 1, lane = token
 #pragma unroll
-            for (int i = 0; i < 2; i++) {
-                const int m = 2 * warp + i, pos = r.len - r.n + (m0 + m) / p.G;
-                float z = 0.f;
-                for (int c = 0; c < D; c++) z += qf[m][c] * kf[lane][c];
-                z = m0 + m < rows && lane < ch && pos0 + lane <= pos ? z * a.scale_log2 : -INFINITY;
-                const float mx = fmaxf(ms[m], warp_max(z)), mu = mx == -INFINITY ? 0.f : mx;
-                const float w = exp2f(z - mu), sum = warp_sum(w);
-                pr[m][lane] = w;
-                __syncwarp();
-                if (lane == 0) {
-                    al[m] = exp2f(ms[m] - mu);
-                    ls[m] = ls[m] * al[m] + sum;
-                    ms[m] = mx;
-                }
-                __syncwarp();
+            for (int i = 0; i < D / 4; i++) top = fmaxf(top, fabsf(x[i]));
+            top = fmaxf(top, __shfl_xor_sync(FULL, top, 1));
+            top = fmaxf(top, __shfl_xor_sync(FULL, top, 2));
+            // top < 2^(e + 1) -> scaled below 2^14
+            int up = 13 - (static_cast<int>(__float_as_uint(top) >> 23) - 127);
+            up = top > 0.f ? (up > 126 ? 126 : up) : 0;
+            const float s = pow2i(up);
+#pragma unroll
+            for (int i = 0; i < D / 16; i++) {
+                q[n][i][0] = half2_of(x[4 * i] * s, x[4 * i + 1] * s);
+                q[n][i][1] = half2_of(x[4 * i + 2] * s, x[4 * i + 3] * s);
             }
-            __syncthreads();
-            if (tid < D) {
 #pragma unroll
-                for (int m = 0; m < AT_ROWS; m++) {
-                    acc[m] *= al[m];
-                    for (int t = 0; t < AT_CH; t++) acc[m] += pr[m][t] * vf[t][tid];
-                }
+            for (int e = 0; e < 2; e++) {
+                const int other = __shfl_sync(FULL, up, 4 * (2 * t + e));
+                const int rw = row0 + 8 * n + 2 * t + e;
+                f[n][e] = a.scale_log2 * pow2i(-other);
+                pos[n][e] = rw < rows ? r.len - r.n + rw / a.p.G : 0x7fffffff;  // no row: nothing to mask
             }
         }
     }
-    __syncthreads();
+
+    __device__ __forceinline__ void step(const Tile<D> &x, int len, int least) {
+        const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+        float s[NT][4];
 #pragma unroll
-    for (int m = 0; m < AT_ROWS; m++) {
-        if (m0 + m >= rows) break;
-        const long long o = (static_cast<long long>(r.q0) + (m0 + m) / p.G) * p.Hq + head * p.G + (m0 + m) % p.G;
-        if (tid < D) a.out[o * D + tid] = to16(ls[m] == 0.f ? 0.f : acc[m] * a.out_scale / ls[m], p.bf16);
-        if (tid == 0 && a.lse) a.lse[o] = ls[m] == 0.f ? -INFINITY : (ms[m] + log2f(ls[m])) * LN2;
+        for (int n = 0; n < NT; n++) s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.f;
+        uint32_t sc[2][2];  // key scales of tokens g, g + 8: both halves of a register each
+#pragma unroll
+        for (int h = 0; h < 2; h++) {
+            const uint32_t two = e4m3x2_to_half2(static_cast<uint16_t>(x.ks[h]));
+            sc[h][0] = __byte_perm(two, two, 0x1010);
+            sc[h][1] = D == 128 ? __byte_perm(two, two, 0x3232) : sc[h][0];
+        }
+#pragma unroll
+        for (int w = 0; w < D / 32; w++) {
+            uint32_t a[4], b[4];
+            e2m1x8_to_half(x.k[0][w], a);
+            e2m1x8_to_half(x.k[1][w], b);
+#pragma unroll
+            for (int i = 0; i < 4; i++) {
+                a[i] = hmul2(a[i], sc[0][w >> 1]);
+                b[i] = hmul2(b[i], sc[1][w >> 1]);
+            }
+#pragma unroll
+            for (int n = 0; n < NT; n++) {
+                mma_f16(s[n], a[0], b[0], a[1], b[1], q[n][2 * w][0], q[n][2 * w][1]);
+                mma_f16(s[n], a[2], b[2], a[3], b[3], q[n][2 * w + 1][0], q[n][2 * w + 1][1]);
+            }
+        }
+        // s: tokens g (0, 1) and g + 8 (2, 3), rows 2t (0, 2) and 2t + 1 (1, 3)
+        const bool tail = x.pos + 15 > least;  // a token that some row does not see
+        bool grow = false;
+#pragma unroll
+        for (int n = 0; n < NT; n++)
+#pragma unroll
+            for (int i = 0; i < 4; i++) {
+                float z = s[n][i] * f[n][i & 1];
+                if (tail && x.pos + g + 8 * (i >> 1) > pos[n][i & 1]) z = -INFINITY;
+                s[n][i] = z;
+                grow |= z > m[n][i & 1] + SLACK;  // also the first finite logit
+            }
+        if (__any_sync(FULL, grow)) {
+#pragma unroll
+            for (int n = 0; n < NT; n++)
+#pragma unroll
+                for (int e = 0; e < 2; e++) {
+                    float top = fmaxf(s[n][e], s[n][e + 2]);
+                    top = fmaxf(top, __shfl_xor_sync(FULL, top, 4));
+                    top = fmaxf(top, __shfl_xor_sync(FULL, top, 8));
+                    top = fmaxf(top, __shfl_xor_sync(FULL, top, 16));
+                    top = fmaxf(top, m[n][e]);
+                    const float al = top == -INFINITY ? 1.f : ex2(m[n][e] - top);
+                    m[n][e] = top;
+                    l[n][e] *= al;
+#pragma unroll
+                    for (int i = 0; i < D / 16; i++) {
+                        acc[n][i][e] *= al;
+                        acc[n][i][e + 2] *= al;
+                    }
+                }
+        }
+        uint32_t p[NT][2];
+#pragma unroll
+        for (int n = 0; n < NT; n++) {
+#pragma unroll
+            for (int i = 0; i < 4; i++) {
+                const float mu = m[n][i & 1] == -INFINITY ? 0.f : m[n][i & 1] - LIFT;
+                s[n][i] = ex2(s[n][i] - mu);
+                l[n][i & 1] += s[n][i];
+            }
+            p[n][0] = transpose8(half2_of(s[n][0], s[n][1]));
+            p[n][1] = transpose8(half2_of(s[n][2], s[n][3]));
+        }
+        uint32_t v0 = e4m3x2_to_half2(static_cast<uint16_t>(x.vs[0])), v1 = e4m3x2_to_half2(static_cast<uint16_t>(x.vs[1]));
+        if (x.pos + 15 >= len) {  // tokens that are not there may hold anything, NaN scales too: 0 . NaN must not count
+            v0 &= (x.pos + 2 * t < len ? 0x0000ffffu : 0u) | (x.pos + 2 * t + 1 < len ? 0xffff0000u : 0u);
+            v1 &= (x.pos + 2 * t + 8 < len ? 0x0000ffffu : 0u) | (x.pos + 2 * t + 9 < len ? 0xffff0000u : 0u);
+        }
+#pragma unroll
+        for (int w = 0; w < D / 32; w++) {
+            uint32_t a[4], b[4];
+            e2m1x8_to_half(x.v[0][w], a);
+            e2m1x8_to_half(x.v[1][w], b);
+#pragma unroll
+            for (int i = 0; i < 4; i++) {
+                a[i] = hmul2(a[i], v0);
+                b[i] = hmul2(b[i], v1);
+            }
+#pragma unroll
+            for (int n = 0; n < NT; n++) {
+                mma_f16(acc[n][2 * w], a[0], a[1], b[0], b[1], p[n][0], p[n][1]);
+                mma_f16(acc[n][2 * w + 1], a[2], a[3], b[2], b[3], p[n][0], p[n][1]);
+            }
+        }
     }
+
+    __device__ __forceinline__ void sum_l() {
+#pragma unroll
+        for (int n = 0; n < NT; n++)
+#pragma unroll
+            for (int e = 0; e < 2; e++) {
+                l[n][e] += __shfl_xor_sync(FULL, l[n][e], 4);
+                l[n][e] += __shfl_xor_sync(FULL, l[n][e], 8);
+                l[n][e] += __shfl_xor_sync(FULL, l[n][e], 16);
+            }
+    }
+
+    // A part of a unit: [8 NT][D] accumulators, then m, then l of each row.
+    __device__ __forceinline__ void to_record(float *rec) {
+        sum_l();
+        const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+#pragma unroll
+        for (int n = 0; n < NT; n++)
+#pragma unroll
+            for (int e = 0; e < 2; e++) {
+                const int row = 8 * n + 2 * t + e;
+#pragma unroll
+                for (int i = 0; i < D / 16; i++)
+                    *reinterpret_cast<float2 *>(rec + row * D + g * (D / 8) + 2 * i) = make_float2(acc[n][i][e], acc[n][i][e + 2]);
+                if (g == 0) {
+                    rec[8 * NT * D + row] = m[n][e];
+                    rec[8 * NT * (D + 1) + row] = l[n][e];
+                }
+            }
+    }
+
+    // A whole unit: the rows' outputs.
+    __device__ __forceinline__ void to_output(const PagesAttnArgs &a, const PageRow &r, int head, int row0) {
+        sum_l();
+        const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+        const int rows = r.n * a.p.G;
+#pragma unroll
+        for (int n = 0; n < NT; n++)
+#pragma unroll
+            for (int e = 0; e < 2; e++) {
+                const int row = row0 + 8 * n + 2 * t + e;
+                if (row >= rows) continue;
+                const int tok = row / a.p.G;
+                const long long o = (static_cast<long long>(r.q0) + tok) * a.p.Hq + head * a.p.G + row - tok * a.p.G;
+                const float w = l[n][e] == 0.f ? 0.f : a.out_scale / l[n][e];
+                uint32_t u[D / 16];
+#pragma unroll
+                for (int i = 0; i < D / 16; i++)
+                    u[i] = pack2(to16(acc[n][i][e] * w, a.p.bf16), to16(acc[n][i][e + 2] * w, a.p.bf16));
+                uint4 *dst = reinterpret_cast<uint4 *>(a.out + o * D + g * (D / 8));
+#pragma unroll
+                for (int i = 0; i < D / 64; i++) dst[i] = make_uint4(u[4 * i], u[4 * i + 1], u[4 * i + 2], u[4 * i + 3]);
+                if (a.lse && g == 0) a.lse[o] = l[n][e] == 0.f ? -INFINITY : (m[n][e] - LIFT + log2f(l[n][e])) * LN2;
+            }
+    }
+};
+
+// ---- the call's units --------------------------------------------------------------------
+// Unit `unit` of row i (head-major, query blocks within), its first tile and tile count.
+struct Unit {
+    int i, head, row0;
+    long long first;
+    int tiles;
+};
+
+template <int D, int NT, int NW>
+struct Shared {
+    static constexpr int REC = 8 * NT * (D + 2);  // floats of a record
+    float rec[NW][2][REC];  // each warp's parts: of a unit begun before it, of one that goes on after it
+    long long first[DQ_PAGES_MAX_ROWS + 1];  // tiles before row i
+    int tiles[DQ_PAGES_MAX_ROWS];            // of each of the row's units
+    long long part[NW];
+    long long unit[2 * NW];  // first tile of the unit that each record is a part of, -1: none
+    int list[2 * NW], n_list, last;
+};
+
+__device__ __forceinline__ int row_tiles(const PagesAttnArgs &a, int len) {
+    // every unit has a tile, so that queries that see nothing get their zeros
+    const int n = a.sel ? (len > 0 ? a.n_sel * (a.p.P >> 4) : 0) : (len + 15) >> 4;
+    return n > 1 ? n : 1;
+}
+
+// The unit that holds tile x.
+template <int D, int NT, int NW>
+__device__ __forceinline__ Unit find_unit(const Shared<D, NT, NW> &sh, int n_rows, int Hkv, long long x) {
+    int lo = 0, hi = n_rows - 1;
+    while (lo < hi) {  // the last row whose first tile is <= x (rows without tiles share it with the next)
+        const int mid = (lo + hi + 1) >> 1;
+        if (sh.first[mid] <= x) lo = mid;
+        else hi = mid - 1;
+    }
+    Unit u;
+    u.i = lo;
+    u.tiles = sh.tiles[lo];
+    const long long in = x - sh.first[lo];
+    const int unit = static_cast<int>(in / u.tiles);
+    u.first = sh.first[lo] + static_cast<long long>(unit) * u.tiles;
+    const int blocks = static_cast<int>((sh.first[lo + 1] - sh.first[lo]) / (static_cast<long long>(u.tiles) * Hkv));
+    u.head = unit / blocks;
+    u.row0 = (unit % blocks) * 8 * NT;
+    return u;
+}
+
+// One thread's 4 channels at c of row `row` over n records, added up in order.
+template <int D, int NT, class F>
+__device__ __forceinline__ void add_records(int n, int row, int c, F rec_of, float (&acc)[4], float &m, float &l) {
+    m = -INFINITY;
+    for (int k = 0; k < n; k++) m = fmaxf(m, rec_of(k)[8 * NT * D + row]);
+    l = 0.f;
+    acc[0] = acc[1] = acc[2] = acc[3] = 0.f;
+    for (int k = 0; k < n; k++) {
+        const float *r = rec_of(k);
+        const float mk = r[8 * NT * D + row], w = mk == -INFINITY ? 0.f : ex2(mk - m);
+        l += w * r[8 * NT * (D + 1) + row];
+        const float4 x = *reinterpret_cast<const float4 *>(r + row * D + c);
+        acc[0] += w * x.x;
+        acc[1] += w * x.y;
+        acc[2] += w * x.z;
+        acc[3] += w * x.w;
+    }
+}
+
+template <int D>
+__device__ __forceinline__ void write4(const PagesAttnArgs &a, const PageRow &r, int head, int row, int c, const float (&acc)[4], float m, float l) {
+    if (row >= r.n * a.p.G) return;
+    const int tok = row / a.p.G;
+    const long long o = (static_cast<long long>(r.q0) + tok) * a.p.Hq + head * a.p.G + row - tok * a.p.G;
+    const float w = l == 0.f ? 0.f : a.out_scale / l;
+    *reinterpret_cast<uint2 *>(a.out + o * D + c) =
+        make_uint2(pack2(to16(acc[0] * w, a.p.bf16), to16(acc[1] * w, a.p.bf16)), pack2(to16(acc[2] * w, a.p.bf16), to16(acc[3] * w, a.p.bf16)));
+    if (a.lse && c == 0) a.lse[o] = l == 0.f ? -INFINITY : (m - LIFT + log2f(l)) * LN2;
+}
+
+template <int D, int NT, int NW>
+__global__ void __launch_bounds__(32 * NW, 1) attn_tiles(PagesAttnArgs a) {
+    extern __shared__ __align__(16) uint8_t raw[];
+    using S = Shared<D, NT, NW>;
+    S &sh = *reinterpret_cast<S *>(raw);
+    const PagesView &p = a.p;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    // tiles before each row: a prefix over the rows, NW 32 at a time
+    long long base = 0;
+    for (int i0 = 0; i0 < a.r.n_rows; i0 += 32 * NW) {
+        const int i = i0 + tid;
+        long long w = 0;
+        if (i < a.r.n_rows) {
+            const PageRow r = page_row(p, a.r, i);
+            const int tiles = row_tiles(a, r.len);
+            sh.tiles[i] = tiles;
+            w = static_cast<long long>((r.n * p.G + 8 * NT - 1) / (8 * NT)) * p.Hkv * tiles;
+        }
+        long long s = w;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long t = __shfl_up_sync(FULL, s, o);
+            if (lane >= o) s += t;
+        }
+        if (lane == 31) sh.part[warp] = s;
+        __syncthreads();
+        long long before = base;
+        for (int k = 0; k < warp; k++) before += sh.part[k];
+        if (i < a.r.n_rows) sh.first[i] = before + s - w;
+        for (int k = 0; k < NW; k++) base += sh.part[k];
+        __syncthreads();
+    }
+    const long long N = base;
+    if (tid == 0) sh.first[a.r.n_rows] = N;
+    if (tid < 2 * NW) sh.unit[tid] = -1;
+    __syncthreads();
+    // this CTA's tiles [c0, c1), this warp's [w0, w1)
+    long long ctas = N / MIN_TILES;
+    ctas = ctas < 1 ? 1 : (ctas > gridDim.x ? gridDim.x : ctas);
+    if (blockIdx.x >= ctas) return;
+    const long long c0 = N * blockIdx.x / ctas, c1 = N * (blockIdx.x + 1) / ctas;
+    const long long w0 = c0 + (c1 - c0) * warp / NW, w1 = c0 + (c1 - c0) * (warp + 1) / NW;
+
+    const int per = p.P >> 4;  // tiles of a page, a power of two
+    const int shift = 31 - __clz(per);
+    State<D, NT> st;
+    for (long long x = w0; x < w1;) {
+        const Unit u = find_unit<D, NT, NW>(sh, a.r.n_rows, p.Hkv, x);
+        const PageRow r = page_row(p, a.r, u.i);
+        const int t0 = static_cast<int>(x - u.first);
+        const long long left = u.first + u.tiles - x;
+        const int t1 = t0 + static_cast<int>(left < w1 - x ? left : w1 - x);
+        st.load_q(a, r, u.head, u.row0);
+        st.reset();
+        // the rows' least and greatest position: tiles past the greatest are nobody's
+        const int rows = r.n * p.G;
+        const int end = u.row0 + 8 * NT < rows ? u.row0 + 8 * NT : rows;
+        const int least = r.len - r.n + u.row0 / p.G, most = r.len - r.n + (end - 1) / p.G;
+        // page numbers of 32 entries at a time, one a lane, the next 32 on their way
+        const int *sel = a.sel ? a.sel + (static_cast<long long>(u.i) * p.Hkv + u.head) * a.n_sel : nullptr;
+        auto entry = [&](int e, int &id, int &ord) {
+            id = -1;
+            ord = e;
+            if (r.row < 0) return;
+            if (sel) ord = e < a.n_sel ? sel[e] : -1;
+            if (ord < 0 || ord >= p.M || static_cast<long long>(ord) * p.P >= r.len) return;
+            id = page_of(p, r.row, ord);
+        };
+        int e0 = t0 >> shift, id0, ord0, id1, ord1;
+        entry(e0 + lane, id0, ord0);
+        entry(e0 + 32 + lane, id1, ord1);
+        auto fetch = [&](int t, Tile<D> &x_) {
+            x_.pos = -1;
+            if (t >= t1) return;
+            int e = t >> shift;
+            if (e >= e0 + 32) {
+                e0 += 32;
+                id0 = id1;
+                ord0 = ord1;
+                entry(e0 + 32 + lane, id1, ord1);
+            }
+            const int id = __shfl_sync(FULL, id0, e - e0), ord = __shfl_sync(FULL, ord0, e - e0);
+            const int off = (t & (per - 1)) << 4;
+            if (id < 0 || ord * p.P + off > most) return;
+            x_.pos = ord * p.P + off;
+            load_tile<D>(x_, page_ptr(p, id, u.head), off, p.blk);
+        };
+        Tile<D> ta, tb;
+        fetch(t0, ta);
+        fetch(t0 + 1, tb);
+        for (int t = t0; t < t1; t += 2) {
+            if (ta.pos >= 0) st.step(ta, r.len, least);
+            fetch(t + 2, ta);
+            if (tb.pos >= 0) st.step(tb, r.len, least);
+            fetch(t + 3, tb);
+        }
+        if (t0 == 0 && t1 == u.tiles) st.to_output(a, r, u.head, u.row0);
+        else {
+            st.to_record(sh.rec[warp][t0 == 0]);
+            if (lane == 0) sh.unit[2 * warp + (t0 == 0)] = u.first;
+        }
+        x += t1 - t0;
+    }
+    __syncthreads();
+
+    // The records that warps left, in order: a unit's are neighbours.  All warps add up one
+    // unit after the other; a unit that other CTAs share goes to the workspace.
+    if (tid == 0) {
+        int n = 0;
+        for (int k = 0; k < 2 * NW; k++)
+            if (sh.unit[k] >= 0) sh.list[n++] = k;
+        sh.n_list = n;
+    }
+    __syncthreads();
+    constexpr int REC = S::REC, TH = 32 * NW, ITEMS = 8 * NT * (D / 4);
+    for (int k0 = 0, k1; k0 < sh.n_list; k0 = k1) {
+        const long long first = sh.unit[sh.list[k0]];
+        for (k1 = k0 + 1; k1 < sh.n_list && sh.unit[sh.list[k1]] == first;) k1++;
+        const Unit u = find_unit<D, NT, NW>(sh, a.r.n_rows, p.Hkv, first);
+        const PageRow r = page_row(p, a.r, u.i);
+        const bool begins = u.first >= c0, ends = u.first + u.tiles <= c1;
+        auto part_of = [&](int k) -> const float * { return (&sh.rec[0][0][0]) + sh.list[k0 + k] * REC; };
+        if (begins && ends) {
+            for (int i = tid; i < ITEMS; i += TH) {
+                float acc[4], m, l;
+                const int row = i / (D / 4), c = i % (D / 4) * 4;
+                add_records<D, NT>(k1 - k0, row, c, part_of, acc, m, l);
+                write4<D>(a, r, u.head, u.row0 + row, c, acc, m, l);
+            }
+            continue;
+        }
+        // CTA c holds tiles [N c / ctas, N (c + 1) / ctas)
+        const int cf = static_cast<int>(((u.first + 1) * ctas - 1) / N);
+        const int cl = static_cast<int>(((u.first + u.tiles) * ctas - 1) / N);
+        float *mine = a.records + (2LL * blockIdx.x + begins) * REC;
+        for (int i = tid; i < ITEMS; i += TH) {
+            float acc[4], m, l;
+            const int row = i / (D / 4), c = i % (D / 4) * 4;
+            add_records<D, NT>(k1 - k0, row, c, part_of, acc, m, l);
+            *reinterpret_cast<float4 *>(mine + row * D + c) = make_float4(acc[0], acc[1], acc[2], acc[3]);
+            if (c == 0) {
+                mine[8 * NT * D + row] = m;
+                mine[8 * NT * (D + 1) + row] = l;
+            }
+        }
+        __threadfence();
+        __syncthreads();
+        if (tid == 0) {
+            sh.last = atomic_add_acq_rel_gpu(a.tickets + cf, 1) == cl - cf;
+            if (sh.last) a.tickets[cf] = 0;  // for the next call
+        }
+        __syncthreads();
+        if (sh.last) {
+            __threadfence();
+            auto cta_of = [&](int k) -> const float * { return a.records + (2LL * (cf + k) + (k == 0)) * REC; };
+            for (int i = tid; i < ITEMS; i += TH) {
+                float acc[4], m, l;
+                const int row = i / (D / 4), c = i % (D / 4) * 4;
+                add_records<D, NT>(cl - cf + 1, row, c, cta_of, acc, m, l);
+                write4<D>(a, r, u.head, u.row0 + row, c, acc, m, l);
+            }
+        }
+        __syncthreads();
+    }
+}
+
+template <int D, int NT, int NW>
+int launch_tiles(const PagesAttnArgs &a, int grid, cudaStream_t st) {
+    const int smem = static_cast<int>(sizeof(Shared<D, NT, NW>));
+    const cudaError_t e = cudaFuncSetAttribute(attn_tiles<D, NT, NW>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return static_cast<int>(e);
+    attn_tiles<D, NT, NW><<<grid, 32 * NW, smem, st>>>(a);
+    return static_cast<int>(cudaGetLastError());
 }
 
 }  // namespace
 
-int launch_pages_attention(const PagesAttnArgs &a, void *stream) {
-    const dim3 grid((a.r.max_new * a.p.G + AT_ROWS - 1) / AT_ROWS, a.r.n_rows, a.p.Hkv);
+int launch_pages_attention(const PagesAttnArgs &a, int num_sms, void *stream) {
     auto st = static_cast<cudaStream_t>(stream);
-    if (a.p.d == 128) attn_simple<128><<<grid, AT_THREADS, 0, st>>>(a);
-    else attn_simple<64><<<grid, AT_THREADS, 0, st>>>(a);
-    return static_cast<int>(cudaGetLastError());
+    const int grid = num_sms < PAGES_MAX_CTAS ? num_sms : PAGES_MAX_CTAS;
+    // 8 query rows fill one n tile; more share the conversions of two
+    if (a.r.max_new * a.p.G <= 8) return a.p.d == 128 ? launch_tiles<128, 1, 16>(a, grid, st) : launch_tiles<64, 1, 16>(a, grid, st);
+    return a.p.d == 128 ? launch_tiles<128, 2, 8>(a, grid, st) : launch_tiles<64, 2, 8>(a, grid, st);
 }
 
 }  // namespace dq

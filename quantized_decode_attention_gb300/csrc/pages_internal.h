@@ -42,6 +42,16 @@ struct PagesRows {
 // The int part of the workspace: [0] copies or moves of the last plan, [1] live pages
 // below which moves end, then three lists of n_pages.
 constexpr int PAGES_WS_HEAD = 16;
+// Behind it, attention: CTAs of a launch, and the floats of a record of 16 query rows
+// with head_dim 128 (accumulators, maximum and sum).
+constexpr int PAGES_MAX_CTAS = 256;
+constexpr int PAGES_REC_FLOATS = 16 * (128 + 2);
+inline size_t pages_ws_lists(int n_pages) {  // bytes of the lists, a multiple of 16
+    return (PAGES_WS_HEAD * 4 + 12 * static_cast<size_t>(n_pages) + 15) / 16 * 16;
+}
+inline size_t pages_ws_bytes(int n_pages) {
+    return pages_ws_lists(n_pages) + PAGES_MAX_CTAS * 4 + static_cast<size_t>(PAGES_MAX_CTAS) * 2 * PAGES_REC_FLOATS * 4;
+}
 
 struct PagesStoreArgs {
     PagesView p;
@@ -65,6 +75,8 @@ struct PagesAttnArgs {
     int n_sel;
     float scale_log2;     // sm_scale 2^k_exp log2(e)
     float out_scale;      // 2^v_exp
+    int *tickets;         // workspace: [PAGES_MAX_CTAS], 0 between calls
+    float *records;       // workspace: [PAGES_MAX_CTAS][2][PAGES_REC_FLOATS]
 };
 struct PagesSelectArgs {
     PagesView p;
@@ -81,7 +93,7 @@ int launch_pages_fork(const PagesView &p, const int *src, const int *dst, int n,
 int launch_pages_compact(const PagesView &p, int *ws, int num_sms, void *stream);
 int launch_pages_append(const PagesStoreArgs &a, void *stream);
 int launch_pages_read(const PagesReadArgs &a, void *stream);
-int launch_pages_attention(const PagesAttnArgs &a, void *stream);
+int launch_pages_attention(const PagesAttnArgs &a, int num_sms, void *stream);
 int launch_pages_select(const PagesSelectArgs &a, void *stream);
 
 }  // namespace dq
