@@ -5,17 +5,18 @@
 // in one pass over the pages.
 //
 // Work.  A unit is 8 NT query rows (token, query head of the group) of one row and KV
-// head; it walks the row's tokens in tiles of 16 (a tile lies in one page whatever the
-// page size).  All units' tiles, in order, are cut into equal shares, one for each warp
-// of one CTA per SM, so that ragged lengths and small batches fill the card alike.  A
-// warp that holds all of a unit writes its output; parts of a unit meet in shared
-// memory, and parts in several CTAs in the workspace, where the last CTA to arrive
-// adds them up in CTA order (so that the result does not depend on timing; nobody waits).
+// head; it walks the row's tokens in chunks of 32.  All units' chunks, in order, are cut
+// into equal shares, one for each warp of one CTA per SM, so that ragged lengths and
+// small batches fill the card alike.  A warp that holds all of a unit writes its output;
+// parts of a unit meet in shared memory, and parts in several CTAs in the workspace,
+// where the last CTA to arrive adds them up in CTA order (so that the result does not
+// depend on timing; nobody waits).
 //
-// A tile.  Codes and scales come straight to registers, 16 bytes a lane, two tiles ahead
-// of their use: with 16 warps that keeps some 55 KB in flight per SM, which is what
-// HBM's latency asks for, without shared memory or barriers.  The page layout is made
-// for it: a lane's 16 bytes are its own operands.  Codes become binary16 by one
+// A chunk.  Each warp has a ring of its own in shared memory, filled by bulk copies (four
+// a chunk: codes and scales of keys and of values; eight where a page is 16 tokens) that
+// run ahead of it, so that no warp waits for another and 16 warps x 1.5 chunks keep
+// 110 KB in flight per SM.  The page layout is made for the product: a lane's 16 bytes
+// are its own operands, without bank conflicts.  Codes become binary16 by one
 // conversion and one multiplication by the scale, both exact (2 + 4 significant bits,
 // multiples of 2^-10 below 2^12).  Both products run on mma.sync m16n8k16 with
 // the cache as the 16-row operand: K [16 tokens x 16 channels] . Q^T and
@@ -36,50 +37,25 @@ namespace dq {
 namespace {
 
 constexpr float LN2 = 0.69314718055994530942f;
+constexpr uint64_t WAIT_NS = 2000000000ull;  // longest wait for a copy
 constexpr float SLACK = 8.f, LIFT = 7.f;   // log2 units
-constexpr int MIN_TILES = 32;              // tiles that make a CTA worth its merge
+constexpr int CHUNK = 32;                  // tokens
+constexpr int MIN_CHUNKS = 16;             // chunks that make a CTA worth its merge
 
-// ---- one tile in registers ---------------------------------------------------------------
-template <int D>
-struct Tile {
-    uint32_t k[2][D / 32], v[2][D / 32];  // tokens g, g + 8; pairs t, t + 4
-    uint32_t ks[2], vs[2];
-    int pos;                              // position of the first token, -1: nothing to do
-};
-
+// ---- a chunk in shared memory: a block of 32 tokens in the page's own layout ---------------
 template <int N>
 __device__ __forceinline__ void ld_words(const uint8_t *p, uint32_t (&w)[N]) {
     if (N == 4) {
-        asm("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];\n" : "=r"(w[0]), "=r"(w[1]), "=r"(w[N > 2 ? 2 : 0]), "=r"(w[N > 3 ? 3 : 0]) : "l"(p));
+        const uint4 v = *reinterpret_cast<const uint4 *>(p);
+        w[0] = v.x;
+        w[1] = v.y;
+        w[N > 2 ? 2 : 0] = v.z;
+        w[N > 3 ? 3 : 0] = v.w;
     } else {
-        asm("ld.global.nc.L1::no_allocate.v2.u32 {%0,%1}, [%2];\n" : "=r"(w[0]), "=r"(w[1]) : "l"(p));
+        const uint2 v = *reinterpret_cast<const uint2 *>(p);
+        w[0] = v.x;
+        w[1] = v.y;
     }
-}
-
-// Tile at token `off` of a page (a multiple of 16).
-template <int D>
-__device__ __forceinline__ void load_tile(Tile<D> &x, const uint8_t *page, int off, int b) {
-    using B = PageBlock<D>;
-    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    const uint8_t *blk = page + (off / b) * B::size(b);
-    const int o = off % b;
-    const uint8_t *kc = blk + (o + g) * (D / 2) + t * (D / 8);
-    ld_words(kc, x.k[0]);
-    ld_words(kc + 4 * D, x.k[1]);
-    const uint8_t *vc = blk + B::vc(b) + o * (D / 2) + ((D == 128 ? g : g >> 1) * 4 + t) * 16 + (D == 128 ? 0 : (g & 1) * 8);
-    ld_words(vc, x.v[0]);
-    ld_words(vc + 4 * D, x.v[1]);
-    const uint8_t *ks = blk + B::ks(b) + (o + g) * (D / 16) + t * (D / 64);
-    const uint8_t *vs = blk + B::vs(b) + o * (D / 16) + ((D == 128 ? g : g >> 1) * 4 + t) * 2;
-    if (D == 128) {
-        x.ks[0] = *reinterpret_cast<const uint16_t *>(ks);
-        x.ks[1] = *reinterpret_cast<const uint16_t *>(ks + D / 2);
-    } else {
-        x.ks[0] = *ks;
-        x.ks[1] = *(ks + D / 2);
-    }
-    x.vs[0] = *reinterpret_cast<const uint16_t *>(vs);
-    x.vs[1] = *reinterpret_cast<const uint16_t *>(vs + D / 2);
 }
 
 __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
@@ -106,6 +82,9 @@ struct State {
     int pos[NT][2];            // positions of the rows
     float m[NT][2], l[NT][2];  // m the same in every lane of a row; l this lane's part
     float acc[NT][D / 16][4];  // [channel g D/8 + 2 mi (+ 1: 2, 3)][row 2t (+ 1: 1, 3)]
+
+    // what a logit loses before the exponential
+    __device__ __forceinline__ float mu(int n, int e) const { return m[n][e] == -INFINITY ? 0.f : m[n][e] - LIFT; }
 
     __device__ __forceinline__ void reset() {
 #pragma unroll
@@ -166,58 +145,83 @@ struct State {
         }
     }
 
-    __device__ __forceinline__ void step(const Tile<D> &x, int len, int least) {
+    // One chunk at `c`: tokens at positions pa .. pa + 15 and pb .. pb + 15 (negative: not there).
+    __device__ __forceinline__ void step(const uint8_t *c, int pa, int pb, int len, int least) {
+        using B = PageBlock<D>;
         const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-        float s[NT][4];
-#pragma unroll
-        for (int n = 0; n < NT; n++) s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.f;
-        uint32_t sc[2][2];  // key scales of tokens g, g + 8: both halves of a register each
-#pragma unroll
-        for (int h = 0; h < 2; h++) {
-            const uint32_t two = e4m3x2_to_half2(static_cast<uint16_t>(x.ks[h]));
-            sc[h][0] = __byte_perm(two, two, 0x1010);
-            sc[h][1] = D == 128 ? __byte_perm(two, two, 0x3232) : sc[h][0];
-        }
-#pragma unroll
-        for (int w = 0; w < D / 32; w++) {
-            uint32_t a[4], b[4];
-            e2m1x8_to_half(x.k[0][w], a);
-            e2m1x8_to_half(x.k[1][w], b);
-#pragma unroll
-            for (int i = 0; i < 4; i++) {
-                a[i] = hmul2(a[i], sc[0][w >> 1]);
-                b[i] = hmul2(b[i], sc[1][w >> 1]);
-            }
-#pragma unroll
-            for (int n = 0; n < NT; n++) {
-                mma_f16(s[n], a[0], b[0], a[1], b[1], q[n][2 * w][0], q[n][2 * w][1]);
-                mma_f16(s[n], a[2], b[2], a[3], b[3], q[n][2 * w + 1][0], q[n][2 * w + 1][1]);
-            }
-        }
-        // s: tokens g (0, 1) and g + 8 (2, 3), rows 2t (0, 2) and 2t + 1 (1, 3)
-        const bool tail = x.pos + 15 > least;  // a token that some row does not see
-        bool grow = false;
+        float s[NT][8];  // tokens g, g + 8, g + 16, g + 24, rows 2t and 2t + 1 of each
 #pragma unroll
         for (int n = 0; n < NT; n++)
 #pragma unroll
-            for (int i = 0; i < 4; i++) {
-                float z = s[n][i] * f[n][i & 1];
-                if (tail && x.pos + g + 8 * (i >> 1) > pos[n][i & 1]) z = -INFINITY;
-                s[n][i] = z;
-                grow |= z > m[n][i & 1] + SLACK;  // also the first finite logit
+            for (int i = 0; i < 8; i++) s[n][i] = 0.f;
+        const uint8_t *kc = c + g * (D / 2) + t * (D / 8), *ks = c + B::ks(CHUNK) + g * (D / 16) + t * (D / 64);
+#pragma unroll
+        for (int h = 0; h < 2; h++) {
+            uint32_t ka[D / 32], kb[D / 32], sa[2], sb[2];
+            ld_words(kc + h * 16 * (D / 2), ka);
+            ld_words(kc + (h * 16 + 8) * (D / 2), kb);
+            // scales of tokens g, g + 8: both halves of a register each
+            const uint8_t *s0 = ks + h * D, *s1 = s0 + D / 2;
+            const uint32_t two0 = e4m3x2_to_half2(D == 128 ? *reinterpret_cast<const uint16_t *>(s0) : *s0);
+            const uint32_t two1 = e4m3x2_to_half2(D == 128 ? *reinterpret_cast<const uint16_t *>(s1) : *s1);
+            sa[0] = __byte_perm(two0, two0, 0x1010);
+            sb[0] = __byte_perm(two1, two1, 0x1010);
+            sa[1] = D == 128 ? __byte_perm(two0, two0, 0x3232) : sa[0];
+            sb[1] = D == 128 ? __byte_perm(two1, two1, 0x3232) : sb[0];
+#pragma unroll
+            for (int w = 0; w < D / 32; w++) {
+                uint32_t a[4], b[4];
+                e2m1x8_to_half(ka[w], a);
+                e2m1x8_to_half(kb[w], b);
+#pragma unroll
+                for (int i = 0; i < 4; i++) {
+                    a[i] = hmul2(a[i], sa[w >> 1]);
+                    b[i] = hmul2(b[i], sb[w >> 1]);
+                }
+#pragma unroll
+                for (int n = 0; n < NT; n++) {
+                    float(&d)[4] = *reinterpret_cast<float(*)[4]>(&s[n][4 * h]);
+                    mma_f16(d, a[0], b[0], a[1], b[1], q[n][2 * w][0], q[n][2 * w][1]);
+                    mma_f16(d, a[2], b[2], a[3], b[3], q[n][2 * w + 1][0], q[n][2 * w + 1][1]);
+                }
             }
+        }
+        // exponents z - m + LIFT
+        bool grow = false;
+        const bool tail = pa < 0 || pb < 0 || pa + 15 > least || pb + 15 > least;  // a token that some row does not see
+#pragma unroll
+        for (int n = 0; n < NT; n++) {
+#pragma unroll
+            for (int i = 0; i < 8; i++) s[n][i] = fmaf(s[n][i], f[n][i & 1], -mu(n, i & 1));
+            if (tail) {
+#pragma unroll
+                for (int i = 0; i < 8; i++) {
+                    const int at = i < 4 ? pa : pb;
+                    if (at < 0 || at + g + 8 * ((i >> 1) & 1) > pos[n][i & 1]) s[n][i] = -INFINITY;
+                }
+            }
+#pragma unroll
+            for (int e = 0; e < 2; e++) {
+                const float top = fmaxf(fmaxf(s[n][e], s[n][e + 2]), fmaxf(s[n][e + 4], s[n][e + 6]));
+                grow |= top > (m[n][e] == -INFINITY ? -INFINITY : SLACK + LIFT);  // also the first finite logit
+            }
+        }
         if (__any_sync(FULL, grow)) {
 #pragma unroll
             for (int n = 0; n < NT; n++)
 #pragma unroll
                 for (int e = 0; e < 2; e++) {
-                    float top = fmaxf(s[n][e], s[n][e + 2]);
+                    float top = fmaxf(fmaxf(s[n][e], s[n][e + 2]), fmaxf(s[n][e + 4], s[n][e + 6]));
                     top = fmaxf(top, __shfl_xor_sync(FULL, top, 4));
                     top = fmaxf(top, __shfl_xor_sync(FULL, top, 8));
                     top = fmaxf(top, __shfl_xor_sync(FULL, top, 16));
-                    top = fmaxf(top, m[n][e]);
-                    const float al = top == -INFINITY ? 1.f : ex2(m[n][e] - top);
-                    m[n][e] = top;
+                    const float old = mu(n, e);
+                    const float mx = fmaxf(top + old, m[n][e]);  // top is z - old
+                    const float al = mx == -INFINITY ? 1.f : ex2(m[n][e] - mx);
+                    m[n][e] = mx;
+                    const float by = old - mu(n, e);
+#pragma unroll
+                    for (int i = e; i < 8; i += 2) s[n][i] += by;
                     l[n][e] *= al;
 #pragma unroll
                     for (int i = 0; i < D / 16; i++) {
@@ -226,37 +230,46 @@ struct State {
                     }
                 }
         }
-        uint32_t p[NT][2];
+        uint32_t p[NT][4];
 #pragma unroll
         for (int n = 0; n < NT; n++) {
 #pragma unroll
-            for (int i = 0; i < 4; i++) {
-                const float mu = m[n][i & 1] == -INFINITY ? 0.f : m[n][i & 1] - LIFT;
-                s[n][i] = ex2(s[n][i] - mu);
-                l[n][i & 1] += s[n][i];
-            }
-            p[n][0] = transpose8(half2_of(s[n][0], s[n][1]));
-            p[n][1] = transpose8(half2_of(s[n][2], s[n][3]));
-        }
-        uint32_t v0 = e4m3x2_to_half2(static_cast<uint16_t>(x.vs[0])), v1 = e4m3x2_to_half2(static_cast<uint16_t>(x.vs[1]));
-        if (x.pos + 15 >= len) {  // tokens that are not there may hold anything, NaN scales too: 0 . NaN must not count
-            v0 &= (x.pos + 2 * t < len ? 0x0000ffffu : 0u) | (x.pos + 2 * t + 1 < len ? 0xffff0000u : 0u);
-            v1 &= (x.pos + 2 * t + 8 < len ? 0x0000ffffu : 0u) | (x.pos + 2 * t + 9 < len ? 0xffff0000u : 0u);
-        }
+            for (int i = 0; i < 8; i++) s[n][i] = ex2(s[n][i]);
+            l[n][0] += (s[n][0] + s[n][2]) + (s[n][4] + s[n][6]);
+            l[n][1] += (s[n][1] + s[n][3]) + (s[n][5] + s[n][7]);
 #pragma unroll
-        for (int w = 0; w < D / 32; w++) {
-            uint32_t a[4], b[4];
-            e2m1x8_to_half(x.v[0][w], a);
-            e2m1x8_to_half(x.v[1][w], b);
+            for (int i = 0; i < 4; i++) p[n][i] = transpose8(half2_of(s[n][2 * i], s[n][2 * i + 1]));
+        }
+        const uint8_t *vc = c + B::vc(CHUNK) + ((D == 128 ? g : g >> 1) * 4 + t) * 16 + (D == 128 ? 0 : (g & 1) * 8);
+        const uint8_t *vs = c + B::vs(CHUNK) + ((D == 128 ? g : g >> 1) * 4 + t) * 2;
 #pragma unroll
-            for (int i = 0; i < 4; i++) {
-                a[i] = hmul2(a[i], v0);
-                b[i] = hmul2(b[i], v1);
+        for (int h = 0; h < 2; h++) {
+            uint32_t va[D / 32], vb[D / 32];
+            ld_words(vc + (2 * h) * 4 * D, va);
+            ld_words(vc + (2 * h + 1) * 4 * D, vb);
+            uint32_t v0 = e4m3x2_to_half2(*reinterpret_cast<const uint16_t *>(vs + (2 * h) * (D / 2)));
+            uint32_t v1 = e4m3x2_to_half2(*reinterpret_cast<const uint16_t *>(vs + (2 * h + 1) * (D / 2)));
+            if (tail) {  // tokens that are not there may hold anything, NaN scales too: 0 . NaN must not count
+                const int at = h ? pb : pa;
+                const int n = at < 0 ? 0 : len - at;
+                v0 &= (2 * t < n ? 0x0000ffffu : 0u) | (2 * t + 1 < n ? 0xffff0000u : 0u);
+                v1 &= (2 * t + 8 < n ? 0x0000ffffu : 0u) | (2 * t + 9 < n ? 0xffff0000u : 0u);
             }
 #pragma unroll
-            for (int n = 0; n < NT; n++) {
-                mma_f16(acc[n][2 * w], a[0], a[1], b[0], b[1], p[n][0], p[n][1]);
-                mma_f16(acc[n][2 * w + 1], a[2], a[3], b[2], b[3], p[n][0], p[n][1]);
+            for (int w = 0; w < D / 32; w++) {
+                uint32_t a[4], b[4];
+                e2m1x8_to_half(va[w], a);
+                e2m1x8_to_half(vb[w], b);
+#pragma unroll
+                for (int i = 0; i < 4; i++) {
+                    a[i] = hmul2(a[i], v0);
+                    b[i] = hmul2(b[i], v1);
+                }
+#pragma unroll
+                for (int n = 0; n < NT; n++) {
+                    mma_f16(acc[n][2 * w], a[0], a[1], b[0], b[1], p[n][2 * h], p[n][2 * h + 1]);
+                    mma_f16(acc[n][2 * w + 1], a[2], a[3], b[2], b[3], p[n][2 * h], p[n][2 * h + 1]);
+                }
             }
         }
     }
@@ -318,7 +331,7 @@ struct State {
 };
 
 // ---- the call's units --------------------------------------------------------------------
-// Unit `unit` of row i (head-major, query blocks within), its first tile and tile count.
+// A unit of row i (head-major, query blocks within), its first chunk and their number.
 struct Unit {
     int i, head, row0;
     long long first;
@@ -327,26 +340,34 @@ struct Unit {
 
 template <int D, int NT, int NW>
 struct Shared {
-    static constexpr int REC = 8 * NT * (D + 2);  // floats of a record
-    float rec[NW][2][REC];  // each warp's parts: of a unit begun before it, of one that goes on after it
-    long long first[DQ_PAGES_MAX_ROWS + 1];  // tiles before row i
-    int tiles[DQ_PAGES_MAX_ROWS];            // of each of the row's units
+    static constexpr int REC = 8 * NT * (D + 2);   // floats of a record
+    static constexpr int ST = 32 / NW;             // chunks of a warp's ring
+    static constexpr int CB = CHUNK * D * 9 / 8;   // bytes of a chunk
+    // each warp's ring, and its part of a unit begun before it; its part of a unit that
+    // goes on after it takes the ring's place, which is done by then
+    __align__(128) uint8_t ring[NW][ST][CB];
+    __align__(16) float rec[NW][REC];
+    uint64_t full[NW][ST];
+    int2 pos[NW][ST];                              // positions of a chunk's two halves
+    long long first[DQ_PAGES_MAX_ROWS + 1];        // chunks before row i
+    int tiles[DQ_PAGES_MAX_ROWS];                  // chunks of each of the row's units
     long long part[NW];
-    long long unit[2 * NW];  // first tile of the unit that each record is a part of, -1: none
+    long long unit[2 * NW];                        // first chunk of the unit that each record is a part of, -1: none
     int list[2 * NW], n_list, last;
+    __device__ float *record(int k) { return k & 1 ? reinterpret_cast<float *>(ring[k >> 1]) : rec[k >> 1]; }
 };
 
 __device__ __forceinline__ int row_tiles(const PagesAttnArgs &a, int len) {
-    // every unit has a tile, so that queries that see nothing get their zeros
-    const int n = a.sel ? (len > 0 ? a.n_sel * (a.p.P >> 4) : 0) : (len + 15) >> 4;
+    // every unit has a chunk, so that queries that see nothing get their zeros
+    const int n = a.sel ? (len > 0 ? (a.n_sel * a.p.P + CHUNK - 1) / CHUNK : 0) : (len + CHUNK - 1) / CHUNK;
     return n > 1 ? n : 1;
 }
 
-// The unit that holds tile x.
+// The unit that holds chunk x.
 template <int D, int NT, int NW>
 __device__ __forceinline__ Unit find_unit(const Shared<D, NT, NW> &sh, int n_rows, int Hkv, long long x) {
     int lo = 0, hi = n_rows - 1;
-    while (lo < hi) {  // the last row whose first tile is <= x (rows without tiles share it with the next)
+    while (lo < hi) {  // the last row whose first chunk is <= x (rows without any share it with the next)
         const int mid = (lo + hi + 1) >> 1;
         if (sh.first[mid] <= x) lo = mid;
         else hi = mid - 1;
@@ -395,12 +416,12 @@ __device__ __forceinline__ void write4(const PagesAttnArgs &a, const PageRow &r,
 
 template <int D, int NT, int NW>
 __global__ void __launch_bounds__(32 * NW, 1) attn_tiles(PagesAttnArgs a) {
-    extern __shared__ __align__(16) uint8_t raw[];
+    extern __shared__ __align__(128) uint8_t raw[];
     using S = Shared<D, NT, NW>;
     S &sh = *reinterpret_cast<S *>(raw);
     const PagesView &p = a.p;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    // tiles before each row: a prefix over the rows, NW 32 at a time
+    // chunks before each row: a prefix over the rows, NW 32 at a time
     long long base = 0;
     for (int i0 = 0; i0 < a.r.n_rows; i0 += 32 * NW) {
         const int i = i0 + tid;
@@ -429,69 +450,105 @@ __global__ void __launch_bounds__(32 * NW, 1) attn_tiles(PagesAttnArgs a) {
     if (tid == 0) sh.first[a.r.n_rows] = N;
     if (tid < 2 * NW) sh.unit[tid] = -1;
     __syncthreads();
-    // this CTA's tiles [c0, c1), this warp's [w0, w1)
-    long long ctas = N / MIN_TILES;
+    // this CTA's chunks [c0, c1), this warp's [w0, w1)
+    long long ctas = N / MIN_CHUNKS;
     ctas = ctas < 1 ? 1 : (ctas > gridDim.x ? gridDim.x : ctas);
     if (blockIdx.x >= ctas) return;
     const long long c0 = N * blockIdx.x / ctas, c1 = N * (blockIdx.x + 1) / ctas;
     const long long w0 = c0 + (c1 - c0) * warp / NW, w1 = c0 + (c1 - c0) * (warp + 1) / NW;
 
-    const int per = p.P >> 4;  // tiles of a page, a power of two
-    const int shift = 31 - __clz(per);
+    // chunks of a page, a power of two (2 pages make a chunk where a page is 16 tokens)
+    const int shift = p.P > CHUNK ? 31 - __clz(p.P / CHUNK) : 0;
     State<D, NT> st;
+    constexpr int ST = S::ST;
+    unsigned sent = 0, done = 0;  // chunks of this warp's ring
+    if (lane < ST) mbar_init(&sh.full[warp][lane], 1);
+    fence_mbar_init();
+    __syncwarp();
     for (long long x = w0; x < w1;) {
         const Unit u = find_unit<D, NT, NW>(sh, a.r.n_rows, p.Hkv, x);
         const PageRow r = page_row(p, a.r, u.i);
         const int t0 = static_cast<int>(x - u.first);
         const long long left = u.first + u.tiles - x;
         const int t1 = t0 + static_cast<int>(left < w1 - x ? left : w1 - x);
-        st.load_q(a, r, u.head, u.row0);
-        st.reset();
-        // the rows' least and greatest position: tiles past the greatest are nobody's
+        // the rows' least and greatest position: tokens past the greatest are nobody's
         const int rows = r.n * p.G;
         const int end = u.row0 + 8 * NT < rows ? u.row0 + 8 * NT : rows;
         const int least = r.len - r.n + u.row0 / p.G, most = r.len - r.n + (end - 1) / p.G;
         // page numbers of 32 entries at a time, one a lane, the next 32 on their way
         const int *sel = a.sel ? a.sel + (static_cast<long long>(u.i) * p.Hkv + u.head) * a.n_sel : nullptr;
-        auto entry = [&](int e, int &id, int &ord) {
+        auto entry = [&](int e, int &id, int &at) {  // at: position of the page's first token
             id = -1;
-            ord = e;
-            if (r.row < 0) return;
+            int ord = e;
             if (sel) ord = e < a.n_sel ? sel[e] : -1;
-            if (ord < 0 || ord >= p.M || static_cast<long long>(ord) * p.P >= r.len) return;
+            if (r.row < 0 || ord < 0 || ord >= p.M || ord * p.P >= r.len) return;
+            at = ord * p.P;
             id = page_of(p, r.row, ord);
         };
-        int e0 = t0 >> shift, id0, ord0, id1, ord1;
-        entry(e0 + lane, id0, ord0);
-        entry(e0 + 32 + lane, id1, ord1);
-        auto fetch = [&](int t, Tile<D> &x_) {
-            x_.pos = -1;
-            if (t >= t1) return;
-            int e = t >> shift;
-            if (e >= e0 + 32) {
-                e0 += 32;
-                id0 = id1;
-                ord0 = ord1;
-                entry(e0 + 32 + lane, id1, ord1);
+        const bool two = p.P < CHUNK;
+        int e0 = two ? 2 * t0 : t0 >> shift, id0, at0 = 0, id1, at1 = 0;
+        entry(e0 + lane, id0, at0);
+        entry(e0 + 32 + lane, id1, at1);
+        int next = t0;
+        // copy the next chunk that holds something into the ring
+        auto send = [&]() {
+            while (next < t1) {
+                const int c = next++, e = two ? 2 * c : c >> shift;
+                if (e >= e0 + 32) {
+                    e0 += 32;
+                    id0 = id1;
+                    at0 = at1;
+                    entry(e0 + 32 + lane, id1, at1);
+                }
+                const int half = two ? lane >> 2 & 1 : 0;  // lanes 4 .. 7 copy the second page
+                const int off = two ? 0 : (c & ((1 << shift) - 1)) * CHUNK;
+                const int ida = __shfl_sync(FULL, id0, e - e0), idb = __shfl_sync(FULL, id0, e - e0 + two);
+                const int ata = __shfl_sync(FULL, at0, e - e0), atb = __shfl_sync(FULL, at0, e - e0 + two);
+                int pa = ida < 0 ? -1 : ata + off, pb = idb < 0 ? -1 : atb + (two ? 0 : off + 16);
+                if (pa > most) pa = -1;
+                if (pb > most) pb = -1;
+                if (pa < 0 && pb < 0) continue;
+                const int k = sent % ST;
+                constexpr int HB = 16 * D * 9 / 8;
+                if (lane == 0) {
+                    sh.pos[warp][k] = make_int2(pa, pb);
+                    mbar_expect_tx(&sh.full[warp][k], two ? (pa < 0 ? 0 : HB) + (pb < 0 ? 0 : HB) : 2 * HB);
+                }
+                __syncwarp();
+                if (lane < (two ? 8 : 4) && (!two || (half ? pb : pa) >= 0)) {
+                    using B = PageBlock<D>;
+                    const int b = p.blk, n = two ? 16 : CHUNK, part = lane & 3;
+                    const uint8_t *src = page_ptr(p, half ? idb : ida, u.head) + off / b * B::size(b);
+                    const int line = part & 1 ? D / 16 : D / 2;  // bytes of a token
+                    const int from = part == 0 ? 0 : (part == 1 ? B::ks(b) : (part == 2 ? B::vc(b) : B::vs(b)));
+                    const int to = part == 0 ? 0 : (part == 1 ? B::ks(CHUNK) : (part == 2 ? B::vc(CHUNK) : B::vs(CHUNK)));
+                    bulk_g2s(sh.ring[warp][k] + to + half * 16 * line, src + from + off % b * line, n * line, &sh.full[warp][k]);
+                }
+                sent++;
+                return;
             }
-            const int id = __shfl_sync(FULL, id0, e - e0), ord = __shfl_sync(FULL, ord0, e - e0);
-            const int off = (t & (per - 1)) << 4;
-            if (id < 0 || ord * p.P + off > most) return;
-            x_.pos = ord * p.P + off;
-            load_tile<D>(x_, page_ptr(p, id, u.head), off, p.blk);
         };
-        Tile<D> ta, tb;
-        fetch(t0, ta);
-        fetch(t0 + 1, tb);
-        for (int t = t0; t < t1; t += 2) {
-            if (ta.pos >= 0) st.step(ta, r.len, least);
-            fetch(t + 2, ta);
-            if (tb.pos >= 0) st.step(tb, r.len, least);
-            fetch(t + 3, tb);
+#pragma unroll
+        for (int k = 0; k < ST; k++) send();
+        st.load_q(a, r, u.head, u.row0);
+        st.reset();
+        while (done != sent) {
+            const int k = done % ST;
+            if (!mbar_wait(&sh.full[warp][k], done / ST & 1, WAIT_NS)) {
+                if (lane == 0) atomicOr(p.status, PST_TIMEOUT);
+                break;  // (mbar_wait had its limit: what is in flight had it too)
+            }
+            const int2 at = sh.pos[warp][k];
+            st.step(sh.ring[warp][k], at.x, at.y, r.len, least);
+            done++;
+            __syncwarp();
+            send();
         }
+        if (done != sent) break;
         if (t0 == 0 && t1 == u.tiles) st.to_output(a, r, u.head, u.row0);
         else {
-            st.to_record(sh.rec[warp][t0 == 0]);
+            __syncwarp();
+            st.to_record(sh.record(2 * warp + (t0 == 0)));
             if (lane == 0) sh.unit[2 * warp + (t0 == 0)] = u.first;
         }
         x += t1 - t0;
@@ -514,7 +571,7 @@ __global__ void __launch_bounds__(32 * NW, 1) attn_tiles(PagesAttnArgs a) {
         const Unit u = find_unit<D, NT, NW>(sh, a.r.n_rows, p.Hkv, first);
         const PageRow r = page_row(p, a.r, u.i);
         const bool begins = u.first >= c0, ends = u.first + u.tiles <= c1;
-        auto part_of = [&](int k) -> const float * { return (&sh.rec[0][0][0]) + sh.list[k0 + k] * REC; };
+        auto part_of = [&](int k) -> const float * { return sh.record(sh.list[k0 + k]); };
         if (begins && ends) {
             for (int i = tid; i < ITEMS; i += TH) {
                 float acc[4], m, l;
@@ -524,7 +581,7 @@ __global__ void __launch_bounds__(32 * NW, 1) attn_tiles(PagesAttnArgs a) {
             }
             continue;
         }
-        // CTA c holds tiles [N c / ctas, N (c + 1) / ctas)
+        // CTA c holds chunks [N c / ctas, N (c + 1) / ctas)
         const int cf = static_cast<int>(((u.first + 1) * ctas - 1) / N);
         const int cl = static_cast<int>(((u.first + u.tiles) * ctas - 1) / N);
         float *mine = a.records + (2LL * blockIdx.x + begins) * REC;
