@@ -42,6 +42,14 @@ constexpr float SLACK = 8.f, LIFT = 7.f;   // log2 units
 constexpr int CHUNK = 32;                  // tokens
 constexpr int MIN_CHUNKS = 16;             // chunks that make a CTA worth its merge
 
+__device__ __forceinline__ void mbar_expect(uint32_t bar, unsigned bytes) {
+    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n" ::"r"(bar), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void bulk_copy(uint32_t dst, const void *src, unsigned bytes, uint32_t bar) {
+    asm volatile("cp.async.bulk.shared::cta.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];\n" ::"r"(dst), "l"(src), "r"(bytes), "r"(bar)
+                 : "memory");
+}
+
 // ---- a chunk in shared memory: a block of 32 tokens in the page's own layout ---------------
 template <int N>
 __device__ __forceinline__ void ld_words(const uint8_t *p, uint32_t (&w)[N]) {
@@ -335,7 +343,7 @@ struct State {
 struct Unit {
     int i, head, row0;
     long long first;
-    int tiles;
+    int chunks;
 };
 
 template <int D, int NT, int NW>
@@ -350,14 +358,14 @@ struct Shared {
     uint64_t full[NW][ST];
     int2 pos[NW][ST];                              // positions of a chunk's two halves
     long long first[DQ_PAGES_MAX_ROWS + 1];        // chunks before row i
-    int tiles[DQ_PAGES_MAX_ROWS];                  // chunks of each of the row's units
+    int chunks[DQ_PAGES_MAX_ROWS];                  // chunks of each of the row's units
     long long part[NW];
     long long unit[2 * NW];                        // first chunk of the unit that each record is a part of, -1: none
     int list[2 * NW], n_list, last;
     __device__ float *record(int k) { return k & 1 ? reinterpret_cast<float *>(ring[k >> 1]) : rec[k >> 1]; }
 };
 
-__device__ __forceinline__ int row_tiles(const PagesAttnArgs &a, int len) {
+__device__ __forceinline__ int row_chunks(const PagesAttnArgs &a, int len) {
     // every unit has a chunk, so that queries that see nothing get their zeros
     const int n = a.sel ? (len > 0 ? (a.n_sel * a.p.P + CHUNK - 1) / CHUNK : 0) : (len + CHUNK - 1) / CHUNK;
     return n > 1 ? n : 1;
@@ -374,11 +382,11 @@ __device__ __forceinline__ Unit find_unit(const Shared<D, NT, NW> &sh, int n_row
     }
     Unit u;
     u.i = lo;
-    u.tiles = sh.tiles[lo];
+    u.chunks = sh.chunks[lo];
     const long long in = x - sh.first[lo];
-    const int unit = static_cast<int>(in / u.tiles);
-    u.first = sh.first[lo] + static_cast<long long>(unit) * u.tiles;
-    const int blocks = static_cast<int>((sh.first[lo + 1] - sh.first[lo]) / (static_cast<long long>(u.tiles) * Hkv));
+    const int unit = static_cast<int>(in / u.chunks);
+    u.first = sh.first[lo] + static_cast<long long>(unit) * u.chunks;
+    const int blocks = static_cast<int>((sh.first[lo + 1] - sh.first[lo]) / (static_cast<long long>(u.chunks) * Hkv));
     u.head = unit / blocks;
     u.row0 = (unit % blocks) * 8 * NT;
     return u;
@@ -414,8 +422,8 @@ __device__ __forceinline__ void write4(const PagesAttnArgs &a, const PageRow &r,
     if (a.lse && c == 0) a.lse[o] = l == 0.f ? -INFINITY : (m - LIFT + log2f(l)) * LN2;
 }
 
-template <int D, int NT, int NW>
-__global__ void __launch_bounds__(32 * NW, 1) attn_tiles(PagesAttnArgs a) {
+template <int D, int NT, int NW, bool TWO>
+__global__ void __launch_bounds__(32 * NW, 1) attn_chunks(PagesAttnArgs a) {
     extern __shared__ __align__(128) uint8_t raw[];
     using S = Shared<D, NT, NW>;
     S &sh = *reinterpret_cast<S *>(raw);
@@ -428,9 +436,9 @@ __global__ void __launch_bounds__(32 * NW, 1) attn_tiles(PagesAttnArgs a) {
         long long w = 0;
         if (i < a.r.n_rows) {
             const PageRow r = page_row(p, a.r, i);
-            const int tiles = row_tiles(a, r.len);
-            sh.tiles[i] = tiles;
-            w = static_cast<long long>((r.n * p.G + 8 * NT - 1) / (8 * NT)) * p.Hkv * tiles;
+            const int chunks = row_chunks(a, r.len);
+            sh.chunks[i] = chunks;
+            w = static_cast<long long>((r.n * p.G + 8 * NT - 1) / (8 * NT)) * p.Hkv * chunks;
         }
         long long s = w;
 #pragma unroll
@@ -457,8 +465,18 @@ __global__ void __launch_bounds__(32 * NW, 1) attn_tiles(PagesAttnArgs a) {
     const long long c0 = N * blockIdx.x / ctas, c1 = N * (blockIdx.x + 1) / ctas;
     const long long w0 = c0 + (c1 - c0) * warp / NW, w1 = c0 + (c1 - c0) * (warp + 1) / NW;
 
-    // chunks of a page, a power of two (2 pages make a chunk where a page is 16 tokens)
-    const int shift = p.P > CHUNK ? 31 - __clz(p.P / CHUNK) : 0;
+    // chunks of a page, a power of two (TWO: 2 pages of 16 tokens make a chunk)
+    const int shift = TWO ? 0 : 31 - __clz(p.P / CHUNK), mask = (1 << shift) - 1;
+    // what this lane copies: part 0 .. 3 (of the second page in lanes 4 .. 7) of `bytes` bytes
+    using B = PageBlock<D>;
+    constexpr int HB = 16 * D * 9 / 8;
+    const int b = TWO ? 16 : p.blk, part = lane & 3, half = TWO ? lane >> 2 & 1 : 0;
+    const int line = part & 1 ? D / 16 : D / 2;  // bytes of a token
+    const unsigned bytes = (TWO ? 16 : CHUNK) * line;
+    const int from = part == 0 ? 0 : (part == 1 ? B::ks(b) : (part == 2 ? B::vc(b) : B::vs(b)));
+    const int to = (part == 0 ? 0 : (part == 1 ? B::ks(CHUNK) : (part == 2 ? B::vc(CHUNK) : B::vs(CHUNK)))) + half * 16 * line;
+    const unsigned page_stride = static_cast<unsigned>(p.Hkv) * p.page_bytes;
+    const uint32_t ring = smem_u32(sh.ring[warp][0]), lane_to = ring + to, bars = smem_u32(sh.full[warp]);
     State<D, NT> st;
     constexpr int ST = S::ST;
     unsigned sent = 0, done = 0;  // chunks of this warp's ring
@@ -469,7 +487,7 @@ __global__ void __launch_bounds__(32 * NW, 1) attn_tiles(PagesAttnArgs a) {
         const Unit u = find_unit<D, NT, NW>(sh, a.r.n_rows, p.Hkv, x);
         const PageRow r = page_row(p, a.r, u.i);
         const int t0 = static_cast<int>(x - u.first);
-        const long long left = u.first + u.tiles - x;
+        const long long left = u.first + u.chunks - x;
         const int t1 = t0 + static_cast<int>(left < w1 - x ? left : w1 - x);
         // the rows' least and greatest position: tokens past the greatest are nobody's
         const int rows = r.n * p.G;
@@ -485,44 +503,49 @@ __global__ void __launch_bounds__(32 * NW, 1) attn_tiles(PagesAttnArgs a) {
             at = ord * p.P;
             id = page_of(p, r.row, ord);
         };
-        const bool two = p.P < CHUNK;
-        int e0 = two ? 2 * t0 : t0 >> shift, id0, at0 = 0, id1, at1 = 0;
+        int e0 = TWO ? 2 * t0 : t0 >> shift, id0, at0 = 0, id1, at1 = 0;
         entry(e0 + lane, id0, at0);
         entry(e0 + 32 + lane, id1, at1);
         int next = t0;
+        const uint8_t *lane_from = p.pages + static_cast<long long>(u.head) * p.page_bytes + from;
         // copy the next chunk that holds something into the ring
         auto send = [&]() {
             while (next < t1) {
-                const int c = next++, e = two ? 2 * c : c >> shift;
-                if (e >= e0 + 32) {
+                const int c = next++;
+                int e = (TWO ? 2 * c : c >> shift) - e0;
+                if (e >= 32) {
+                    e -= 32;
                     e0 += 32;
                     id0 = id1;
                     at0 = at1;
                     entry(e0 + 32 + lane, id1, at1);
                 }
-                const int half = two ? lane >> 2 & 1 : 0;  // lanes 4 .. 7 copy the second page
-                const int off = two ? 0 : (c & ((1 << shift) - 1)) * CHUNK;
-                const int ida = __shfl_sync(FULL, id0, e - e0), idb = __shfl_sync(FULL, id0, e - e0 + two);
-                const int ata = __shfl_sync(FULL, at0, e - e0), atb = __shfl_sync(FULL, at0, e - e0 + two);
-                int pa = ida < 0 ? -1 : ata + off, pb = idb < 0 ? -1 : atb + (two ? 0 : off + 16);
-                if (pa > most) pa = -1;
-                if (pb > most) pb = -1;
-                if (pa < 0 && pb < 0) continue;
-                const int k = sent % ST;
-                constexpr int HB = 16 * D * 9 / 8;
-                if (lane == 0) {
-                    sh.pos[warp][k] = make_int2(pa, pb);
-                    mbar_expect_tx(&sh.full[warp][k], two ? (pa < 0 ? 0 : HB) + (pb < 0 ? 0 : HB) : 2 * HB);
-                }
-                __syncwarp();
-                if (lane < (two ? 8 : 4) && (!two || (half ? pb : pa) >= 0)) {
-                    using B = PageBlock<D>;
-                    const int b = p.blk, n = two ? 16 : CHUNK, part = lane & 3;
-                    const uint8_t *src = page_ptr(p, half ? idb : ida, u.head) + off / b * B::size(b);
-                    const int line = part & 1 ? D / 16 : D / 2;  // bytes of a token
-                    const int from = part == 0 ? 0 : (part == 1 ? B::ks(b) : (part == 2 ? B::vc(b) : B::vs(b)));
-                    const int to = part == 0 ? 0 : (part == 1 ? B::ks(CHUNK) : (part == 2 ? B::vc(CHUNK) : B::vs(CHUNK)));
-                    bulk_g2s(sh.ring[warp][k] + to + half * 16 * line, src + from + off % b * line, n * line, &sh.full[warp][k]);
+                const unsigned k = sent % ST;
+                const uint32_t bar = bars + 8 * k, dst = lane_to + k * S::CB;
+                if (TWO) {
+                    const int ia = __shfl_sync(FULL, id0, e), ib = __shfl_sync(FULL, id0, e + 1);
+                    int pa = __shfl_sync(FULL, at0, e), pb = __shfl_sync(FULL, at0, e + 1);
+                    if (ia < 0 || pa > most) pa = -1;
+                    if (ib < 0 || pb > most) pb = -1;
+                    if ((pa & pb) < 0) continue;
+                    if (lane == 0) {
+                        sh.pos[warp][k] = make_int2(pa, pb);
+                        mbar_expect(bar, (pa < 0 ? 0 : HB) + (pb < 0 ? 0 : HB));
+                    }
+                    __syncwarp();
+                    if (lane < 8 && (half ? pb : pa) >= 0)
+                        bulk_copy(dst, lane_from + static_cast<unsigned long long>(half ? ib : ia) * page_stride, bytes, bar);
+                } else {
+                    const int id = __shfl_sync(FULL, id0, e), j = c & mask, pa = __shfl_sync(FULL, at0, e) + j * CHUNK;
+                    if (id < 0 || pa > most) continue;
+                    if (lane == 0) {
+                        sh.pos[warp][k] = make_int2(pa, pa + 16 > most ? -1 : pa + 16);
+                        mbar_expect(bar, 2 * HB);
+                    }
+                    __syncwarp();
+                    if (lane < 4)
+                        bulk_copy(dst, lane_from + static_cast<unsigned long long>(id) * page_stride + ((j >> 1) * B::size(64) + (j & 1) * CHUNK * line),
+                                  bytes, bar);
                 }
                 sent++;
                 return;
@@ -545,7 +568,7 @@ __global__ void __launch_bounds__(32 * NW, 1) attn_tiles(PagesAttnArgs a) {
             send();
         }
         if (done != sent) break;
-        if (t0 == 0 && t1 == u.tiles) st.to_output(a, r, u.head, u.row0);
+        if (t0 == 0 && t1 == u.chunks) st.to_output(a, r, u.head, u.row0);
         else {
             __syncwarp();
             st.to_record(sh.record(2 * warp + (t0 == 0)));
@@ -570,7 +593,7 @@ __global__ void __launch_bounds__(32 * NW, 1) attn_tiles(PagesAttnArgs a) {
         for (k1 = k0 + 1; k1 < sh.n_list && sh.unit[sh.list[k1]] == first;) k1++;
         const Unit u = find_unit<D, NT, NW>(sh, a.r.n_rows, p.Hkv, first);
         const PageRow r = page_row(p, a.r, u.i);
-        const bool begins = u.first >= c0, ends = u.first + u.tiles <= c1;
+        const bool begins = u.first >= c0, ends = u.first + u.chunks <= c1;
         auto part_of = [&](int k) -> const float * { return sh.record(sh.list[k0 + k]); };
         if (begins && ends) {
             for (int i = tid; i < ITEMS; i += TH) {
@@ -583,7 +606,7 @@ __global__ void __launch_bounds__(32 * NW, 1) attn_tiles(PagesAttnArgs a) {
         }
         // CTA c holds chunks [N c / ctas, N (c + 1) / ctas)
         const int cf = static_cast<int>(((u.first + 1) * ctas - 1) / N);
-        const int cl = static_cast<int>(((u.first + u.tiles) * ctas - 1) / N);
+        const int cl = static_cast<int>(((u.first + u.chunks) * ctas - 1) / N);
         float *mine = a.records + (2LL * blockIdx.x + begins) * REC;
         for (int i = tid; i < ITEMS; i += TH) {
             float acc[4], m, l;
@@ -616,13 +639,17 @@ __global__ void __launch_bounds__(32 * NW, 1) attn_tiles(PagesAttnArgs a) {
     }
 }
 
-template <int D, int NT, int NW>
-int launch_tiles(const PagesAttnArgs &a, int grid, cudaStream_t st) {
+template <int D, int NT, int NW, bool TWO>
+int launch_as(const PagesAttnArgs &a, int grid, cudaStream_t st) {
     const int smem = static_cast<int>(sizeof(Shared<D, NT, NW>));
-    const cudaError_t e = cudaFuncSetAttribute(attn_tiles<D, NT, NW>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    const cudaError_t e = cudaFuncSetAttribute(attn_chunks<D, NT, NW, TWO>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return static_cast<int>(e);
-    attn_tiles<D, NT, NW><<<grid, 32 * NW, smem, st>>>(a);
+    attn_chunks<D, NT, NW, TWO><<<grid, 32 * NW, smem, st>>>(a);
     return static_cast<int>(cudaGetLastError());
+}
+template <int D, int NT, int NW>
+int launch_chunks(const PagesAttnArgs &a, int grid, cudaStream_t st) {
+    return a.p.P < CHUNK ? launch_as<D, NT, NW, true>(a, grid, st) : launch_as<D, NT, NW, false>(a, grid, st);
 }
 
 }  // namespace
@@ -631,8 +658,8 @@ int launch_pages_attention(const PagesAttnArgs &a, int num_sms, void *stream) {
     auto st = static_cast<cudaStream_t>(stream);
     const int grid = num_sms < PAGES_MAX_CTAS ? num_sms : PAGES_MAX_CTAS;
     // 8 query rows fill one n tile; more share the conversions of two
-    if (a.r.max_new * a.p.G <= 8) return a.p.d == 128 ? launch_tiles<128, 1, 16>(a, grid, st) : launch_tiles<64, 1, 16>(a, grid, st);
-    return a.p.d == 128 ? launch_tiles<128, 2, 8>(a, grid, st) : launch_tiles<64, 2, 8>(a, grid, st);
+    if (a.r.max_new * a.p.G <= 8) return a.p.d == 128 ? launch_chunks<128, 1, 16>(a, grid, st) : launch_chunks<64, 1, 16>(a, grid, st);
+    return a.p.d == 128 ? launch_chunks<128, 2, 8>(a, grid, st) : launch_chunks<64, 2, 8>(a, grid, st);
 }
 
 }  // namespace dq
