@@ -40,7 +40,8 @@ constexpr float LN2 = 0.69314718055994530942f;
 constexpr uint64_t WAIT_NS = 2000000000ull;  // longest wait for a copy
 constexpr float SLACK = 8.f, LIFT = 7.f;   // log2 units
 constexpr int CHUNK = 32;                  // tokens
-constexpr int MIN_CHUNKS = 16;             // chunks that make a CTA worth its merge
+constexpr int UNIT_COST = 2;               // chunks that a unit's beginning and end are worth
+constexpr int MIN_PLACES = 16;             // places that make a CTA worth its merge
 
 __device__ __forceinline__ void mbar_expect(uint32_t bar, unsigned bytes) {
     asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n" ::"r"(bar), "r"(bytes) : "memory");
@@ -104,31 +105,33 @@ struct State {
         }
     }
 
-    // Queries of rows row0 .. row0 + 8 NT of the unit's (token, head) rows.
-    __device__ __forceinline__ void load_q(const PagesAttnArgs &a, const PageRow &r, int head, int row0) {
+    // Queries of rows row0 .. row0 + 8 NT of the unit's (token, head) rows: the loads first,
+    // so that they are on their way while the first chunks are sent for.
+    __device__ __forceinline__ static void fetch_q(uint4 (&w)[NT][D / 32], const PagesAttnArgs &a, const PageRow &r, int head, int row0) {
         const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+#pragma unroll
+        for (int n = 0; n < NT; n++) {
+            const int row = row0 + 8 * n + g, tok = row / a.p.G;
+            const uint16_t *src = a.q + (static_cast<long long>(r.q0) + tok) * a.qt + (head * a.p.G + row - tok * a.p.G) * a.qh + t * (D / 4);
+#pragma unroll
+            for (int i = 0; i < D / 32; i++)
+                w[n][i] = row < r.n * a.p.G ? *reinterpret_cast<const uint4 *>(src + 8 * i) : make_uint4(0, 0, 0, 0);
+        }
+    }
+    __device__ __forceinline__ void load_q(const uint4 (&w)[NT][D / 32], const PagesAttnArgs &a, const PageRow &r, int row0) {
+        const int lane = threadIdx.x & 31, t = lane & 3;
         const int rows = r.n * a.p.G;
 #pragma unroll
         for (int n = 0; n < NT; n++) {
-            const int row = row0 + 8 * n + g;
-            float x[D / 4];
-            float top = 0.f;
-            if (row < rows) {
-                const int tok = row / a.p.G;
-                const uint16_t *src = a.q + (static_cast<long long>(r.q0) + tok) * a.qt + (head * a.p.G + row - tok * a.p.G) * a.qh + t * (D / 4);
+            float x[D / 4], top = 0.f;
 #pragma unroll
-                for (int i = 0; i < D / 32; i++) {
-                    const uint4 w = *reinterpret_cast<const uint4 *>(src + 8 * i);
-                    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+            for (int i = 0; i < D / 32; i++) {
+                const uint32_t u[4] = {w[n][i].x, w[n][i].y, w[n][i].z, w[n][i].w};
 #pragma unroll
-                    for (int j = 0; j < 4; j++) {
-                        x[8 * i + 2 * j] = from16(static_cast<uint16_t>(u[j] & 0xffffu), a.p.bf16);
-                        x[8 * i + 2 * j + 1] = from16(static_cast<uint16_t>(u[j] >> 16), a.p.bf16);
-                    }
+                for (int j = 0; j < 4; j++) {
+                    x[8 * i + 2 * j] = from16(static_cast<uint16_t>(u[j] & 0xffffu), a.p.bf16);
+                    x[8 * i + 2 * j + 1] = from16(static_cast<uint16_t>(u[j] >> 16), a.p.bf16);
                 }
-            } else {
-#pragma unroll
-                for (int i = 0; i < D / 4; i++) x[i] = 0.f;
             }
 #pragma unroll
             for (int i = 0; i < D / 4; i++) top = fmaxf(top, fabsf(x[i]));
@@ -339,11 +342,11 @@ struct State {
 };
 
 // ---- the call's units --------------------------------------------------------------------
-// A unit of row i (head-major, query blocks within), its first chunk and their number.
+// Units stand one after the other on a line, rows in order, KV heads, then query blocks
+// within: UNIT_COST places for what a unit costs beside its chunks, then its chunks.
 struct Unit {
     int i, head, row0;
-    long long first;
-    int chunks;
+    int first, chunks;  // place of its first chunk, and their number
 };
 
 template <int D, int NT, int NW>
@@ -356,58 +359,85 @@ struct Shared {
     __align__(128) uint8_t ring[NW][ST][CB];
     __align__(16) float rec[NW][REC];
     uint64_t full[NW][ST];
-    int2 pos[NW][ST];                              // positions of a chunk's two halves
-    long long first[DQ_PAGES_MAX_ROWS + 1];        // chunks before row i
-    int chunks[DQ_PAGES_MAX_ROWS];                  // chunks of each of the row's units
+    int2 pos[NW][ST];                  // positions of a chunk's two halves
+    int first[DQ_PAGES_MAX_ROWS + 1];  // places before row i
+    int row[DQ_PAGES_MAX_ROWS], len[DQ_PAGES_MAX_ROWS];
     long long part[NW];
-    long long unit[2 * NW];                        // first chunk of the unit that each record is a part of, -1: none
-    int list[2 * NW], n_list, last;
+    int unit[2 * NW];                  // the unit that each record is a part of, by its first chunk's place; -1: none
+    int last;
+    __device__ const float *record(int k) const { return k & 1 ? reinterpret_cast<const float *>(ring[k >> 1]) : rec[k >> 1]; }
     __device__ float *record(int k) { return k & 1 ? reinterpret_cast<float *>(ring[k >> 1]) : rec[k >> 1]; }
 };
 
 __device__ __forceinline__ int row_chunks(const PagesAttnArgs &a, int len) {
-    // every unit has a chunk, so that queries that see nothing get their zeros
-    const int n = a.sel ? (len > 0 ? (a.n_sel * a.p.P + CHUNK - 1) / CHUNK : 0) : (len + CHUNK - 1) / CHUNK;
-    return n > 1 ? n : 1;
+    return (a.sel ? a.n_sel * a.p.P + CHUNK - 1 : len + CHUNK - 1) / CHUNK;
 }
 
-// The unit that holds chunk x.
+// The unit at place x (the same for the whole warp).
 template <int D, int NT, int NW>
-__device__ __forceinline__ Unit find_unit(const Shared<D, NT, NW> &sh, int n_rows, int Hkv, long long x) {
-    int lo = 0, hi = n_rows - 1;
-    while (lo < hi) {  // the last row whose first chunk is <= x (rows without any share it with the next)
-        const int mid = (lo + hi + 1) >> 1;
-        if (sh.first[mid] <= x) lo = mid;
-        else hi = mid - 1;
-    }
+__device__ __forceinline__ Unit find_unit(const Shared<D, NT, NW> &sh, const PagesAttnArgs &a, int x) {
+    // the last row that begins at or before x (rows without a place begin where the next one does)
+    const int lane = threadIdx.x & 31, n = a.r.n_rows;
+    int lo = 0;
+    if (n > 32) lo = 32 * (__popc(__ballot_sync(FULL, 32 * lane < n && sh.first[32 * lane] <= x)) - 1);
+    lo += __popc(__ballot_sync(FULL, lo + lane < n && sh.first[lo + lane] <= x)) - 1;
     Unit u;
     u.i = lo;
-    u.chunks = sh.chunks[lo];
-    const long long in = x - sh.first[lo];
-    const int unit = static_cast<int>(in / u.chunks);
-    u.first = sh.first[lo] + static_cast<long long>(unit) * u.chunks;
-    const int blocks = static_cast<int>((sh.first[lo + 1] - sh.first[lo]) / (static_cast<long long>(u.chunks) * Hkv));
-    u.head = unit / blocks;
-    u.row0 = (unit % blocks) * 8 * NT;
+    u.chunks = row_chunks(a, sh.len[lo]);
+    const unsigned places = u.chunks + UNIT_COST, unit = static_cast<unsigned>(x - sh.first[lo]) / places;
+    u.first = sh.first[lo] + unit * places + UNIT_COST;
+    if (a.r.max_new * a.p.G <= 8 * NT) {
+        u.head = unit;
+        u.row0 = 0;
+    } else {
+        const unsigned blocks = static_cast<unsigned>(sh.first[lo + 1] - sh.first[lo]) / (places * a.p.Hkv);
+        u.head = unit / blocks;
+        u.row0 = (unit - u.head * blocks) * 8 * NT;
+    }
     return u;
+}
+
+// Row i of the call, which the prefix found to be in order.
+template <int D, int NT, int NW>
+__device__ __forceinline__ PageRow known_row(const Shared<D, NT, NW> &sh, const PagesAttnArgs &a, int i) {
+    PageRow r;
+    r.row = sh.row[i];
+    r.len = sh.len[i];
+    r.q0 = a.r.cu ? a.r.cu[i] : i;
+    r.n = a.r.cu ? a.r.cu[i + 1] - r.q0 : 1;
+    return r;
+}
+
+// Share k of n places among m: [share(k), share(k + 1)).
+__device__ __forceinline__ int share(int n, int m, int k) {
+    const unsigned q = static_cast<unsigned>(n) / m, rest = n - q * m;
+    return k * q + (k < static_cast<int>(rest) ? k : rest);
+}
+// The share that place x is in (m <= n).
+__device__ __forceinline__ int share_of(int n, int m, int x) {
+    const unsigned q = static_cast<unsigned>(n) / m, rest = n - q * m, ahead = rest * (q + 1);
+    return static_cast<unsigned>(x) < ahead ? x / (q + 1) : rest + (x - ahead) / q;
 }
 
 // One thread's 4 channels at c of row `row` over n records, added up in order.
 template <int D, int NT, class F>
 __device__ __forceinline__ void add_records(int n, int row, int c, F rec_of, float (&acc)[4], float &m, float &l) {
     m = -INFINITY;
-    for (int k = 0; k < n; k++) m = fmaxf(m, rec_of(k)[8 * NT * D + row]);
     l = 0.f;
     acc[0] = acc[1] = acc[2] = acc[3] = 0.f;
+#pragma unroll 4
     for (int k = 0; k < n; k++) {
         const float *r = rec_of(k);
-        const float mk = r[8 * NT * D + row], w = mk == -INFINITY ? 0.f : ex2(mk - m);
-        l += w * r[8 * NT * (D + 1) + row];
+        const float mk = r[8 * NT * D + row], lk = r[8 * NT * (D + 1) + row];
         const float4 x = *reinterpret_cast<const float4 *>(r + row * D + c);
-        acc[0] += w * x.x;
-        acc[1] += w * x.y;
-        acc[2] += w * x.z;
-        acc[3] += w * x.w;
+        const float mx = fmaxf(m, mk), mu = mx == -INFINITY ? 0.f : mx;
+        const float wa = ex2(m - mu), wb = ex2(mk - mu);  // 0 for a part that saw nothing
+        m = mx;
+        l = l * wa + lk * wb;
+        acc[0] = acc[0] * wa + x.x * wb;
+        acc[1] = acc[1] * wa + x.y * wb;
+        acc[2] = acc[2] * wa + x.z * wb;
+        acc[3] = acc[3] * wa + x.w * wb;
     }
 }
 
@@ -429,16 +459,19 @@ __global__ void __launch_bounds__(32 * NW, 1) attn_chunks(PagesAttnArgs a) {
     S &sh = *reinterpret_cast<S *>(raw);
     const PagesView &p = a.p;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    // chunks before each row: a prefix over the rows, NW 32 at a time
+    constexpr int ST = S::ST;
+    if (lane < ST) mbar_init(&sh.full[warp][lane], 1);
+    fence_mbar_init();
+    // places before each row: a prefix over the rows, 32 NW at a time
     long long base = 0;
     for (int i0 = 0; i0 < a.r.n_rows; i0 += 32 * NW) {
         const int i = i0 + tid;
         long long w = 0;
         if (i < a.r.n_rows) {
             const PageRow r = page_row(p, a.r, i);
-            const int chunks = row_chunks(a, r.len);
-            sh.chunks[i] = chunks;
-            w = static_cast<long long>((r.n * p.G + 8 * NT - 1) / (8 * NT)) * p.Hkv * chunks;
+            sh.row[i] = r.row;
+            sh.len[i] = r.len;
+            if (r.len > 0) w = static_cast<long long>((r.n * p.G + 8 * NT - 1) / (8 * NT)) * p.Hkv * (row_chunks(a, r.len) + UNIT_COST);
         }
         long long s = w;
 #pragma unroll
@@ -449,21 +482,38 @@ __global__ void __launch_bounds__(32 * NW, 1) attn_chunks(PagesAttnArgs a) {
         if (lane == 31) sh.part[warp] = s;
         __syncthreads();
         long long before = base;
-        for (int k = 0; k < warp; k++) before += sh.part[k];
-        if (i < a.r.n_rows) sh.first[i] = before + s - w;
-        for (int k = 0; k < NW; k++) base += sh.part[k];
-        __syncthreads();
+#pragma unroll
+        for (int k = 0; k < NW; k++) {
+            const long long t = sh.part[k];
+            if (k < warp) before += t;
+            base += t;
+        }
+        if (i < a.r.n_rows) sh.first[i] = static_cast<int>(before + s - w);
+        if (i0 + 32 * NW < a.r.n_rows) __syncthreads();
     }
-    const long long N = base;
+    if (base > 0x7fffffff) {  // more places than int counts
+        if (tid == 0) atomicOr(p.status, PST_ARG);
+        return;
+    }
+    const int N = static_cast<int>(base);
     if (tid == 0) sh.first[a.r.n_rows] = N;
     if (tid < 2 * NW) sh.unit[tid] = -1;
     __syncthreads();
-    // this CTA's chunks [c0, c1), this warp's [w0, w1)
-    long long ctas = N / MIN_CHUNKS;
-    ctas = ctas < 1 ? 1 : (ctas > gridDim.x ? gridDim.x : ctas);
-    if (blockIdx.x >= ctas) return;
-    const long long c0 = N * blockIdx.x / ctas, c1 = N * (blockIdx.x + 1) / ctas;
-    const long long w0 = c0 + (c1 - c0) * warp / NW, w1 = c0 + (c1 - c0) * (warp + 1) / NW;
+    // rows that hold nothing: zeros
+    for (int i = blockIdx.x; i < a.r.n_rows; i += gridDim.x) {
+        if (sh.len[i] > 0) continue;
+        const PageRow r = page_row(p, a.r, i);
+        uint4 *o = reinterpret_cast<uint4 *>(a.out + static_cast<long long>(r.q0) * p.Hq * D);
+        for (int k = tid; k < r.n * p.Hq * (D / 8); k += 32 * NW) o[k] = make_uint4(0, 0, 0, 0);
+        if (a.lse)
+            for (int k = tid; k < r.n * p.Hq; k += 32 * NW) a.lse[static_cast<long long>(r.q0) * p.Hq + k] = -INFINITY;
+    }
+    // this CTA's places [c0, c1), this warp's [w0, w1)
+    int ctas = N / MIN_PLACES;
+    ctas = ctas < 1 ? 1 : (ctas > static_cast<int>(gridDim.x) ? gridDim.x : ctas);
+    if (N == 0 || static_cast<int>(blockIdx.x) >= ctas) return;
+    const int c0 = share(N, ctas, blockIdx.x), c1 = share(N, ctas, blockIdx.x + 1);
+    const int w0 = c0 + share(c1 - c0, NW, warp), w1 = c0 + share(c1 - c0, NW, warp + 1);
 
     // chunks of a page, a power of two (TWO: 2 pages of 16 tokens make a chunk)
     const int shift = TWO ? 0 : 31 - __clz(p.P / CHUNK), mask = (1 << shift) - 1;
@@ -478,21 +528,20 @@ __global__ void __launch_bounds__(32 * NW, 1) attn_chunks(PagesAttnArgs a) {
     const unsigned page_stride = static_cast<unsigned>(p.Hkv) * p.page_bytes;
     const uint32_t ring = smem_u32(sh.ring[warp][0]), lane_to = ring + to, bars = smem_u32(sh.full[warp]);
     State<D, NT> st;
-    constexpr int ST = S::ST;
     unsigned sent = 0, done = 0;  // chunks of this warp's ring
-    if (lane < ST) mbar_init(&sh.full[warp][lane], 1);
-    fence_mbar_init();
-    __syncwarp();
-    for (long long x = w0; x < w1;) {
-        const Unit u = find_unit<D, NT, NW>(sh, a.r.n_rows, p.Hkv, x);
-        const PageRow r = page_row(p, a.r, u.i);
-        const int t0 = static_cast<int>(x - u.first);
-        const long long left = u.first + u.chunks - x;
-        const int t1 = t0 + static_cast<int>(left < w1 - x ? left : w1 - x);
+    for (int x = w0; x < w1;) {
+        const Unit u = find_unit<D, NT, NW>(sh, a, x);
+        const int t0 = x > u.first ? x - u.first : 0;
+        const int t1 = u.first + u.chunks < w1 ? u.chunks : w1 - u.first;
+        x = u.first + u.chunks;
+        if (t1 <= t0) continue;  // none of its chunks
+        const PageRow r = known_row<D, NT, NW>(sh, a, u.i);
         // the rows' least and greatest position: tokens past the greatest are nobody's
         const int rows = r.n * p.G;
         const int end = u.row0 + 8 * NT < rows ? u.row0 + 8 * NT : rows;
         const int least = r.len - r.n + u.row0 / p.G, most = r.len - r.n + (end - 1) / p.G;
+        uint4 qw[NT][D / 32];
+        st.fetch_q(qw, a, r, u.head, u.row0);
         // page numbers of 32 entries at a time, one a lane, the next 32 on their way
         const int *sel = a.sel ? a.sel + (static_cast<long long>(u.i) * p.Hkv + u.head) * a.n_sel : nullptr;
         auto entry = [&](int e, int &id, int &at) {  // at: position of the page's first token
@@ -553,7 +602,7 @@ __global__ void __launch_bounds__(32 * NW, 1) attn_chunks(PagesAttnArgs a) {
         };
 #pragma unroll
         for (int k = 0; k < ST; k++) send();
-        st.load_q(a, r, u.head, u.row0);
+        st.load_q(qw, a, r, u.row0);
         st.reset();
         while (done != sent) {
             const int k = done % ST;
@@ -574,44 +623,40 @@ __global__ void __launch_bounds__(32 * NW, 1) attn_chunks(PagesAttnArgs a) {
             st.to_record(sh.record(2 * warp + (t0 == 0)));
             if (lane == 0) sh.unit[2 * warp + (t0 == 0)] = u.first;
         }
-        x += t1 - t0;
     }
     __syncthreads();
 
     // The records that warps left, in order: a unit's are neighbours.  All warps add up one
     // unit after the other; a unit that other CTAs share goes to the workspace.
-    if (tid == 0) {
-        int n = 0;
-        for (int k = 0; k < 2 * NW; k++)
-            if (sh.unit[k] >= 0) sh.list[n++] = k;
-        sh.n_list = n;
-    }
-    __syncthreads();
     constexpr int REC = S::REC, TH = 32 * NW, ITEMS = 8 * NT * (D / 4);
-    for (int k0 = 0, k1; k0 < sh.n_list; k0 = k1) {
-        const long long first = sh.unit[sh.list[k0]];
-        for (k1 = k0 + 1; k1 < sh.n_list && sh.unit[sh.list[k1]] == first;) k1++;
-        const Unit u = find_unit<D, NT, NW>(sh, a.r.n_rows, p.Hkv, first);
-        const PageRow r = page_row(p, a.r, u.i);
-        const bool begins = u.first >= c0, ends = u.first + u.chunks <= c1;
-        auto part_of = [&](int k) -> const float * { return sh.record(sh.list[k0 + k]); };
+    const int mine_is = lane < 2 * NW ? sh.unit[lane] : -1;
+    unsigned left = __ballot_sync(FULL, mine_is >= 0);
+    while (left) {
+        const int k0 = __ffs(left) - 1, first = __shfl_sync(FULL, mine_is, k0);
+        const unsigned run = __ballot_sync(FULL, mine_is == first);
+        left &= ~run;
+        const int n = __popc(run);
+        const Unit u = find_unit<D, NT, NW>(sh, a, first);
+        const PageRow r = known_row<D, NT, NW>(sh, a, u.i);
+        const bool begins = first >= c0, ends = first + u.chunks <= c1;
+        // the run: an odd record (begun in its warp) at most at the front, then every warp's even one
+        const int even = (k0 + 1) & ~1, odd = k0 & 1;
+        auto part_of = [&](int k) -> const float * { return k < odd ? sh.record(k0) : sh.rec[(even >> 1) + k - odd]; };
         if (begins && ends) {
             for (int i = tid; i < ITEMS; i += TH) {
                 float acc[4], m, l;
                 const int row = i / (D / 4), c = i % (D / 4) * 4;
-                add_records<D, NT>(k1 - k0, row, c, part_of, acc, m, l);
+                add_records<D, NT>(n, row, c, part_of, acc, m, l);
                 write4<D>(a, r, u.head, u.row0 + row, c, acc, m, l);
             }
             continue;
         }
-        // CTA c holds chunks [N c / ctas, N (c + 1) / ctas)
-        const int cf = static_cast<int>(((u.first + 1) * ctas - 1) / N);
-        const int cl = static_cast<int>(((u.first + u.chunks) * ctas - 1) / N);
+        const int cf = share_of(N, ctas, first), cl = share_of(N, ctas, first + u.chunks - 1);
         float *mine = a.records + (2LL * blockIdx.x + begins) * REC;
         for (int i = tid; i < ITEMS; i += TH) {
             float acc[4], m, l;
             const int row = i / (D / 4), c = i % (D / 4) * 4;
-            add_records<D, NT>(k1 - k0, row, c, part_of, acc, m, l);
+            add_records<D, NT>(n, row, c, part_of, acc, m, l);
             *reinterpret_cast<float4 *>(mine + row * D + c) = make_float4(acc[0], acc[1], acc[2], acc[3]);
             if (c == 0) {
                 mine[8 * NT * D + row] = m;
