@@ -364,7 +364,7 @@ struct Shared {
     int row[DQ_PAGES_MAX_ROWS], len[DQ_PAGES_MAX_ROWS];
     long long part[NW];
     int unit[2 * NW];                  // the unit that each record is a part of, by its first chunk's place; -1: none
-    int last;
+    int last[2];
     __device__ const float *record(int k) const { return k & 1 ? reinterpret_cast<const float *>(ring[k >> 1]) : rec[k >> 1]; }
     __device__ float *record(int k) { return k & 1 ? reinterpret_cast<float *>(ring[k >> 1]) : rec[k >> 1]; }
 };
@@ -544,17 +544,23 @@ __global__ void __launch_bounds__(32 * NW, 1) attn_chunks(PagesAttnArgs a) {
         st.fetch_q(qw, a, r, u.head, u.row0);
         // page numbers of 32 entries at a time, one a lane, the next 32 on their way
         const int *sel = a.sel ? a.sel + (static_cast<long long>(u.i) * p.Hkv + u.head) * a.n_sel : nullptr;
-        auto entry = [&](int e, int &id, int &at) {  // at: position of the page's first token
-            id = -1;
+        auto entry = [&](int e, int &id, int &at) {  // at: position of the page's first token, -1: no page
+            id = at = -1;
             int ord = e;
             if (sel) ord = e < a.n_sel ? sel[e] : -1;
             if (r.row < 0 || ord < 0 || ord >= p.M || ord * p.P >= r.len) return;
             at = ord * p.P;
-            id = page_of(p, r.row, ord);
+            id = p.table[static_cast<long long>(r.row) * p.M + ord];
         };
-        int e0 = TWO ? 2 * t0 : t0 >> shift, id0, at0 = 0, id1, at1 = 0;
+        auto checked = [&](int id, int at) {
+            if (at < 0 || (id >= 0 && id < p.n_pages)) return id;
+            atomicOr(p.status, PST_TABLE);
+            return -1;
+        };
+        int e0 = TWO ? 2 * t0 : t0 >> shift, id0, at0, id1, at1;
         entry(e0 + lane, id0, at0);
         entry(e0 + 32 + lane, id1, at1);
+        id0 = checked(id0, at0);
         int next = t0;
         const uint8_t *lane_from = p.pages + static_cast<long long>(u.head) * p.page_bytes + from;
         // copy the next chunk that holds something into the ring
@@ -565,7 +571,7 @@ __global__ void __launch_bounds__(32 * NW, 1) attn_chunks(PagesAttnArgs a) {
                 if (e >= 32) {
                     e -= 32;
                     e0 += 32;
-                    id0 = id1;
+                    id0 = checked(id1, at1);
                     at0 = at1;
                     entry(e0 + 32 + lane, id1, at1);
                 }
@@ -626,61 +632,75 @@ __global__ void __launch_bounds__(32 * NW, 1) attn_chunks(PagesAttnArgs a) {
     }
     __syncthreads();
 
-    // The records that warps left, in order: a unit's are neighbours.  All warps add up one
-    // unit after the other; a unit that other CTAs share goes to the workspace.
-    constexpr int REC = S::REC, TH = 32 * NW, ITEMS = 8 * NT * (D / 4);
+    // The records that warps left, in order: a unit's are neighbours (a run), the first of
+    // them odd where the unit begins in its warp, then one for each warp.  Groups of
+    // warps take the runs in turn: a unit that is all here is written, a part of one goes
+    // to the workspace (at most two: of the unit that began before this CTA, and of the
+    // one that goes on after it).
+    constexpr int REC = S::REC, ITEMS = 8 * NT * (D / 4);
+    constexpr int GROUPS = 32 * NW > ITEMS ? 32 * NW / ITEMS : 1, TH = 32 * NW / GROUPS;
     const int mine_is = lane < 2 * NW ? sh.unit[lane] : -1;
-    unsigned left = __ballot_sync(FULL, mine_is >= 0);
-    while (left) {
+    int front = -1, back = -1, turn = 0;
+    for (unsigned left = __ballot_sync(FULL, mine_is >= 0); left; turn++) {
         const int k0 = __ffs(left) - 1, first = __shfl_sync(FULL, mine_is, k0);
         const unsigned run = __ballot_sync(FULL, mine_is == first);
         left &= ~run;
-        const int n = __popc(run);
         const Unit u = find_unit<D, NT, NW>(sh, a, first);
-        const PageRow r = known_row<D, NT, NW>(sh, a, u.i);
         const bool begins = first >= c0, ends = first + u.chunks <= c1;
-        // the run: an odd record (begun in its warp) at most at the front, then every warp's even one
-        const int even = (k0 + 1) & ~1, odd = k0 & 1;
+        if (!begins) front = first;
+        else if (!ends) back = first;
+        if (turn % GROUPS != tid / TH) continue;
+        const PageRow r = known_row<D, NT, NW>(sh, a, u.i);
+        const int n = __popc(run), even = (k0 + 1) & ~1, odd = k0 & 1;
         auto part_of = [&](int k) -> const float * { return k < odd ? sh.record(k0) : sh.rec[(even >> 1) + k - odd]; };
-        if (begins && ends) {
-            for (int i = tid; i < ITEMS; i += TH) {
-                float acc[4], m, l;
-                const int row = i / (D / 4), c = i % (D / 4) * 4;
-                add_records<D, NT>(n, row, c, part_of, acc, m, l);
-                write4<D>(a, r, u.head, u.row0 + row, c, acc, m, l);
-            }
-            continue;
-        }
-        const int cf = share_of(N, ctas, first), cl = share_of(N, ctas, first + u.chunks - 1);
-        float *mine = a.records + (2LL * blockIdx.x + begins) * REC;
-        for (int i = tid; i < ITEMS; i += TH) {
+        float *to = a.records + (2LL * blockIdx.x + begins) * REC;
+        for (int i = tid % TH; i < ITEMS; i += TH) {
             float acc[4], m, l;
             const int row = i / (D / 4), c = i % (D / 4) * 4;
             add_records<D, NT>(n, row, c, part_of, acc, m, l);
-            *reinterpret_cast<float4 *>(mine + row * D + c) = make_float4(acc[0], acc[1], acc[2], acc[3]);
-            if (c == 0) {
-                mine[8 * NT * D + row] = m;
-                mine[8 * NT * (D + 1) + row] = l;
-            }
-        }
-        __threadfence();
-        __syncthreads();
-        if (tid == 0) {
-            sh.last = atomic_add_acq_rel_gpu(a.tickets + cf, 1) == cl - cf;
-            if (sh.last) a.tickets[cf] = 0;  // for the next call
-        }
-        __syncthreads();
-        if (sh.last) {
-            __threadfence();
-            auto cta_of = [&](int k) -> const float * { return a.records + (2LL * (cf + k) + (k == 0)) * REC; };
-            for (int i = tid; i < ITEMS; i += TH) {
-                float acc[4], m, l;
-                const int row = i / (D / 4), c = i % (D / 4) * 4;
-                add_records<D, NT>(cl - cf + 1, row, c, cta_of, acc, m, l);
+            if (begins && ends) {
                 write4<D>(a, r, u.head, u.row0 + row, c, acc, m, l);
+            } else {
+                *reinterpret_cast<float4 *>(to + row * D + c) = make_float4(acc[0], acc[1], acc[2], acc[3]);
+                if (c == 0) {
+                    to[8 * NT * D + row] = m;
+                    to[8 * NT * (D + 1) + row] = l;
+                }
             }
         }
-        __syncthreads();
+    }
+    if (front < 0 && back < 0) return;
+    // The last of a unit's CTAs to bring its part adds all parts up.  The count releases the
+    // block's writes (which the barrier put before it) and acquires the others'.
+    __syncthreads();
+    if (warp < 2) {
+        const int first = warp == 0 ? front : back;
+        int all = 0;
+        if (first >= 0) {
+            const Unit u = find_unit<D, NT, NW>(sh, a, first);
+            const int cf = share_of(N, ctas, first), others = share_of(N, ctas, first + u.chunks - 1) - cf;
+            if (lane == 0) {
+                all = atomic_add_acq_rel_gpu(a.tickets + cf, 1) == others;
+                if (all) a.tickets[cf] = 0;  // for the next call
+            }
+        }
+        if (lane == 0) sh.last[warp] = all;
+    }
+    __syncthreads();
+#pragma unroll 1
+    for (int s = 0; s < 2; s++) {
+        if (!sh.last[s]) continue;
+        const int first = s == 0 ? front : back;
+        const Unit u = find_unit<D, NT, NW>(sh, a, first);
+        const PageRow r = known_row<D, NT, NW>(sh, a, u.i);
+        const int cf = share_of(N, ctas, first), n = share_of(N, ctas, first + u.chunks - 1) - cf + 1;
+        auto cta_of = [&](int k) -> const float * { return a.records + (2LL * (cf + k) + (k == 0)) * REC; };
+        for (int i = tid; i < ITEMS; i += 32 * NW) {
+            float acc[4], m, l;
+            const int row = i / (D / 4), c = i % (D / 4) * 4;
+            add_records<D, NT>(n, row, c, cta_of, acc, m, l);
+            write4<D>(a, r, u.head, u.row0 + row, c, acc, m, l);
+        }
     }
 }
 
