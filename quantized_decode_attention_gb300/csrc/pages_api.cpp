@@ -250,7 +250,7 @@ dq_status dq_pages_select(const dq_pages_config *cfg, const dq_pages_buffers *bu
     a.n_sel = n_sel;
     a.keep_first = keep_first;
     a.keep_last = keep_last;
-    return launched(dq::launch_pages_select(a, stream), "select launch");
+    return launched(dq::launch_pages_select(a, device_sms(), stream), "select launch");
 }
 
 dq_status dq_pages_check(const dq_pages_buffers *bufs, void *stream) {

@@ -94,6 +94,6 @@ int launch_pages_compact(const PagesView &p, int *ws, int num_sms, void *stream)
 int launch_pages_append(const PagesStoreArgs &a, void *stream);
 int launch_pages_read(const PagesReadArgs &a, void *stream);
 int launch_pages_attention(const PagesAttnArgs &a, int num_sms, void *stream);
-int launch_pages_select(const PagesSelectArgs &a, void *stream);
+int launch_pages_select(const PagesSelectArgs &a, int num_sms, void *stream);
 
 }  // namespace dq

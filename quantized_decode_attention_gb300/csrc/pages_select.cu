@@ -1,4 +1,12 @@
 // Paged cache: the pages that a cheap score chooses for each row and KV head.
+//
+// score(page) = sum_c Q+_c largest_c + Q-_c smallest_c, both factors whole numbers of 8
+// bits: 2 D products in D / 2 dp4a, exact.  A page costs its summary of 2 D + 4 bytes, so
+// the kernel is bound by reading summaries, and for few rows by latency: a cluster of up
+// to 8 CTAs shares the pages of one (row, KV head) and sends its scores to the first
+// CTA's shared memory.  That CTA finds the n_sel-th largest score digit by digit (four
+// histograms of 8 bits) and writes the pages above it, and the first of those equal to
+// it, in order: counts and prefixes alone, so that the choice depends on nothing else.
 #include <cuda_runtime.h>
 
 #include "pages.cuh"
@@ -6,7 +14,7 @@
 namespace dq {
 namespace {
 
-constexpr int SE_THREADS = 256;
+constexpr int SE_THREADS = 512, SE_WARPS = SE_THREADS / 32;
 
 // Keys that order like the floats (no NaN), as unsigned.
 __device__ __forceinline__ uint32_t order_key(float x) {
@@ -36,7 +44,7 @@ __device__ void group_query(const PagesSelectArgs &a, int q0, int head, int8_t *
     if ((tid & 31) == 0) red[tid >> 5] = m;
     __syncthreads();
     m = red[0];
-    for (int i = 1; i < SE_THREADS / 32; i++) m = fmaxf(m, red[i]);
+    for (int i = 1; i < SE_WARPS; i++) m = fmaxf(m, red[i]);
     if (tid < D) {
         const bool ok = m > 0.f && m < INFINITY;
         const float inv = ok ? __fdiv_rn(127.f, m) : 0.f;
@@ -46,74 +54,189 @@ __device__ void group_query(const PagesSelectArgs &a, int q0, int head, int8_t *
     __syncthreads();
 }
 
-// One CTA per (row, KV head): scores of all pages to shared memory; a page's place is the
-// number of pages before it in the order (score down, ordinal up).
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm("mov.u32 %0, %%cluster_ctarank;\n" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ uint32_t cluster_size() {
+    uint32_t r;
+    asm("mov.u32 %0, %%cluster_nctarank;\n" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_sync_all() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;\n" ::: "memory");
+}
+// Store to the first CTA's shared memory.
+__device__ __forceinline__ void store_first(uint32_t addr, uint32_t v) {
+    uint32_t there;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, 0;\n" : "=r"(there) : "r"(addr));
+    asm volatile("st.shared::cluster.u32 [%0], %1;\n" ::"r"(there), "r"(v) : "memory");
+}
+
+// One cluster per (row, KV head).
 template <int D>
 __global__ void __launch_bounds__(SE_THREADS) select_kernel(PagesSelectArgs a) {
-    extern __shared__ uint32_t key[];
+    extern __shared__ uint32_t key[];  // [max_pages_per_seq], the first CTA's counts
     __shared__ __align__(16) int8_t qi[2 * D];
-    __shared__ float red[SE_THREADS / 32];
-    __shared__ int wsum[SE_THREADS / 32], base;
+    __shared__ float red[SE_WARPS];
+    __shared__ int hist[256], above[SE_WARPS], equal[SE_WARPS];
+    __shared__ uint32_t prefix;
+    __shared__ int want;
     const PagesView &p = a.p;
-    const PageRow r = page_row(p, a.r, blockIdx.x);
-    const int head = blockIdx.y, tid = threadIdx.x;
+    const uint32_t rank = cluster_rank(), ctas = cluster_size();
+    const int row = blockIdx.x / ctas, head = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const PageRow r = page_row(p, a.r, row);
     const int np = (r.len + p.P - 1) / p.P;
-    int *out = a.sel + (static_cast<long long>(blockIdx.x) * p.Hkv + head) * a.n_sel;
-    if (np <= a.n_sel) {
-        for (int i = tid; i < a.n_sel; i += SE_THREADS) out[i] = i < np ? i : -1;
+    int *out = a.sel + (static_cast<long long>(row) * p.Hkv + head) * a.n_sel;
+    if (np <= a.n_sel) {  // the same for the whole cluster
+        if (rank == 0)
+            for (int i = tid; i < a.n_sel; i += SE_THREADS) out[i] = i < np ? i : -1;
         return;
     }
     group_query<D>(a, r.q0, head, qi, red);
-    for (int j = tid; j < np; j += SE_THREADS) {
-        const int id = page_of(p, r.row, j);
-        uint32_t k = 0;
-        if (j < a.keep_first || j >= np - a.keep_last) k = 0xffffffffu;
-        else if (id >= 0) {
-            const int *s = reinterpret_cast<const int *>(summary_ptr(p, id, head));
-            int v = 0;
-            for (int c = 0; c < 2 * D / 4; c++) v = __dp4a(s[c], reinterpret_cast<const int *>(qi)[c], v);
-            const int e = s[2 * D / 4];
-            k = order_key(static_cast<float>(v) * pow2i(e < -100 ? -100 : (e > 100 ? 100 : e)) + 0.f);
+    if (ctas > 1) cluster_sync_all();  // the first CTA is there
+    // a page's summary is D / 8 lanes' 16 bytes; each warp has 4 x 32 / (D / 8) pages on their way
+    constexpr int LANES = D / 8, PER = 32 / LANES, DEEP = 4;
+    const int part = lane % LANES, sub = lane / LANES;
+    const int4 q = *reinterpret_cast<const int4 *>(qi + 16 * part);
+    const int j0 = static_cast<int>(static_cast<long long>(np) * rank / ctas), j1 = static_cast<int>(static_cast<long long>(np) * (rank + 1) / ctas);
+    const uint32_t keys = smem_u32(key);
+    for (int jw = j0 + warp * PER * DEEP; jw < j1; jw += SE_WARPS * PER * DEEP) {
+        int id[DEEP];
+        int4 s[DEEP];
+        int e[DEEP];
+#pragma unroll
+        for (int k = 0; k < DEEP; k++) {
+            const int j = jw + k * PER + sub;
+            id[k] = j < j1 ? page_of(p, r.row, j) : -1;
         }
-        key[j] = k;
+#pragma unroll
+        for (int k = 0; k < DEEP; k++) {
+            s[k] = make_int4(0, 0, 0, 0);
+            e[k] = 0;
+            if (id[k] < 0) continue;
+            const uint8_t *sum = summary_ptr(p, id[k], head);
+            s[k] = *reinterpret_cast<const int4 *>(sum + 16 * part);
+            e[k] = *reinterpret_cast<const int *>(sum + 2 * D);
+        }
+#pragma unroll
+        for (int k = 0; k < DEEP; k++) {
+            const int j = jw + k * PER + sub;
+            int v = __dp4a(s[k].x, q.x, __dp4a(s[k].y, q.y, __dp4a(s[k].z, q.z, __dp4a(s[k].w, q.w, 0))));
+#pragma unroll
+            for (int o = 1; o < LANES; o <<= 1) v += __shfl_xor_sync(FULL, v, o);
+            if (part != 0 || j >= j1) continue;
+            const int ex = e[k] < -100 ? -100 : (e[k] > 100 ? 100 : e[k]);
+            uint32_t o = id[k] < 0 ? 0u : order_key(static_cast<float>(v) * pow2i(ex));
+            if (j < a.keep_first || j >= np - a.keep_last) o = 0xffffffffu;
+            if (ctas == 1) key[j] = o;
+            else store_first(keys + 4 * j, o);
+        }
     }
-    if (tid == 0) base = 0;
+    if (ctas > 1) {
+        cluster_sync_all();
+        if (rank != 0) return;
+    } else {
+        __syncthreads();
+    }
+    // the n_sel-th largest key: `prefix` holds its digits so far, `want` its place among keys that share them
+    for (int shift = 24; shift >= 0; shift -= 8) {
+        if (tid < 256) hist[tid] = 0;
+        if (shift == 24 && tid == 0) {
+            prefix = 0;
+            want = a.n_sel;
+        }
+        __syncthreads();
+        const uint32_t pre = prefix;
+        const int w = want;
+        for (int j = tid; j < np; j += SE_THREADS) {
+            const uint32_t k = key[j];
+            if (shift == 24 || (k ^ pre) >> (shift + 8) == 0) atomicAdd(&hist[k >> shift & 255], 1);
+        }
+        __syncthreads();
+        if (warp == 0) {  // lane l: digits 255 - 8 l down to 248 - 8 l
+            int c[8], sum = 0;
+#pragma unroll
+            for (int i = 0; i < 8; i++) sum += c[i] = hist[255 - 8 * lane - i];
+            int before = sum;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int t = __shfl_up_sync(FULL, before, o);
+                if (lane >= o) before += t;
+            }
+            before -= sum;
+#pragma unroll
+            for (int i = 0; i < 8; i++) {
+                if (before < w && before + c[i] >= w) {
+                    prefix = pre | static_cast<uint32_t>(255 - 8 * lane - i) << shift;
+                    want = w - before;
+                }
+                before += c[i];
+            }
+        }
+        __syncthreads();
+    }
+    const uint32_t last = prefix;
+    const int take = want;  // of the keys equal to the last one, the first `take`
+    // a warp's pages are neighbours: [b0, b1)
+    const int b0 = static_cast<int>(static_cast<long long>(np) * warp / SE_WARPS), b1 = static_cast<int>(static_cast<long long>(np) * (warp + 1) / SE_WARPS);
+    int na = 0, ne = 0;
+    for (int j = b0; j < b1; j += 32) {
+        const uint32_t k = j + lane < b1 ? key[j + lane] : 0;
+        na += __popc(__ballot_sync(FULL, j + lane < b1 && k > last));
+        ne += __popc(__ballot_sync(FULL, j + lane < b1 && k == last));
+    }
+    if (lane == 0) {
+        above[warp] = na;
+        equal[warp] = ne;
+    }
     __syncthreads();
-    for (int j0 = 0; j0 < np; j0 += SE_THREADS) {
-        const int j = j0 + tid;
-        int take = 0;
-        if (j < np) {
-            int rank = 0;
-            for (int i = 0; i < np; i++) rank += key[i] > key[j] || (key[i] == key[j] && i < j);
-            take = rank < a.n_sel;
-        }
-        const unsigned b = __ballot_sync(FULL, take);
-        if ((tid & 31) == 0) wsum[tid >> 5] = __popc(b);
-        __syncthreads();
-        int at = base + __popc(b & ((1u << (tid & 31)) - 1u));
-        for (int i = 0; i < tid >> 5; i++) at += wsum[i];
-        if (take) out[at] = j;
-        __syncthreads();
-        if (tid == SE_THREADS - 1) base = at + take;
-        __syncthreads();
+    na = ne = 0;
+    for (int w = 0; w < warp; w++) {
+        na += above[w];
+        ne += equal[w];
     }
+    const unsigned below = (1u << lane) - 1u;
+    for (int j = b0; j < b1; j += 32) {
+        const bool in = j + lane < b1;
+        const uint32_t k = in ? key[j + lane] : 0;
+        const unsigned ma = __ballot_sync(FULL, in && k > last), me = __ballot_sync(FULL, in && k == last);
+        const int before_a = na + __popc(ma & below), before_e = ne + __popc(me & below);
+        const bool mine = (ma >> lane & 1u) || ((me >> lane & 1u) && before_e < take);
+        if (mine) out[before_a + (before_e < take ? before_e : take)] = j + lane;
+        na += __popc(ma);
+        ne += __popc(me);
+    }
+}
+
+template <int D>
+int launch_as(const PagesSelectArgs &a, int ctas, cudaStream_t st) {
+    const int smem = a.p.M * 4;
+    cudaError_t e = cudaFuncSetAttribute(select_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return static_cast<int>(e);
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(a.r.n_rows * ctas, a.p.Hkv);
+    cfg.blockDim = dim3(SE_THREADS);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute at{};
+    at.id = cudaLaunchAttributeClusterDimension;
+    at.val.clusterDim.x = ctas;
+    at.val.clusterDim.y = at.val.clusterDim.z = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, select_kernel<D>, a);
+    return static_cast<int>(e != cudaSuccess ? e : cudaGetLastError());
 }
 
 }  // namespace
 
-int launch_pages_select(const PagesSelectArgs &a, void *stream) {
-    const dim3 grid(a.r.n_rows, a.p.Hkv);
-    const int smem = a.p.M * 4;
-    auto st = static_cast<cudaStream_t>(stream);
-    cudaError_t e;
-    if (a.p.d == 128) {
-        if ((e = cudaFuncSetAttribute(select_kernel<128>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) == cudaSuccess)
-            select_kernel<128><<<grid, SE_THREADS, smem, st>>>(a);
-    } else {
-        if ((e = cudaFuncSetAttribute(select_kernel<64>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) == cudaSuccess)
-            select_kernel<64><<<grid, SE_THREADS, smem, st>>>(a);
-    }
-    return static_cast<int>(e != cudaSuccess ? e : cudaGetLastError());
+int launch_pages_select(const PagesSelectArgs &a, int num_sms, void *stream) {
+    // clusters while the card has room for them and a CTA keeps 128 pages (of a full table)
+    int ctas = 1;
+    while (ctas < 8 && a.r.n_rows * a.p.Hkv * ctas * 2 <= 2 * num_sms && a.p.M / (ctas * 2) >= 128) ctas *= 2;
+    return a.p.d == 128 ? launch_as<128>(a, ctas, static_cast<cudaStream_t>(stream)) : launch_as<64>(a, ctas, static_cast<cudaStream_t>(stream));
 }
 
 }  // namespace dq
