@@ -1,9 +1,16 @@
 // Paged cache: new tokens into pages (append) and back to 16 bits (read).
 //
 // A scale block is 16 channels of one token: top = max|x|, s = e4m3(top / 6 / 2^exp),
-// codes e2m1(x / (2^exp s)).  The quotient is IEEE-rounded: for 16-bit x no quotient
-// lies within half an fp32 step of a rounding border without being on it, so that
-// the codes are those of exact arithmetic.
+// codes e2m1(x / (2^exp s)).  The quotient is taken as x r, r = 1 / (2^exp s) rounded,
+// and put on a grid of 2^-16 by adding and subtracting 192: x has at most 11
+// significant bits and a border between two codes, times the scale, at most 7, so
+// that a quotient off a border is off by 2^-13 or more, while x r is off by less than
+// 2^-21.  What the grid gives therefore lies on a border where the quotient does and
+// on its side where it does not, and the codes are those of exact arithmetic.
+//
+// Both kernels are bound by moving 16-bit values once; the arithmetic (about 8
+// instructions for a value on its way in, 4 on its way out) nearly fills the issue slots
+// beside that.
 #include <cuda_runtime.h>
 
 #include "pages.cuh"
@@ -11,116 +18,247 @@
 namespace dq {
 namespace {
 
-constexpr int ST_THREADS = 128;
+constexpr int ST_THREADS = 128, ST_WARPS = ST_THREADS / 32;
 
-// 16 values at x (a block of one token) -> 8 bytes of code pairs (channel order) and
-// the scale.  Returns false if a value is not finite.
-__device__ __forceinline__ bool quantise16(const uint16_t *x, bool bf16, float inv_unit, float unit, uint32_t (&code)[2],
-                                           uint8_t &scale) {
-    const uint4 a = *reinterpret_cast<const uint4 *>(x), b = *reinterpret_cast<const uint4 *>(x + 8);
-    const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-    float f[16], top = 0.f, nan = 0.f;
-#pragma unroll
-    for (int i = 0; i < 8; i++) {
-        f[2 * i] = from16(static_cast<uint16_t>(w[i] & 0xffffu), bf16);
-        f[2 * i + 1] = from16(static_cast<uint16_t>(w[i] >> 16), bf16);
-    }
-#pragma unroll
-    for (int i = 0; i < 16; i++) {
-        top = fmaxf(top, fabsf(f[i]));
-        nan += f[i] * 0.f;
-    }
-    float S;
-    scale = block_scale(top, inv_unit, unit, S);
-    code[0] = code[1] = 0;
-    if (S > 0.f) {
-#pragma unroll
-        for (int i = 0; i < 8; i++)
-            code[i >> 2] |= float2_to_e2m1(__fdiv_rn(f[2 * i], S), __fdiv_rn(f[2 * i + 1], S)) << (8 * (i & 3));
-    } else {  // every code 0, signs kept
-#pragma unroll
-        for (int i = 0; i < 16; i++) code[i >> 3] |= (__float_as_uint(f[i]) >> 31) << (4 * (i & 7) + 3);
-    }
-    return nan == 0.f;
+__device__ __forceinline__ uint32_t max2_nan(uint32_t a, uint32_t b, bool bf16) {
+    uint32_t r;
+    if (bf16) asm("max.NaN.bf16x2 %0, %1, %2;\n" : "=r"(r) : "r"(a), "r"(b));
+    else asm("max.NaN.f16x2 %0, %1, %2;\n" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+__device__ __forceinline__ uint32_t hmax2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("max.f16x2 %0, %1, %2;\n" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+__device__ __forceinline__ uint32_t hmin2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("min.f16x2 %0, %1, %2;\n" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("mul.rn.f16x2 %0, %1, %2;\n" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+__device__ __forceinline__ float2 pair_to_float(uint32_t w, bool bf16) {
+    if (bf16) return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+    return __half22float2(*reinterpret_cast<const __half2 *>(&w));
 }
 
-// One CTA per (row, touched page, KV head): the page's bytes come to shared memory,
-// the new tokens' codes go in, the summary is taken over all tokens, and the bytes go
-// back.  The page is one row's alone, so no other CTA writes it.
-template <int D>
+// 16 channels of one token.
+struct Block16 {
+    uint32_t w[8];  // the values, two a word
+    __device__ __forceinline__ void load(const uint16_t *x) {
+        const uint4 a = *reinterpret_cast<const uint4 *>(x), b = *reinterpret_cast<const uint4 *>(x + 8);
+        w[0] = a.x; w[1] = a.y; w[2] = a.z; w[3] = a.w;
+        w[4] = b.x; w[5] = b.y; w[6] = b.z; w[7] = b.w;
+    }
+    __device__ __forceinline__ void clear() {
+#pragma unroll
+        for (int i = 0; i < 8; i++) w[i] = 0;
+    }
+    // The scale's byte, and the reciprocal that turns values into codes (0 for a scale of 0).
+    // `fine` is cleared where a value is not finite; the scale is then the largest one.
+    __device__ __forceinline__ uint8_t scale(bool bf16, float inv_unit, float unit, float &r, bool &fine) const {
+        uint32_t m = w[0] & 0x7fff7fffu;
+#pragma unroll
+        for (int i = 1; i < 8; i++) m = max2_nan(m, w[i] & 0x7fff7fffu, bf16);
+        const uint32_t lo = m & 0xffffu, hi = m >> 16, inf = bf16 ? 0x7f80u : 0x7c00u;
+        uint32_t top = lo > hi ? lo : hi;  // magnitudes order like their bits
+        if (top >= inf) {
+            top = inf;
+            fine = false;
+        }
+        float S;
+        const uint8_t s = block_scale(from16(static_cast<uint16_t>(top), bf16), inv_unit, unit, S);
+        r = S > 0.f ? __frcp_rn(S) : 0.f;
+        return s;
+    }
+};
+__device__ __forceinline__ float on_grid(float x, float r) {
+    const float q = fmaf(x, r, 192.f) - 192.f;
+    return __uint_as_float((__float_as_uint(q) & 0x7fffffffu) | (__float_as_uint(x) & 0x80000000u));  // tiny ones keep their sign
+}
+
+// One CTA per (row, touched page, KV head).  A block of B = min(P, 64) tokens at a time
+// is put together in shared memory in the page's layout.  What a page holds already is
+// read only where it is needed: its keys for the summary, and the groups of 8 tokens
+// that the new ones share with others.  The page is one row's alone, so that no other
+// CTA writes it.
+template <int D, int B>
 __global__ void __launch_bounds__(ST_THREADS) append_kernel(PagesStoreArgs a) {
-    extern __shared__ __align__(16) uint8_t img[];
-    __shared__ float red[ST_THREADS / 32];
+    using L = PageBlock<D>;
+    constexpr int C = D / 16;                                     // scale blocks of a token
+    constexpr int KI = (B * C + ST_THREADS - 1) / ST_THREADS;     // (token, scale block) items of a thread
+    constexpr int VI = (B / 2 * C + ST_THREADS - 1) / ST_THREADS; // (token pair, scale block) items
+    __shared__ __align__(16) uint8_t img[L::size(B)];
+    __shared__ float top_s[ST_WARPS][D], low_s[ST_WARPS][D], red[ST_WARPS];
     const PagesView &p = a.p;
     const PageRow r = page_row(p, a.r, blockIdx.y);
-    const int head = blockIdx.z, tid = threadIdx.x;
+    const int head = blockIdx.z, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int lo = r.len - r.n < 0 ? 0 : r.len - r.n;  // first position written
     const int j = lo / p.P + blockIdx.x;
     if (r.row < 0 || r.n == 0 || j * p.P >= r.len) return;
     const int id = page_of(p, r.row, j);
     if (id < 0) return;
-    if (p.refs[id] != 1) {
+    const int t0 = lo > j * p.P ? lo - j * p.P : 0;  // new tokens of the page: [t0, t1)
+    const int t1 = r.len - j * p.P < p.P ? r.len - j * p.P : p.P;
+    const bool shared = p.refs[id] != 1;
+    if (shared) {
         if (tid == 0) atomicOr(p.status, PST_SHARED);
         return;
     }
-    using B = PageBlock<D>;
-    uint4 *page = reinterpret_cast<uint4 *>(page_ptr(p, id, head));
-    for (int i = tid; i < p.page_bytes / 16; i += ST_THREADS) reinterpret_cast<uint4 *>(img)[i] = page[i];
-    __syncthreads();
-    const int t0 = lo > j * p.P ? lo - j * p.P : 0;                        // new tokens of the page: [t0, t1)
-    const int t1 = r.len - j * p.P < p.P ? r.len - j * p.P : p.P;
-    const long long first = r.q0 + (static_cast<long long>(j) * p.P - (r.len - r.n));  // the call's token at t = 0
+    // the call's token at t = 0, k and v of this head there
+    const long long first = r.q0 + (static_cast<long long>(j) * p.P - (r.len - r.n));
+    const uint16_t *kp = a.k + first * a.kt + head * a.kh, *vp = a.v + first * a.vt + head * a.vh;
     const float ku = pow2i(p.k_exp), ki = pow2i(-p.k_exp), vu = pow2i(p.v_exp), vi = pow2i(-p.v_exp);
+    const bool bf16 = p.bf16;
     bool fine = true;
-    // keys: a thread takes a (token, scale block)
-    for (int i = tid; i < (t1 - t0) * (D / 16); i += ST_THREADS) {
-        const int t = t0 + i / (D / 16), c = i % (D / 16);
-        uint8_t *blk = img + (t / p.blk) * B::size(p.blk);
-        uint32_t code[2];
-        uint8_t s;
-        fine &= quantise16(a.k + (first + t) * a.kt + head * a.kh + 16 * c, p.bf16, ki, ku, code, s);
-        *reinterpret_cast<uint2 *>(blk + (t % p.blk) * (D / 2) + 8 * c) = make_uint2(code[0], code[1]);
-        blk[B::ks(p.blk) + (t % p.blk) * (D / 16) + c] = s;
+    // summary: this thread's 8 channels over every (128 / (D / 8))-th token
+    const int col = tid % (D / 8);
+    uint32_t top[4], low[4];
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+        top[i] = 0xfc00fc00u;
+        low[i] = 0x7c007c00u;
     }
-    // values: a thread takes a (token pair, scale block) and puts the new tokens' halves in
-    for (int i = tid; i < ((t1 + 1) / 2 - t0 / 2) * (D / 16); i += ST_THREADS) {
-        const int t = 2 * (t0 / 2 + i / (D / 16)), c = i % (D / 16);
-        uint8_t *blk = img + (t / p.blk) * B::size(p.blk);
-        uint8_t *cp = blk + B::vc(p.blk) + B::vcode(t % p.blk, c), *sp = blk + B::vs(p.blk) + B::vscale(t % p.blk, c);
-        for (int e = 0; e < 2; e++) {
-            if (t + e < t0 || t + e >= t1) continue;
-            uint32_t code[2];
-            uint8_t s;
-            fine &= quantise16(a.v + (first + t + e) * a.vt + head * a.vh + 16 * c, p.bf16, vi, vu, code, s);
-            sp[e] = s;
-            for (int ch = 0; ch < 16; ch++) {
-                const uint32_t m = (code[ch >> 3] >> (4 * (ch & 7))) & 15u;
-                cp[ch] = static_cast<uint8_t>(e ? ((cp[ch] & 0x0fu) | (m << 4)) : ((cp[ch] & 0xf0u) | m));
+    for (int b0 = 0; b0 < t1; b0 += B) {  // the page's blocks
+        uint8_t *blk = page_ptr(p, id, head) + b0 / B * L::size(B);
+        const int n0 = t0 > b0 ? t0 - b0 : 0, n1 = t1 - b0 < B ? t1 - b0 : B;  // the block's new tokens, if n0 < n1
+        const bool some = n0 < n1;
+        Block16 kx[KI], vx[VI][2];
+        if (some) {  // the new tokens are on their way first
+#pragma unroll
+            for (int i = 0; i < KI; i++) {
+                const int u = tid + i * ST_THREADS, t = n0 + u / C;
+                if (t < n1) kx[i].load(kp + (b0 + t) * a.kt + 16 * (u % C));
+            }
+#pragma unroll
+            for (int i = 0; i < VI; i++) {
+                const int u = tid + i * ST_THREADS, t = (n0 & ~1) + 2 * (u / C);
+#pragma unroll
+                for (int e = 0; e < 2; e++)
+                    if (t + e >= n0 && t + e < n1) vx[i][e].load(vp + (b0 + t + e) * a.vt + 16 * (u % C));
+                    else vx[i][e].clear();
+            }
+        }
+        const int g0 = some ? n0 / 8 : B / 8, g1 = (n1 + 7) / 8;  // 8-token groups written: [g0, g1)
+        if (b0) __syncthreads();
+        if (!some || n0 > 0 || (n1 & 7)) {  // old keys, for the summary and beside new ones in a group
+            for (int i = tid; i < g1 * (D / 4); i += ST_THREADS) reinterpret_cast<uint4 *>(img)[i] = reinterpret_cast<const uint4 *>(blk)[i];
+            for (int i = tid; i < g1 * (D / 32); i += ST_THREADS)
+                reinterpret_cast<uint4 *>(img + L::ks(B))[i] = reinterpret_cast<const uint4 *>(blk + L::ks(B))[i];
+        }
+        for (int g = g0; g < g1; g++) {  // old values beside new ones in a group
+            if (8 * g >= n0 && 8 * g + 8 <= n1) continue;
+            for (int i = tid; i < D / 4 + D / 32; i += ST_THREADS) {
+                const int at = i < D / 4 ? L::vc(B) + g * 4 * D + 16 * i : L::vs(B) + g * (D / 2) + 16 * (i - D / 4);
+                *reinterpret_cast<uint4 *>(img + at) = *reinterpret_cast<const uint4 *>(blk + at);
+            }
+        }
+        __syncthreads();
+        if (some) {
+#pragma unroll
+            for (int i = 0; i < KI; i++) {
+                const int u = tid + i * ST_THREADS, t = n0 + u / C, c = u % C;
+                if (t >= n1) break;
+                float rc;
+                img[L::ks(B) + t * C + c] = kx[i].scale(bf16, ki, ku, rc, fine);
+                uint32_t code[2] = {0, 0};
+#pragma unroll
+                for (int k = 0; k < 8; k++) {
+                    const float2 x = pair_to_float(kx[i].w[k], bf16);
+                    code[k >> 2] |= float2_to_e2m1(on_grid(x.x, rc), on_grid(x.y, rc)) << (8 * (k & 3));
+                }
+                *reinterpret_cast<uint2 *>(img + t * (D / 2) + 8 * c) = make_uint2(code[0], code[1]);
+            }
+#pragma unroll
+            for (int i = 0; i < VI; i++) {
+                const int u = tid + i * ST_THREADS, t = (n0 & ~1) + 2 * (u / C), c = u % C;
+                if (t >= n1) break;
+                const bool e0 = t >= n0, e1 = t + 1 < n1;
+                float r0 = 0.f, r1 = 0.f;
+                uint8_t *cp = img + L::vc(B) + L::vcode(t, c), *sp = img + L::vs(B) + L::vscale(t, c);
+                if (e0) sp[0] = vx[i][0].scale(bf16, vi, vu, r0, fine);
+                if (e1) sp[1] = vx[i][1].scale(bf16, vi, vu, r1, fine);
+                uint32_t code[4] = {0, 0, 0, 0};  // a byte is a channel: even token low, odd token high
+#pragma unroll
+                for (int k = 0; k < 8; k++) {
+                    const float2 x = pair_to_float(vx[i][0].w[k], bf16), y = pair_to_float(vx[i][1].w[k], bf16);
+                    code[k >> 1] |= (float2_to_e2m1(on_grid(x.x, r0), on_grid(y.x, r1)) | float2_to_e2m1(on_grid(x.y, r0), on_grid(y.y, r1)) << 8)
+                                    << (16 * (k & 1));
+                }
+                uint4 *dst = reinterpret_cast<uint4 *>(cp);
+                if (!e0 || !e1) {  // one of the two is new
+                    const uint32_t m = e0 ? 0x0f0f0f0fu : 0xf0f0f0f0u;
+                    const uint4 old = *dst;
+                    code[0] = (code[0] & m) | (old.x & ~m);
+                    code[1] = (code[1] & m) | (old.y & ~m);
+                    code[2] = (code[2] & m) | (old.z & ~m);
+                    code[3] = (code[3] & m) | (old.w & ~m);
+                }
+                *dst = make_uint4(code[0], code[1], code[2], code[3]);
+            }
+        }
+        __syncthreads();
+        // the groups with new tokens go back
+        const int n = g1 - g0;
+        for (int i = tid; i < n * (D / 4); i += ST_THREADS) {
+            const int at = g0 * 4 * D + 16 * i;
+            *reinterpret_cast<uint4 *>(blk + at) = *reinterpret_cast<const uint4 *>(img + at);
+            *reinterpret_cast<uint4 *>(blk + L::vc(B) + at) = *reinterpret_cast<const uint4 *>(img + L::vc(B) + at);
+        }
+        for (int i = tid; i < n * (D / 32); i += ST_THREADS) {
+            const int at = g0 * (D / 2) + 16 * i;
+            *reinterpret_cast<uint4 *>(blk + L::ks(B) + at) = *reinterpret_cast<const uint4 *>(img + L::ks(B) + at);
+            *reinterpret_cast<uint4 *>(blk + L::vs(B) + at) = *reinterpret_cast<const uint4 *>(img + L::vs(B) + at);
+        }
+        for (int t = tid / (D / 8); t < n1; t += ST_THREADS / (D / 8)) {
+            uint32_t h[4];
+            e2m1x8_to_half(*reinterpret_cast<const uint32_t *>(img + t * (D / 2) + 4 * col), h);
+            const uint32_t s = e4m3x2_to_half2(img[L::ks(B) + t * C + (col >> 1)]), s2 = __byte_perm(s, s, 0x1010);
+#pragma unroll
+            for (int i = 0; i < 4; i++) {
+                h[i] = hmul2(h[i], s2);  // exact
+                top[i] = hmax2(top[i], h[i]);
+                low[i] = hmin2(low[i], h[i]);
             }
         }
     }
     if (!fine) atomicOr(p.status, PST_NONFINITE);
-    __syncthreads();
-    for (int i = tid; i < p.page_bytes / 16; i += ST_THREADS) page[i] = reinterpret_cast<uint4 *>(img)[i];
-    // summary: thread c takes channel c over tokens [0, t1)
-    float mx = -INFINITY, mn = INFINITY;
-    if (tid < D) {
-        for (int t = 0; t < t1; t++) {
-            const uint8_t *blk = img + (t / p.blk) * B::size(p.blk);
-            const uint32_t byte = blk[(t % p.blk) * (D / 2) + (tid >> 1)];
-            const float x = e2m1_to_float((byte >> (4 * (tid & 1))) & 15u) *
-                            e4m3_to_float(blk[B::ks(p.blk) + (t % p.blk) * (D / 16) + (tid >> 4)]);
-            mx = fmaxf(mx, x);
-            mn = fminf(mn, x);
+    // the threads with the same channels: within the warp, then over the warps
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+#pragma unroll
+        for (int o = D / 8; o < 32; o <<= 1) {
+            top[i] = hmax2(top[i], __shfl_xor_sync(FULL, top[i], o));
+            low[i] = hmin2(low[i], __shfl_xor_sync(FULL, low[i], o));
+        }
+        if (lane < D / 8) {
+            const float2 h = __half22float2(*reinterpret_cast<const __half2 *>(&top[i])), l = __half22float2(*reinterpret_cast<const __half2 *>(&low[i]));
+            top_s[warp][8 * lane + 2 * i] = h.x;
+            top_s[warp][8 * lane + 2 * i + 1] = h.y;
+            low_s[warp][8 * lane + 2 * i] = l.x;
+            low_s[warp][8 * lane + 2 * i + 1] = l.y;
         }
     }
-    const float w = warp_max(tid < D ? fmaxf(fabsf(mx), fabsf(mn)) : 0.f);
-    if ((tid & 31) == 0) red[tid >> 5] = w;
     __syncthreads();
-    float top = red[0];
-    for (int i = 1; i < ST_THREADS / 32; i++) top = fmaxf(top, red[i]);
-    // held keys are multiples of 2^-10 below 2^12: top = m 2^E with E from the exponent field
-    const int e = top > 0.f ? static_cast<int>(__float_as_uint(top) >> 23) - 126 - 7 : 0;
+    float mx = -INFINITY, mn = INFINITY;
+    if (tid < D)
+#pragma unroll
+        for (int i = 0; i < ST_WARPS; i++) {
+            mx = fmaxf(mx, top_s[i][tid]);
+            mn = fminf(mn, low_s[i][tid]);
+        }
+    const float w = warp_max(tid < D ? fmaxf(fabsf(mx), fabsf(mn)) : 0.f);
+    if (lane == 0) red[warp] = w;
+    __syncthreads();
+    float most = red[0];
+#pragma unroll
+    for (int i = 1; i < ST_WARPS; i++) most = fmaxf(most, red[i]);
+    // held keys are multiples of 2^-10 below 2^12 of at most 6 bits: most = m 2^E, E from the exponent field
+    const int e = most > 0.f ? static_cast<int>(__float_as_uint(most) >> 23) - 126 - 7 : 0;
     uint8_t *sum = summary_ptr(p, id, head);
     if (tid < D) {
         const float unit = pow2i(-e);
@@ -130,46 +268,82 @@ __global__ void __launch_bounds__(ST_THREADS) append_kernel(PagesStoreArgs a) {
     if (tid == 0) *reinterpret_cast<int *>(sum + 2 * D) = e;
 }
 
-// One thread per (token, KV head, scale block).
+// Two half2 words of held values (in units of 2^exp) -> 16-bit words.
+__device__ __forceinline__ uint32_t held_to_16(uint32_t h, float unit, bool bf16) {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h));
+    uint32_t r;
+    if (bf16) asm("cvt.rn.bf16x2.f32 %0, %1, %2;\n" : "=r"(r) : "f"(f.y * unit), "f"(f.x * unit));
+    else asm("cvt.rn.f16x2.f32 %0, %1, %2;\n" : "=r"(r) : "f"(f.y * unit), "f"(f.x * unit));
+    return r;
+}
+
+// One thread per (pair of positions 2 i and 2 i + 1, KV head, 8 channels).
 template <int D>
 __global__ void __launch_bounds__(256) read_kernel(PagesReadArgs a) {
     const PagesView &p = a.p;
     const PageRow r = page_row(p, a.r, blockIdx.y);
-    const int per = p.Hkv * (D / 16);
     using B = PageBlock<D>;
-    for (long long i = blockIdx.x * 256LL + threadIdx.x; i < static_cast<long long>(r.n) * per; i += gridDim.x * 256LL) {
-        const int n = static_cast<int>(i / per), u = static_cast<int>(i % per), head = u / (D / 16), c = u % (D / 16);
-        const int pos = r.len - r.n + n;
-        uint16_t *ko = a.k + ((static_cast<long long>(r.q0) + n) * p.Hkv + head) * D + 16 * c;
-        uint16_t *vo = a.v + ((static_cast<long long>(r.q0) + n) * p.Hkv + head) * D + 16 * c;
-        const int id = pos >= 0 && r.row >= 0 ? page_of(p, r.row, pos / p.P) : -1;
-        float kx[16], vx[16];
+    constexpr int C8 = D / 8;
+    const int per = p.Hkv * C8, pos0 = r.len - r.n;  // the first token's position
+    const int pair0 = pos0 >> 1, pairs = r.n ? ((r.len - 1) >> 1) - pair0 + 1 : 0;
+    const float ku = pow2i(p.k_exp), vu = pow2i(p.v_exp);
+    const bool bf16 = p.bf16;
+    for (long long i = blockIdx.x * 256LL + threadIdx.x; i < static_cast<long long>(pairs) * per; i += gridDim.x * 256LL) {
+        const int pr = static_cast<int>(i / per), u = static_cast<int>(i) - pr * per, head = u / C8, c8 = u % C8;
+        const int pos = 2 * (pair0 + pr);
+        uint32_t k[2][4], v[2][4];
+        int id = -1;
+        if (pos >= 0 && r.row >= 0 && pos < r.len) id = page_of(p, r.row, pos / p.P);
+        if (id < 0) {
 #pragma unroll
-        for (int ch = 0; ch < 16; ch++) kx[ch] = vx[ch] = 0.f;
-        if (id >= 0) {
-            const int t = pos % p.P, tb = t % p.blk;
-            const uint8_t *blk = page_ptr(p, id, head) + (t / p.blk) * B::size(p.blk);
-            const float ks = e4m3_to_float(blk[B::ks(p.blk) + tb * (D / 16) + c]) * pow2i(p.k_exp);
-            const float vs = e4m3_to_float(blk[B::vs(p.blk) + B::vscale(tb, c)]) * pow2i(p.v_exp);
-            const uint8_t *kc = blk + tb * (D / 2) + 8 * c, *vc = blk + B::vc(p.blk) + B::vcode(tb, c);
+            for (int e = 0; e < 2; e++)
 #pragma unroll
-            for (int ch = 0; ch < 16; ch++) {
-                kx[ch] = e2m1_to_float((kc[ch >> 1] >> (4 * (ch & 1))) & 15u) * ks;
-                vx[ch] = e2m1_to_float((vc[ch] >> (4 * (t & 1))) & 15u) * vs;
+                for (int x = 0; x < 4; x++) k[e][x] = v[e][x] = 0;
+        } else {
+            const int t = pos % p.P, tb = t % p.blk, b = p.blk;
+            const uint8_t *blk = page_ptr(p, id, head) + (t / b) * B::size(b);
+            const uint32_t kw0 = *reinterpret_cast<const uint32_t *>(blk + tb * (D / 2) + 4 * c8);
+            const uint32_t kw1 = *reinterpret_cast<const uint32_t *>(blk + (tb + 1) * (D / 2) + 4 * c8);
+            const uint2 vw = *reinterpret_cast<const uint2 *>(blk + B::vc(b) + B::vcode(tb, c8 >> 1) + 8 * (c8 & 1));
+            const uint8_t *ks = blk + B::ks(b) + tb * (D / 16) + (c8 >> 1);
+            const uint16_t vs = *reinterpret_cast<const uint16_t *>(blk + B::vs(b) + B::vscale(tb, c8 >> 1));
+            const uint32_t s = e4m3x2_to_half2(static_cast<uint16_t>(ks[0] | ks[D / 16] << 8)), sv = e4m3x2_to_half2(vs);
+            uint32_t h0[4], h1[4], va[4], vb[4];
+            e2m1x8_to_half(kw0, h0);
+            e2m1x8_to_half(kw1, h1);
+            e2m1x8_to_half(vw.x, va);  // a half2 is the two tokens of a channel
+            e2m1x8_to_half(vw.y, vb);
+            const uint32_t s0 = __byte_perm(s, s, 0x1010), s1 = __byte_perm(s, s, 0x3232);
+#pragma unroll
+            for (int x = 0; x < 4; x++) {
+                k[0][x] = held_to_16(hmul2(h0[x], s0), ku, bf16);
+                k[1][x] = held_to_16(hmul2(h1[x], s1), ku, bf16);
+                va[x] = hmul2(va[x], sv);
+                vb[x] = hmul2(vb[x], sv);
+            }
+#pragma unroll
+            for (int x = 0; x < 2; x++) {
+                v[0][x] = held_to_16(__byte_perm(va[2 * x], va[2 * x + 1], 0x5410), vu, bf16);
+                v[1][x] = held_to_16(__byte_perm(va[2 * x], va[2 * x + 1], 0x7632), vu, bf16);
+                v[0][x + 2] = held_to_16(__byte_perm(vb[2 * x], vb[2 * x + 1], 0x5410), vu, bf16);
+                v[1][x + 2] = held_to_16(__byte_perm(vb[2 * x], vb[2 * x + 1], 0x7632), vu, bf16);
             }
         }
 #pragma unroll
-        for (int h = 0; h < 2; h++) {
-            uint32_t kw[4], vw[4];
-#pragma unroll
-            for (int i4 = 0; i4 < 4; i4++) {
-                kw[i4] = pack2(to16(kx[8 * h + 2 * i4], p.bf16), to16(kx[8 * h + 2 * i4 + 1], p.bf16));
-                vw[i4] = pack2(to16(vx[8 * h + 2 * i4], p.bf16), to16(vx[8 * h + 2 * i4 + 1], p.bf16));
-            }
-            reinterpret_cast<uint4 *>(ko)[h] = make_uint4(kw[0], kw[1], kw[2], kw[3]);
-            reinterpret_cast<uint4 *>(vo)[h] = make_uint4(vw[0], vw[1], vw[2], vw[3]);
+        for (int e = 0; e < 2; e++) {
+            if (pos + e < pos0 || pos + e >= r.len) continue;
+            const long long o = ((static_cast<long long>(r.q0) + pos + e - pos0) * p.Hkv + head) * D + 8 * c8;
+            *reinterpret_cast<uint4 *>(a.k + o) = make_uint4(k[e][0], k[e][1], k[e][2], k[e][3]);
+            *reinterpret_cast<uint4 *>(a.v + o) = make_uint4(v[e][0], v[e][1], v[e][2], v[e][3]);
         }
     }
+}
+
+template <int D>
+void append_as(const PagesStoreArgs &a, dim3 grid, cudaStream_t st) {
+    if (a.p.blk == 64) append_kernel<D, 64><<<grid, ST_THREADS, 0, st>>>(a);
+    else if (a.p.blk == 32) append_kernel<D, 32><<<grid, ST_THREADS, 0, st>>>(a);
+    else append_kernel<D, 16><<<grid, ST_THREADS, 0, st>>>(a);
 }
 
 }  // namespace
@@ -179,13 +353,13 @@ int launch_pages_append(const PagesStoreArgs &a, void *stream) {
     const int most = (a.r.max_new + a.p.P - 2) / a.p.P + 1;
     const dim3 grid(most < a.p.M ? most : a.p.M, a.r.n_rows, a.p.Hkv);
     auto st = static_cast<cudaStream_t>(stream);
-    if (a.p.d == 128) append_kernel<128><<<grid, ST_THREADS, a.p.page_bytes, st>>>(a);
-    else append_kernel<64><<<grid, ST_THREADS, a.p.page_bytes, st>>>(a);
+    if (a.p.d == 128) append_as<128>(a, grid, st);
+    else append_as<64>(a, grid, st);
     return static_cast<int>(cudaGetLastError());
 }
 
 int launch_pages_read(const PagesReadArgs &a, void *stream) {
-    const long long per = static_cast<long long>(a.r.max_new) * a.p.Hkv * (a.p.d / 16);
+    const long long per = static_cast<long long>(a.r.max_new / 2 + 1) * a.p.Hkv * (a.p.d / 8);
     const long long want = (per + 255) / 256;
     const dim3 grid(static_cast<unsigned>(want < 4096 ? want : 4096), a.r.n_rows);
     auto st = static_cast<cudaStream_t>(stream);
