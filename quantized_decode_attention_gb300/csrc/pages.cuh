@@ -110,10 +110,15 @@ __device__ __forceinline__ uint8_t float_to_e4m3(float x) {
     asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;\n" : "=h"(r) : "f"(0.f), "f"(x));
     return static_cast<uint8_t>(r & 0xff);
 }
-// Codes of two values: x0 in the low half of the byte.
-__device__ __forceinline__ uint32_t float2_to_e2m1(float x0, float x1) {
+// Codes of eight values, the first in the lowest four bits.
+__device__ __forceinline__ uint32_t float8_to_e2m1(float x0, float x1, float x2, float x3, float x4, float x5, float x6, float x7) {
     uint32_t r;
-    asm("{\n .reg .b8 t;\n cvt.rn.satfinite.e2m1x2.f32 t, %1, %2;\n cvt.u32.u8 %0, t;\n}\n" : "=r"(r) : "f"(x1), "f"(x0));
+    asm("{\n .reg .b8 a, b, c, d;\n"
+        " cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n"
+        " cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n"
+        " mov.b32 %0, {a, b, c, d};\n}\n"
+        : "=r"(r)
+        : "f"(x0), "f"(x1), "f"(x2), "f"(x3), "f"(x4), "f"(x5), "f"(x6), "f"(x7));
     return r;
 }
 

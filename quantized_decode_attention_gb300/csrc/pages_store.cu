@@ -20,9 +20,10 @@ namespace {
 
 constexpr int ST_THREADS = 128, ST_WARPS = ST_THREADS / 32;
 
-__device__ __forceinline__ uint32_t max2_nan(uint32_t a, uint32_t b, bool bf16) {
+template <bool BF16>
+__device__ __forceinline__ uint32_t max2_nan(uint32_t a, uint32_t b) {
     uint32_t r;
-    if (bf16) asm("max.NaN.bf16x2 %0, %1, %2;\n" : "=r"(r) : "r"(a), "r"(b));
+    if (BF16) asm("max.NaN.bf16x2 %0, %1, %2;\n" : "=r"(r) : "r"(a), "r"(b));
     else asm("max.NaN.f16x2 %0, %1, %2;\n" : "=r"(r) : "r"(a), "r"(b));
     return r;
 }
@@ -41,8 +42,9 @@ __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
     asm("mul.rn.f16x2 %0, %1, %2;\n" : "=r"(r) : "r"(a), "r"(b));
     return r;
 }
-__device__ __forceinline__ float2 pair_to_float(uint32_t w, bool bf16) {
-    if (bf16) return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+template <bool BF16>
+__device__ __forceinline__ float2 pair_to_float(uint32_t w) {
+    if (BF16) return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
     return __half22float2(*reinterpret_cast<const __half2 *>(&w));
 }
 
@@ -60,18 +62,19 @@ struct Block16 {
     }
     // The scale's byte, and the reciprocal that turns values into codes (0 for a scale of 0).
     // `fine` is cleared where a value is not finite; the scale is then the largest one.
-    __device__ __forceinline__ uint8_t scale(bool bf16, float inv_unit, float unit, float &r, bool &fine) const {
+    template <bool BF16>
+    __device__ __forceinline__ uint8_t scale(float inv_unit, float unit, float &r, bool &fine) const {
         uint32_t m = w[0] & 0x7fff7fffu;
 #pragma unroll
-        for (int i = 1; i < 8; i++) m = max2_nan(m, w[i] & 0x7fff7fffu, bf16);
-        const uint32_t lo = m & 0xffffu, hi = m >> 16, inf = bf16 ? 0x7f80u : 0x7c00u;
+        for (int i = 1; i < 8; i++) m = max2_nan<BF16>(m, w[i] & 0x7fff7fffu);
+        const uint32_t lo = m & 0xffffu, hi = m >> 16, inf = BF16 ? 0x7f80u : 0x7c00u;
         uint32_t top = lo > hi ? lo : hi;  // magnitudes order like their bits
         if (top >= inf) {
             top = inf;
             fine = false;
         }
         float S;
-        const uint8_t s = block_scale(from16(static_cast<uint16_t>(top), bf16), inv_unit, unit, S);
+        const uint8_t s = block_scale(from16(static_cast<uint16_t>(top), BF16), inv_unit, unit, S);
         r = S > 0.f ? __frcp_rn(S) : 0.f;
         return s;
     }
@@ -86,7 +89,7 @@ __device__ __forceinline__ float on_grid(float x, float r) {
 // read only where it is needed: its keys for the summary, and the groups of 8 tokens
 // that the new ones share with others.  The page is one row's alone, so that no other
 // CTA writes it.
-template <int D, int B>
+template <int D, int B, bool BF16>
 __global__ void __launch_bounds__(ST_THREADS) append_kernel(PagesStoreArgs a) {
     using L = PageBlock<D>;
     constexpr int C = D / 16;                                     // scale blocks of a token
@@ -113,7 +116,6 @@ __global__ void __launch_bounds__(ST_THREADS) append_kernel(PagesStoreArgs a) {
     const long long first = r.q0 + (static_cast<long long>(j) * p.P - (r.len - r.n));
     const uint16_t *kp = a.k + first * a.kt + head * a.kh, *vp = a.v + first * a.vt + head * a.vh;
     const float ku = pow2i(p.k_exp), ki = pow2i(-p.k_exp), vu = pow2i(p.v_exp), vi = pow2i(-p.v_exp);
-    const bool bf16 = p.bf16;
     bool fine = true;
     // summary: this thread's 8 channels over every (128 / (D / 8))-th token
     const int col = tid % (D / 8);
@@ -164,12 +166,18 @@ __global__ void __launch_bounds__(ST_THREADS) append_kernel(PagesStoreArgs a) {
                 const int u = tid + i * ST_THREADS, t = n0 + u / C, c = u % C;
                 if (t >= n1) break;
                 float rc;
-                img[L::ks(B) + t * C + c] = kx[i].scale(bf16, ki, ku, rc, fine);
-                uint32_t code[2] = {0, 0};
+                img[L::ks(B) + t * C + c] = kx[i].template scale<BF16>(ki, ku, rc, fine);
+                uint32_t code[2];
 #pragma unroll
-                for (int k = 0; k < 8; k++) {
-                    const float2 x = pair_to_float(kx[i].w[k], bf16);
-                    code[k >> 2] |= float2_to_e2m1(on_grid(x.x, rc), on_grid(x.y, rc)) << (8 * (k & 3));
+                for (int k = 0; k < 2; k++) {
+                    float x[8];
+#pragma unroll
+                    for (int e = 0; e < 4; e++) {
+                        const float2 f = pair_to_float<BF16>(kx[i].w[4 * k + e]);
+                        x[2 * e] = on_grid(f.x, rc);
+                        x[2 * e + 1] = on_grid(f.y, rc);
+                    }
+                    code[k] = float8_to_e2m1(x[0], x[1], x[2], x[3], x[4], x[5], x[6], x[7]);
                 }
                 *reinterpret_cast<uint2 *>(img + t * (D / 2) + 8 * c) = make_uint2(code[0], code[1]);
             }
@@ -180,14 +188,15 @@ __global__ void __launch_bounds__(ST_THREADS) append_kernel(PagesStoreArgs a) {
                 const bool e0 = t >= n0, e1 = t + 1 < n1;
                 float r0 = 0.f, r1 = 0.f;
                 uint8_t *cp = img + L::vc(B) + L::vcode(t, c), *sp = img + L::vs(B) + L::vscale(t, c);
-                if (e0) sp[0] = vx[i][0].scale(bf16, vi, vu, r0, fine);
-                if (e1) sp[1] = vx[i][1].scale(bf16, vi, vu, r1, fine);
-                uint32_t code[4] = {0, 0, 0, 0};  // a byte is a channel: even token low, odd token high
+                if (e0) sp[0] = vx[i][0].template scale<BF16>(vi, vu, r0, fine);
+                if (e1) sp[1] = vx[i][1].template scale<BF16>(vi, vu, r1, fine);
+                uint32_t code[4];  // a byte is a channel: even token low, odd token high
 #pragma unroll
-                for (int k = 0; k < 8; k++) {
-                    const float2 x = pair_to_float(vx[i][0].w[k], bf16), y = pair_to_float(vx[i][1].w[k], bf16);
-                    code[k >> 1] |= (float2_to_e2m1(on_grid(x.x, r0), on_grid(y.x, r1)) | float2_to_e2m1(on_grid(x.y, r0), on_grid(y.y, r1)) << 8)
-                                    << (16 * (k & 1));
+                for (int k = 0; k < 4; k++) {
+                    const float2 x = pair_to_float<BF16>(vx[i][0].w[2 * k]), y = pair_to_float<BF16>(vx[i][1].w[2 * k]);
+                    const float2 z = pair_to_float<BF16>(vx[i][0].w[2 * k + 1]), w = pair_to_float<BF16>(vx[i][1].w[2 * k + 1]);
+                    code[k] = float8_to_e2m1(on_grid(x.x, r0), on_grid(y.x, r1), on_grid(x.y, r0), on_grid(y.y, r1), on_grid(z.x, r0),
+                                             on_grid(w.x, r1), on_grid(z.y, r0), on_grid(w.y, r1));
                 }
                 uint4 *dst = reinterpret_cast<uint4 *>(cp);
                 if (!e0 || !e1) {  // one of the two is new
@@ -268,82 +277,113 @@ __global__ void __launch_bounds__(ST_THREADS) append_kernel(PagesStoreArgs a) {
     if (tid == 0) *reinterpret_cast<int *>(sum + 2 * D) = e;
 }
 
-// Two half2 words of held values (in units of 2^exp) -> 16-bit words.
-__device__ __forceinline__ uint32_t held_to_16(uint32_t h, float unit, bool bf16) {
+// A half2 of held values (in units of 2^exp) -> 16-bit words.
+template <bool BF16>
+__device__ __forceinline__ uint32_t held_to_16(uint32_t h, float unit) {
     const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h));
     uint32_t r;
-    if (bf16) asm("cvt.rn.bf16x2.f32 %0, %1, %2;\n" : "=r"(r) : "f"(f.y * unit), "f"(f.x * unit));
+    if (BF16) asm("cvt.rn.bf16x2.f32 %0, %1, %2;\n" : "=r"(r) : "f"(f.y * unit), "f"(f.x * unit));
     else asm("cvt.rn.f16x2.f32 %0, %1, %2;\n" : "=r"(r) : "f"(f.y * unit), "f"(f.x * unit));
     return r;
 }
 
-// One thread per (pair of positions 2 i and 2 i + 1, KV head, 8 channels).
-template <int D>
+// One thread per (group of 8 positions, KV head, 8 channels): a group is in one page.
+template <int D, bool BF16>
 __global__ void __launch_bounds__(256) read_kernel(PagesReadArgs a) {
     const PagesView &p = a.p;
     const PageRow r = page_row(p, a.r, blockIdx.y);
     using B = PageBlock<D>;
     constexpr int C8 = D / 8;
-    const int per = p.Hkv * C8, pos0 = r.len - r.n;  // the first token's position
-    const int pair0 = pos0 >> 1, pairs = r.n ? ((r.len - 1) >> 1) - pair0 + 1 : 0;
+    const int pos0 = r.len - r.n;  // the first token's position
+    const int group0 = pos0 >> 3, groups = r.n ? ((r.len - 1) >> 3) - group0 + 1 : 0;
     const float ku = pow2i(p.k_exp), vu = pow2i(p.v_exp);
-    const bool bf16 = p.bf16;
-    for (long long i = blockIdx.x * 256LL + threadIdx.x; i < static_cast<long long>(pairs) * per; i += gridDim.x * 256LL) {
-        const int pr = static_cast<int>(i / per), u = static_cast<int>(i) - pr * per, head = u / C8, c8 = u % C8;
-        const int pos = 2 * (pair0 + pr);
-        uint32_t k[2][4], v[2][4];
+    const int c8 = threadIdx.x % C8, units = groups * p.Hkv;
+    for (int u = blockIdx.x * (256 / C8) + threadIdx.x / C8; u < units; u += gridDim.x * (256 / C8)) {
+        const int gr = u / p.Hkv, head = u - gr * p.Hkv, pos = 8 * (group0 + gr);
         int id = -1;
         if (pos >= 0 && r.row >= 0 && pos < r.len) id = page_of(p, r.row, pos / p.P);
-        if (id < 0) {
-#pragma unroll
-            for (int e = 0; e < 2; e++)
-#pragma unroll
-                for (int x = 0; x < 4; x++) k[e][x] = v[e][x] = 0;
-        } else {
+        uint32_t kw[8], ks[8], vs[4];
+        uint2 vw[4];
+        if (id >= 0) {
             const int t = pos % p.P, tb = t % p.blk, b = p.blk;
-            const uint8_t *blk = page_ptr(p, id, head) + (t / b) * B::size(b);
-            const uint32_t kw0 = *reinterpret_cast<const uint32_t *>(blk + tb * (D / 2) + 4 * c8);
-            const uint32_t kw1 = *reinterpret_cast<const uint32_t *>(blk + (tb + 1) * (D / 2) + 4 * c8);
-            const uint2 vw = *reinterpret_cast<const uint2 *>(blk + B::vc(b) + B::vcode(tb, c8 >> 1) + 8 * (c8 & 1));
-            const uint8_t *ks = blk + B::ks(b) + tb * (D / 16) + (c8 >> 1);
-            const uint16_t vs = *reinterpret_cast<const uint16_t *>(blk + B::vs(b) + B::vscale(tb, c8 >> 1));
-            const uint32_t s = e4m3x2_to_half2(static_cast<uint16_t>(ks[0] | ks[D / 16] << 8)), sv = e4m3x2_to_half2(vs);
-            uint32_t h0[4], h1[4], va[4], vb[4];
-            e2m1x8_to_half(kw0, h0);
-            e2m1x8_to_half(kw1, h1);
-            e2m1x8_to_half(vw.x, va);  // a half2 is the two tokens of a channel
-            e2m1x8_to_half(vw.y, vb);
-            const uint32_t s0 = __byte_perm(s, s, 0x1010), s1 = __byte_perm(s, s, 0x3232);
+            const uint8_t *blk = page_ptr(p, id, head) + t / b * B::size(b);
+            const uint8_t *kc = blk + tb * (D / 2) + 4 * c8, *kb = blk + B::ks(b) + tb * (D / 16) + (c8 >> 1);
+            const uint8_t *vc = blk + B::vc(b) + B::vcode(tb, c8 >> 1) + 8 * (c8 & 1), *vb = blk + B::vs(b) + B::vscale(tb, c8 >> 1);
 #pragma unroll
-            for (int x = 0; x < 4; x++) {
-                k[0][x] = held_to_16(hmul2(h0[x], s0), ku, bf16);
-                k[1][x] = held_to_16(hmul2(h1[x], s1), ku, bf16);
-                va[x] = hmul2(va[x], sv);
-                vb[x] = hmul2(vb[x], sv);
+            for (int e = 0; e < 8; e++) {
+                kw[e] = *reinterpret_cast<const uint32_t *>(kc + e * (D / 2));
+                ks[e] = kb[e * (D / 16)];
             }
 #pragma unroll
-            for (int x = 0; x < 2; x++) {
-                v[0][x] = held_to_16(__byte_perm(va[2 * x], va[2 * x + 1], 0x5410), vu, bf16);
-                v[1][x] = held_to_16(__byte_perm(va[2 * x], va[2 * x + 1], 0x7632), vu, bf16);
-                v[0][x + 2] = held_to_16(__byte_perm(vb[2 * x], vb[2 * x + 1], 0x5410), vu, bf16);
-                v[1][x + 2] = held_to_16(__byte_perm(vb[2 * x], vb[2 * x + 1], 0x7632), vu, bf16);
+            for (int e = 0; e < 4; e++) {
+                vw[e] = *reinterpret_cast<const uint2 *>(vc + 16 * e);
+                vs[e] = *reinterpret_cast<const uint16_t *>(vb + 2 * e);
+            }
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; e++) kw[e] = ks[e] = 0;
+#pragma unroll
+            for (int e = 0; e < 4; e++) {
+                vw[e] = make_uint2(0, 0);
+                vs[e] = 0;
             }
         }
+        const long long o = ((static_cast<long long>(r.q0) + pos - pos0) * p.Hkv + head) * D + 8 * c8;
+        uint16_t *ko = a.k + o, *vo = a.v + o;
+        const int stride = p.Hkv * D;
 #pragma unroll
-        for (int e = 0; e < 2; e++) {
+        for (int e = 0; e < 8; e++) {
             if (pos + e < pos0 || pos + e >= r.len) continue;
-            const long long o = ((static_cast<long long>(r.q0) + pos + e - pos0) * p.Hkv + head) * D + 8 * c8;
-            *reinterpret_cast<uint4 *>(a.k + o) = make_uint4(k[e][0], k[e][1], k[e][2], k[e][3]);
-            *reinterpret_cast<uint4 *>(a.v + o) = make_uint4(v[e][0], v[e][1], v[e][2], v[e][3]);
+            uint32_t h[4];
+            e2m1x8_to_half(kw[e], h);
+            const uint32_t s = e4m3x2_to_half2(static_cast<uint16_t>(ks[e])), s2 = __byte_perm(s, s, 0x1010);
+#pragma unroll
+            for (int x = 0; x < 4; x++) h[x] = held_to_16<BF16>(hmul2(h[x], s2), ku);
+            *reinterpret_cast<uint4 *>(ko + e * stride) = make_uint4(h[0], h[1], h[2], h[3]);
+        }
+#pragma unroll
+        for (int e = 0; e < 4; e++) {
+            uint32_t x[4], y[4], w[2][4];  // a half2 is the two tokens of a channel
+            e2m1x8_to_half(vw[e].x, x);
+            e2m1x8_to_half(vw[e].y, y);
+            const uint32_t s = e4m3x2_to_half2(static_cast<uint16_t>(vs[e]));
+#pragma unroll
+            for (int i = 0; i < 4; i++) {
+                x[i] = hmul2(x[i], s);
+                y[i] = hmul2(y[i], s);
+            }
+#pragma unroll
+            for (int i = 0; i < 2; i++) {
+                w[0][i] = held_to_16<BF16>(__byte_perm(x[2 * i], x[2 * i + 1], 0x5410), vu);
+                w[1][i] = held_to_16<BF16>(__byte_perm(x[2 * i], x[2 * i + 1], 0x7632), vu);
+                w[0][i + 2] = held_to_16<BF16>(__byte_perm(y[2 * i], y[2 * i + 1], 0x5410), vu);
+                w[1][i + 2] = held_to_16<BF16>(__byte_perm(y[2 * i], y[2 * i + 1], 0x7632), vu);
+            }
+#pragma unroll
+            for (int i = 0; i < 2; i++) {
+                const int at = pos + 2 * e + i;
+                if (at < pos0 || at >= r.len) continue;
+                *reinterpret_cast<uint4 *>(vo + (2 * e + i) * stride) = make_uint4(w[i][0], w[i][1], w[i][2], w[i][3]);
+            }
         }
     }
 }
 
+template <int D, int B>
+void append_of(const PagesStoreArgs &a, dim3 grid, cudaStream_t st) {
+    if (a.p.bf16) append_kernel<D, B, true><<<grid, ST_THREADS, 0, st>>>(a);
+    else append_kernel<D, B, false><<<grid, ST_THREADS, 0, st>>>(a);
+}
+template <int D>
+void read_of(const PagesReadArgs &a, dim3 grid, cudaStream_t st) {
+    if (a.p.bf16) read_kernel<D, true><<<grid, 256, 0, st>>>(a);
+    else read_kernel<D, false><<<grid, 256, 0, st>>>(a);
+}
 template <int D>
 void append_as(const PagesStoreArgs &a, dim3 grid, cudaStream_t st) {
-    if (a.p.blk == 64) append_kernel<D, 64><<<grid, ST_THREADS, 0, st>>>(a);
-    else if (a.p.blk == 32) append_kernel<D, 32><<<grid, ST_THREADS, 0, st>>>(a);
-    else append_kernel<D, 16><<<grid, ST_THREADS, 0, st>>>(a);
+    if (a.p.blk == 64) append_of<D, 64>(a, grid, st);
+    else if (a.p.blk == 32) append_of<D, 32>(a, grid, st);
+    else append_of<D, 16>(a, grid, st);
 }
 
 }  // namespace
@@ -359,12 +399,12 @@ int launch_pages_append(const PagesStoreArgs &a, void *stream) {
 }
 
 int launch_pages_read(const PagesReadArgs &a, void *stream) {
-    const long long per = static_cast<long long>(a.r.max_new / 2 + 1) * a.p.Hkv * (a.p.d / 8);
+    const long long per = static_cast<long long>((a.r.max_new + 6) / 8 + 1) * a.p.Hkv * (a.p.d / 8);
     const long long want = (per + 255) / 256;
     const dim3 grid(static_cast<unsigned>(want < 4096 ? want : 4096), a.r.n_rows);
     auto st = static_cast<cudaStream_t>(stream);
-    if (a.p.d == 128) read_kernel<128><<<grid, 256, 0, st>>>(a);
-    else read_kernel<64><<<grid, 256, 0, st>>>(a);
+    if (a.p.d == 128) read_of<128>(a, grid, st);
+    else read_of<64>(a, grid, st);
     return static_cast<int>(cudaGetLastError());
 }
 
