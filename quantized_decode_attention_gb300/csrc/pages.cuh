@@ -122,11 +122,4 @@ __device__ __forceinline__ uint32_t float8_to_e2m1(float x0, float x1, float x2,
     return r;
 }
 
-// Scale of 16 channels with the largest magnitude `top`: its e4m3 byte; S = 2^exp scale.
-__device__ __forceinline__ uint8_t block_scale(float top, float inv_unit, float unit, float &S) {
-    const uint8_t s = float_to_e4m3(__fdiv_rn(top, 6.f) * inv_unit);
-    S = e4m3_to_float(s) * unit;
-    return s;
-}
-
 }  // namespace dq

@@ -1,12 +1,14 @@
 // Paged cache: new tokens into pages (append) and back to 16 bits (read).
 //
 // A scale block is 16 channels of one token: top = max|x|, s = e4m3(top / 6 / 2^exp),
-// codes e2m1(x / (2^exp s)).  The quotient is taken as x r, r = 1 / (2^exp s) rounded,
-// and put on a grid of 2^-16 by adding and subtracting 192: x has at most 11
-// significant bits and a border between two codes, times the scale, at most 7, so
-// that a quotient off a border is off by 2^-13 or more, while x r is off by less than
-// 2^-21.  What the grid gives therefore lies on a border where the quotient does and
-// on its side where it does not, and the codes are those of exact arithmetic.
+// codes e2m1(x / (2^exp s)), both as exact arithmetic would round them:
+// - x / S is x (h + l) with h + l = 1 / S to 2^-44 in two fp32 numbers, h below 1 / S:
+//   fma(x, h, x l) is on a border between two codes where the quotient is (the border has
+//   3 bits), and elsewhere on its side, since x has at most 11 significant bits and a border
+//   times S at most 7, so that no other quotient comes within 2^-12 of a border.  l >= 0
+//   keeps the sign of a zero.
+// - top / 6 is a product with a rounded 1 / 6 put on a grid of 17 bits; borders between
+//   scales times 6 have at most 7 bits.
 //
 // Both kernels are bound by moving 16-bit values once; the arithmetic (about 8
 // instructions for a value on its way in, 4 on its way out) nearly fills the issue slots
@@ -20,11 +22,12 @@ namespace {
 
 constexpr int ST_THREADS = 128, ST_WARPS = ST_THREADS / 32;
 
+// The larger magnitudes (with signs of no meaning), NaN where there is one.
 template <bool BF16>
-__device__ __forceinline__ uint32_t max2_nan(uint32_t a, uint32_t b) {
+__device__ __forceinline__ uint32_t max2_abs(uint32_t a, uint32_t b) {
     uint32_t r;
-    if (BF16) asm("max.NaN.bf16x2 %0, %1, %2;\n" : "=r"(r) : "r"(a), "r"(b));
-    else asm("max.NaN.f16x2 %0, %1, %2;\n" : "=r"(r) : "r"(a), "r"(b));
+    if (BF16) asm("max.NaN.xorsign.abs.bf16x2 %0, %1, %2;\n" : "=r"(r) : "r"(a), "r"(b));
+    else asm("max.NaN.xorsign.abs.f16x2 %0, %1, %2;\n" : "=r"(r) : "r"(a), "r"(b));
     return r;
 }
 __device__ __forceinline__ uint32_t hmax2(uint32_t a, uint32_t b) {
@@ -60,29 +63,30 @@ struct Block16 {
 #pragma unroll
         for (int i = 0; i < 8; i++) w[i] = 0;
     }
-    // The scale's byte, and the reciprocal that turns values into codes (0 for a scale of 0).
+    // The scale's byte, and 1 / S in two parts that turns values into codes (0 for S = 0).
     // `fine` is cleared where a value is not finite; the scale is then the largest one.
     template <bool BF16>
-    __device__ __forceinline__ uint8_t scale(float inv_unit, float unit, float &r, bool &fine) const {
-        uint32_t m = w[0] & 0x7fff7fffu;
+    __device__ __forceinline__ uint8_t scale(float sixth, float unit, float2 &r, bool &fine) const {
+        uint32_t m = w[0];
 #pragma unroll
-        for (int i = 1; i < 8; i++) m = max2_nan<BF16>(m, w[i] & 0x7fff7fffu);
-        const uint32_t lo = m & 0xffffu, hi = m >> 16, inf = BF16 ? 0x7f80u : 0x7c00u;
+        for (int i = 1; i < 8; i++) m = max2_abs<BF16>(m, w[i]);
+        const uint32_t lo = m & 0x7fffu, hi = m >> 16 & 0x7fffu, inf = BF16 ? 0x7f80u : 0x7c00u;
         uint32_t top = lo > hi ? lo : hi;  // magnitudes order like their bits
         if (top >= inf) {
             top = inf;
             fine = false;
         }
-        float S;
-        const uint8_t s = block_scale(from16(static_cast<uint16_t>(top), BF16), inv_unit, unit, S);
-        r = S > 0.f ? __frcp_rn(S) : 0.f;
+        const float t = from16(static_cast<uint16_t>(top), BF16) * sixth;
+        const uint8_t s = float_to_e4m3(__uint_as_float((__float_as_uint(t) + 0x40u) & ~0x7fu));
+        const float S = e4m3_to_float(s) * unit;
+        float h;
+        asm("rcp.approx.ftz.f32 %0, %1;\n" : "=f"(h) : "f"(S));
+        h = __uint_as_float(__float_as_uint(h) - 2u);  // off by an ulp at most: below 1 / S now
+        r = S > 0.f ? make_float2(h, fmaf(-S, h, 1.f) * h) : make_float2(0.f, 0.f);
         return s;
     }
 };
-__device__ __forceinline__ float on_grid(float x, float r) {
-    const float q = fmaf(x, r, 192.f) - 192.f;
-    return __uint_as_float((__float_as_uint(q) & 0x7fffffffu) | (__float_as_uint(x) & 0x80000000u));  // tiny ones keep their sign
-}
+__device__ __forceinline__ float quotient(float x, float2 r) { return fmaf(x, r.x, x * r.y); }
 
 // One CTA per (row, touched page, KV head).  A block of B = min(P, 64) tokens at a time
 // is put together in shared memory in the page's layout.  What a page holds already is
@@ -115,7 +119,7 @@ __global__ void __launch_bounds__(ST_THREADS) append_kernel(PagesStoreArgs a) {
     // the call's token at t = 0, k and v of this head there
     const long long first = r.q0 + (static_cast<long long>(j) * p.P - (r.len - r.n));
     const uint16_t *kp = a.k + first * a.kt + head * a.kh, *vp = a.v + first * a.vt + head * a.vh;
-    const float ku = pow2i(p.k_exp), ki = pow2i(-p.k_exp), vu = pow2i(p.v_exp), vi = pow2i(-p.v_exp);
+    const float ku = pow2i(p.k_exp), k6 = 0.16666667f * pow2i(-p.k_exp), vu = pow2i(p.v_exp), v6 = 0.16666667f * pow2i(-p.v_exp);
     bool fine = true;
     // summary: this thread's 8 channels over every (128 / (D / 8))-th token
     const int col = tid % (D / 8);
@@ -131,19 +135,19 @@ __global__ void __launch_bounds__(ST_THREADS) append_kernel(PagesStoreArgs a) {
         const bool some = n0 < n1;
         Block16 kx[KI], vx[VI][2];
         if (some) {  // the new tokens are on their way first
+            const int tk = n0 + tid / C, tv = (n0 & ~1) + 2 * (tid / C);
+            const uint16_t *kq = kp + (b0 + tk) * a.kt + 16 * (tid % C), *vq = vp + (b0 + tv) * a.vt + 16 * (tid % C);
 #pragma unroll
-            for (int i = 0; i < KI; i++) {
-                const int u = tid + i * ST_THREADS, t = n0 + u / C;
-                if (t < n1) kx[i].load(kp + (b0 + t) * a.kt + 16 * (u % C));
-            }
+            for (int i = 0; i < KI; i++)
+                if (tk + i * (ST_THREADS / C) < n1) kx[i].load(kq + i * (ST_THREADS / C * a.kt));
 #pragma unroll
-            for (int i = 0; i < VI; i++) {
-                const int u = tid + i * ST_THREADS, t = (n0 & ~1) + 2 * (u / C);
+            for (int i = 0; i < VI; i++)
 #pragma unroll
-                for (int e = 0; e < 2; e++)
-                    if (t + e >= n0 && t + e < n1) vx[i][e].load(vp + (b0 + t + e) * a.vt + 16 * (u % C));
+                for (int e = 0; e < 2; e++) {
+                    const int t = tv + i * (2 * ST_THREADS / C) + e;
+                    if (t >= n0 && t < n1) vx[i][e].load(vq + i * (2 * ST_THREADS / C * a.vt) + e * a.vt);
                     else vx[i][e].clear();
-            }
+                }
         }
         const int g0 = some ? n0 / 8 : B / 8, g1 = (n1 + 7) / 8;  // 8-token groups written: [g0, g1)
         if (b0) __syncthreads();
@@ -165,8 +169,8 @@ __global__ void __launch_bounds__(ST_THREADS) append_kernel(PagesStoreArgs a) {
             for (int i = 0; i < KI; i++) {
                 const int u = tid + i * ST_THREADS, t = n0 + u / C, c = u % C;
                 if (t >= n1) break;
-                float rc;
-                img[L::ks(B) + t * C + c] = kx[i].template scale<BF16>(ki, ku, rc, fine);
+                float2 rc;
+                img[L::ks(B) + t * C + c] = kx[i].template scale<BF16>(k6, ku, rc, fine);
                 uint32_t code[2];
 #pragma unroll
                 for (int k = 0; k < 2; k++) {
@@ -174,8 +178,8 @@ __global__ void __launch_bounds__(ST_THREADS) append_kernel(PagesStoreArgs a) {
 #pragma unroll
                     for (int e = 0; e < 4; e++) {
                         const float2 f = pair_to_float<BF16>(kx[i].w[4 * k + e]);
-                        x[2 * e] = on_grid(f.x, rc);
-                        x[2 * e + 1] = on_grid(f.y, rc);
+                        x[2 * e] = quotient(f.x, rc);
+                        x[2 * e + 1] = quotient(f.y, rc);
                     }
                     code[k] = float8_to_e2m1(x[0], x[1], x[2], x[3], x[4], x[5], x[6], x[7]);
                 }
@@ -186,17 +190,17 @@ __global__ void __launch_bounds__(ST_THREADS) append_kernel(PagesStoreArgs a) {
                 const int u = tid + i * ST_THREADS, t = (n0 & ~1) + 2 * (u / C), c = u % C;
                 if (t >= n1) break;
                 const bool e0 = t >= n0, e1 = t + 1 < n1;
-                float r0 = 0.f, r1 = 0.f;
+                float2 r0 = make_float2(0.f, 0.f), r1 = r0;
                 uint8_t *cp = img + L::vc(B) + L::vcode(t, c), *sp = img + L::vs(B) + L::vscale(t, c);
-                if (e0) sp[0] = vx[i][0].template scale<BF16>(vi, vu, r0, fine);
-                if (e1) sp[1] = vx[i][1].template scale<BF16>(vi, vu, r1, fine);
+                if (e0) sp[0] = vx[i][0].template scale<BF16>(v6, vu, r0, fine);
+                if (e1) sp[1] = vx[i][1].template scale<BF16>(v6, vu, r1, fine);
                 uint32_t code[4];  // a byte is a channel: even token low, odd token high
 #pragma unroll
                 for (int k = 0; k < 4; k++) {
                     const float2 x = pair_to_float<BF16>(vx[i][0].w[2 * k]), y = pair_to_float<BF16>(vx[i][1].w[2 * k]);
                     const float2 z = pair_to_float<BF16>(vx[i][0].w[2 * k + 1]), w = pair_to_float<BF16>(vx[i][1].w[2 * k + 1]);
-                    code[k] = float8_to_e2m1(on_grid(x.x, r0), on_grid(y.x, r1), on_grid(x.y, r0), on_grid(y.y, r1), on_grid(z.x, r0),
-                                             on_grid(w.x, r1), on_grid(z.y, r0), on_grid(w.y, r1));
+                    code[k] = float8_to_e2m1(quotient(x.x, r0), quotient(y.x, r1), quotient(x.y, r0), quotient(y.y, r1), quotient(z.x, r0),
+                                             quotient(w.x, r1), quotient(z.y, r0), quotient(w.y, r1));
                 }
                 uint4 *dst = reinterpret_cast<uint4 *>(cp);
                 if (!e0 || !e1) {  // one of the two is new
