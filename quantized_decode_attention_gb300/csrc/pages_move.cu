@@ -47,6 +47,11 @@ __device__ __forceinline__ bool page_ok(const PagesView &p, int id) {
     return false;
 }
 
+// A plan's followers may be launched while it runs; they wait for its end before they
+// read anything (the hardware's dependency between launches of one stream).
+__device__ __forceinline__ void let_followers_start() { asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory"); }
+__device__ __forceinline__ void await_plan() { asm volatile("griddepcontrol.wait;\n" ::: "memory"); }
+
 __global__ void __launch_bounds__(MV_THREADS) resize_kernel(PagesView p, const int *rows, const int *lens, int n, int *ws) {
     __shared__ unsigned seen[DQ_PAGES_MAX_ROWS / 32];
     __shared__ int part[MV_WARPS + 1], bad, found;
@@ -54,6 +59,7 @@ __global__ void __launch_bounds__(MV_THREADS) resize_kernel(PagesView p, const i
         first_s[DQ_PAGES_MAX_ROWS];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     int *list = ws + PAGES_WS_HEAD, *src = list + p.n_pages, *dst = src + p.n_pages;
+    let_followers_start();
     if (tid == 0) {
         bad = found = 0;
         ws[0] = 0;
@@ -197,6 +203,7 @@ __global__ void __launch_bounds__(MV_THREADS) compact_kernel(PagesView p, int *w
     __shared__ int part[MV_WARPS + 1], n_src, n_dst;
     const int tid = threadIdx.x;
     int *map = ws + PAGES_WS_HEAD, *src = map + p.n_pages, *dst = src + p.n_pages;
+    let_followers_start();
     if (tid == 0) n_src = n_dst = 0;
     __syncthreads();
     int mine = 0;
@@ -229,25 +236,41 @@ __global__ void __launch_bounds__(MV_THREADS) compact_kernel(PagesView p, int *w
     }
 }
 
-// Copy the planned pages and summaries of every layer: 16 bytes a thread at a time.
-__global__ void __launch_bounds__(256) copy_kernel(PagesView p, const int *ws) {
+// Copy the planned pages and summaries of every layer.  A layer's page (all heads, then
+// its summaries) goes in slices of 16 KB, so that a few copies fill the card as evenly
+// as many do; a thread has four 16-byte loads on their way before it stores.  What the
+// plan names is disjoint: a destination was free.
+constexpr int CP_THREADS = 256, CP_DEEP = 4, CP_SLICE = CP_THREADS * CP_DEEP;
+__global__ void __launch_bounds__(CP_THREADS) copy_kernel(PagesView p, const int *ws) {
+    await_plan();
     const int n = ws[0];
     const int *src = ws + PAGES_WS_HEAD + p.n_pages, *dst = src + p.n_pages;
-    const int pb = p.Hkv * p.page_bytes / 16, sb = p.Hkv * p.sum_bytes / 16;
-    for (int u = blockIdx.x; u < n * p.n_layers; u += gridDim.x) {
-        const int m = u / p.n_layers;
-        const long long base = static_cast<long long>(u % p.n_layers) * p.n_pages;
-        const uint4 *a = reinterpret_cast<const uint4 *>(p.pages) + (base + src[m]) * pb;
-        uint4 *b = reinterpret_cast<uint4 *>(p.pages) + (base + dst[m]) * pb;
-        for (int i = threadIdx.x; i < pb; i += 256) b[i] = a[i];
-        a = reinterpret_cast<const uint4 *>(p.summary) + (base + src[m]) * sb;
-        b = reinterpret_cast<uint4 *>(p.summary) + (base + dst[m]) * sb;
-        for (int i = threadIdx.x; i < sb; i += 256) b[i] = a[i];
+    const int pb = p.Hkv * p.page_bytes / 16, sb = p.Hkv * p.sum_bytes / 16;  // 16-byte words of a page, of its summaries
+    const int slices = (pb + sb + CP_SLICE - 1) / CP_SLICE;
+    const long long items = static_cast<long long>(n) * p.n_layers * slices;
+    for (long long it = blockIdx.x; it < items; it += gridDim.x) {
+        const long long u = it / slices;
+        const int m = static_cast<int>(u / p.n_layers), w0 = static_cast<int>(it - u * slices) * CP_SLICE + threadIdx.x;
+        const long long base = (u - static_cast<long long>(m) * p.n_layers) * p.n_pages, from = base + src[m], to = base + dst[m];
+        const uint4 *ap = reinterpret_cast<const uint4 *>(p.pages) + from * pb, *as = reinterpret_cast<const uint4 *>(p.summary) + from * sb - pb;
+        uint4 *bp = reinterpret_cast<uint4 *>(p.pages) + to * pb, *bs = reinterpret_cast<uint4 *>(p.summary) + to * sb - pb;
+        uint4 v[CP_DEEP];
+#pragma unroll
+        for (int k = 0; k < CP_DEEP; k++) {
+            const int w = w0 + k * CP_THREADS;
+            if (w < pb + sb) v[k] = __ldcs((w < pb ? ap : as) + w);
+        }
+#pragma unroll
+        for (int k = 0; k < CP_DEEP; k++) {
+            const int w = w0 + k * CP_THREADS;
+            if (w < pb + sb) __stcs((w < pb ? bp : bs) + w, v[k]);
+        }
     }
 }
 
 // Table entries of moved pages follow.
 __global__ void __launch_bounds__(256) remap_kernel(PagesView p, const int *ws) {
+    await_plan();
     const int *map = ws + PAGES_WS_HEAD;
     if (ws[0] == 0) return;
     int len = p.seq_len[blockIdx.x];
@@ -261,11 +284,24 @@ __global__ void __launch_bounds__(256) remap_kernel(PagesView p, const int *ws) 
 
 }  // namespace
 
+static int launch_follower(void (*kernel)(PagesView, const int *), int grid, const PagesView &p, const int *ws, cudaStream_t st) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(256);
+    cfg.stream = st;
+    cudaLaunchAttribute at{};
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    return static_cast<int>(cudaLaunchKernelEx(&cfg, kernel, p, ws));
+}
+
 int launch_pages_resize(const PagesView &p, const int *rows, const int *lens, int n, int *ws, int num_sms, void *stream) {
     auto st = static_cast<cudaStream_t>(stream);
     resize_kernel<<<1, MV_THREADS, 0, st>>>(p, rows, lens, n, ws);
-    copy_kernel<<<4 * num_sms, 256, 0, st>>>(p, ws);
-    return static_cast<int>(cudaGetLastError());
+    const int e = static_cast<int>(cudaGetLastError());
+    return e ? e : launch_follower(copy_kernel, 6 * num_sms, p, ws, st);
 }
 
 int launch_pages_fork(const PagesView &p, const int *src, const int *dst, int n, void *stream) {
@@ -276,8 +312,10 @@ int launch_pages_fork(const PagesView &p, const int *src, const int *dst, int n,
 int launch_pages_compact(const PagesView &p, int *ws, int num_sms, void *stream) {
     auto st = static_cast<cudaStream_t>(stream);
     compact_kernel<<<1, MV_THREADS, 0, st>>>(p, ws);
-    copy_kernel<<<4 * num_sms, 256, 0, st>>>(p, ws);
-    remap_kernel<<<p.max_seqs, 256, 0, st>>>(p, ws);
+    int e = static_cast<int>(cudaGetLastError());
+    // the tables first: both depend on the plan alone, and the tables are soon done
+    if (e || (e = launch_follower(remap_kernel, p.max_seqs, p, ws, st))) return e;
+    copy_kernel<<<6 * num_sms, CP_THREADS, 0, st>>>(p, ws);
     return static_cast<int>(cudaGetLastError());
 }
 
