@@ -40,6 +40,7 @@ constexpr float LN2 = 0.69314718055994530942f;
 constexpr uint64_t WAIT_NS = 2000000000ull;  // longest wait for a copy
 constexpr float SLACK = 8.f, LIFT = 7.f;   // log2 units
 constexpr int CHUNK = 32;                  // tokens
+constexpr int PROMPT_ROWS = 32;            // query rows of a row and KV head beyond which the tensor-core kernel takes over
 constexpr int UNIT_COST = 2;               // chunks that a unit's beginning and end are worth
 constexpr int MIN_PLACES = 16;             // places that make a CTA worth its merge
 
@@ -722,6 +723,7 @@ int launch_chunks(const PagesAttnArgs &a, int grid, cudaStream_t st) {
 int launch_pages_attention(const PagesAttnArgs &a, int num_sms, void *stream) {
     auto st = static_cast<cudaStream_t>(stream);
     const int grid = num_sms < PAGES_MAX_CTAS ? num_sms : PAGES_MAX_CTAS;
+    if (!a.sel && a.r.max_new * a.p.G > PROMPT_ROWS) return launch_pages_prompt(a, grid, stream);
     // 8 query rows fill one n tile; more share the conversions of two
     if (a.r.max_new * a.p.G <= 8) return a.p.d == 128 ? launch_chunks<128, 1, 16>(a, grid, st) : launch_chunks<64, 1, 16>(a, grid, st);
     return a.p.d == 128 ? launch_chunks<128, 2, 8>(a, grid, st) : launch_chunks<64, 2, 8>(a, grid, st);

@@ -42,10 +42,10 @@ struct PagesRows {
 // The int part of the workspace: [0] copies or moves of the last plan, [1] live pages
 // below which moves end, then three lists of n_pages.
 constexpr int PAGES_WS_HEAD = 16;
-// Behind it, attention: CTAs of a launch, and the floats of a record of 16 query rows
-// with head_dim 128 (accumulators, maximum and sum).
-constexpr int PAGES_MAX_CTAS = 256;
-constexpr int PAGES_REC_FLOATS = 16 * (128 + 2);
+// Behind it, attention: CTAs of a launch (one per SM), and the floats of a record of 256
+// query rows with head_dim 128 (accumulators, maximum and sum).
+constexpr int PAGES_MAX_CTAS = 160;
+constexpr int PAGES_REC_FLOATS = 256 * (128 + 2);
 inline size_t pages_ws_lists(int n_pages) {  // bytes of the lists, a multiple of 16
     return (PAGES_WS_HEAD * 4 + 12 * static_cast<size_t>(n_pages) + 15) / 16 * 16;
 }
@@ -94,6 +94,8 @@ int launch_pages_compact(const PagesView &p, int *ws, int num_sms, void *stream)
 int launch_pages_append(const PagesStoreArgs &a, void *stream);
 int launch_pages_read(const PagesReadArgs &a, void *stream);
 int launch_pages_attention(const PagesAttnArgs &a, int num_sms, void *stream);
+// many new tokens: the tensor-core kernel on at most `grid` CTAs
+int launch_pages_prompt(const PagesAttnArgs &a, int grid, void *stream);
 int launch_pages_select(const PagesSelectArgs &a, int num_sms, void *stream);
 
 }  // namespace dq
