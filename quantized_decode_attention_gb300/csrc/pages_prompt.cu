@@ -65,7 +65,19 @@ __device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t (&r)[16]
         "r"(r[13]), "r"(r[14]), "r"(r[15])
         : "memory");
 }
-__device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;\n" ::: "memory"); }
+// Wait for the loads so far; nothing that uses r moves before it.
+template <int N>
+__device__ __forceinline__ void tmem_wait_ld(uint32_t (&r)[N]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;\n" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < N; i++) asm volatile("" : "+r"(r[i]));
+}
+__device__ __forceinline__ void tmem_ld16(uint32_t addr, uint32_t (&r)[16]) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]),
+                   "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+                 : "r"(addr));
+}
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory"); }
 __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;\n" ::: "memory"); }
 __device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;\n" ::: "memory"); }
@@ -104,6 +116,97 @@ __device__ __forceinline__ uint32_t half2_of(float a, float b) {
     uint32_t r;
     asm("cvt.rn.f16x2.f32 %0, %1, %2;\n" : "=r"(r) : "f"(b), "f"(a));
     return r;
+}
+
+// Two fp32 numbers at a time.
+__device__ __forceinline__ uint64_t two(float a, float b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};\n" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float2 both(uint64_t x) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;\n" : "=f"(r.x), "=f"(r.y) : "l"(x));
+    return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;\n" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;\n" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
+// One query row's running softmax: m and the sum of weights in two halves.
+struct RowState {
+    float f, m;
+    uint64_t l[2];
+    __device__ __forceinline__ float mu() const { return m == -INFINITY ? 0.f : m - LIFT; }  // what a logit loses before exp2
+    __device__ __forceinline__ float limit() const { return m == -INFINITY ? -INFINITY : m + SLACK; }
+    __device__ __forceinline__ float sum() const {
+        const float2 a = both(l[0]), b = both(l[1]);
+        return (a.x + a.y) + (b.x + b.y);
+    }
+    // A logit z passed the limit (in some row of the warp): raise m; the sums, the accumulator (n_o columns at o_at)
+    // and this tile's weights so far (n_p columns of two at p_at) follow.
+    template <int D>
+    __device__ void raise(float z, bool has_o, uint32_t o_at, int n_p, uint32_t p_at) {
+        const float mx = fmaxf(m, z), al = mx == -INFINITY ? 1.f : ex2(m - mx);
+        m = mx;
+#pragma unroll
+        for (int i = 0; i < 2; i++) {
+            const float2 x = both(l[i]);
+            l[i] = two(x.x * al, x.y * al);
+        }
+        tmem_wait_st();
+        uint32_t s[16];
+        if (has_o) {
+#pragma unroll 1
+            for (int c = 0; c < D; c += 16) {
+                tmem_ld16(o_at + c, s);
+                tmem_wait_ld(s);
+#pragma unroll
+                for (int i = 0; i < 16; i++) s[i] = __float_as_uint(__uint_as_float(s[i]) * al);
+                tmem_st16(o_at + c, s);
+            }
+        }
+#pragma unroll 1
+        for (int c = 0; c < n_p; c += 16) {
+            tmem_ld16(p_at + c, s);
+            tmem_wait_ld(s);
+#pragma unroll
+            for (int i = 0; i < 16; i++) {
+                const float2 x = __half22float2(*reinterpret_cast<const __half2 *>(&s[i]));
+                s[i] = half2_of(x.x * al, x.y * al);
+            }
+            tmem_st16(p_at + c, s);
+        }
+    }
+    // Scores of 32 keys -> weights, two a word.
+    __device__ __forceinline__ void weigh(const uint32_t (&s)[32], uint32_t (&w)[16]) {
+        const float lose = -mu();
+        const uint64_t ff = two(f, f), mm = two(lose, lose);
+#pragma unroll
+        for (int i = 0; i < 16; i++) {
+            const float2 e = both(fma2(two(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])), ff, mm));
+            const float a = ex2(e.x), b = ex2(e.y);
+            l[i & 1] = add2(l[i & 1], two(a, b));
+            w[i] = half2_of(a, b);
+        }
+    }
+};
+__device__ __forceinline__ float top_of(const uint32_t (&s)[32]) {
+    float t[4];
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+        t[i] = fmaxf(__uint_as_float(s[8 * i]), __uint_as_float(s[8 * i + 1]));
+#pragma unroll
+        for (int j = 2; j < 8; j += 2) t[i] = fmaxf(t[i], fmaxf(__uint_as_float(s[8 * i + j]), __uint_as_float(s[8 * i + j + 1])));
+    }
+    return fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3]));
 }
 
 // ---- the line of units ---------------------------------------------------------------------
@@ -295,7 +398,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prompt(PagesAttnArgs a) {
             const bool real = row < tb * p.G && tok < r.n;
             const int pos = real ? r.len - r.n + tok : 0x7fffffff;  // no row: nothing to mask
             // the query, by a power of two below 2^14 and with sm_scale's sign, as binary16
-            float f = 0.f, m = -INFINITY, l = 0.f;
+            RowState row_s{0.f, -INFINITY, {0, 0}};
             if (g.t0 < g.t1) {
                 const uint16_t *src = a.q + (static_cast<long long>(r.q0) + tok) * a.qt + (g.u.head * p.G + gq) * a.qh;
                 uint4 w[D / 8];
@@ -312,7 +415,8 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prompt(PagesAttnArgs a) {
                 int up = 13 - (static_cast<int>(__float_as_uint(top) >> 23) - 127);
                 up = top > 0.f ? (up > 126 ? 126 : up) : 0;
                 const float by = a.scale_log2 < 0.f ? -pow2i(up) : pow2i(up);
-                f = fabsf(a.scale_log2) * pow2i(-up);
+                // (never 0: a hidden key's -inf stays one)
+                row_s.f = fmaxf(fabsf(a.scale_log2) * pow2i(-up), 1e-37f);
 #pragma unroll
                 for (int i = 0; i < D / 8; i++) {
                     const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
@@ -335,55 +439,36 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prompt(PagesAttnArgs a) {
                 tc_fence_after();
                 const int key0 = k * KEYS;
                 const bool tail = key0 + KEYS - 1 > least;
-                uint32_t s[32];
-                float top = -INFINITY;
+                if (tail) {  // hidden keys' scores become -inf
+#pragma unroll 1
+                    for (int c = 0; c < KEYS; c += 32) {
+                        uint32_t s[32];
+                        tmem_ld32(s_at + c, s);
+                        tmem_wait_ld(s);
 #pragma unroll
-                for (int c = 0; c < KEYS / 32; c++) {
-                    tmem_ld32(s_at + 32 * c, s);
-                    tmem_wait_ld();
-                    if (tail) {
-#pragma unroll
-                        for (int i = 0; i < 32; i++) top = fmaxf(top, key0 + 32 * c + i > pos ? -INFINITY : __uint_as_float(s[i]));
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < 32; i++) top = fmaxf(top, __uint_as_float(s[i]));
+                        for (int i = 0; i < 32; i++) s[i] = key0 + c + i > pos ? 0xff800000u : s[i];
+                        tmem_st32(s_at + c, s);
                     }
+                    tmem_wait_st();
                 }
-                const float z = top == -INFINITY ? -INFINITY : top * f;
-                if (__any_sync(FULL, z > (m == -INFINITY ? -INFINITY : m + SLACK))) {
-                    const float mx = fmaxf(m, z), al = mx == -INFINITY ? 1.f : ex2(m - mx);
-                    m = mx;
-                    l *= al;
-                    if (k > g.t0) {  // the products into it are done: they were issued before this score's
-#pragma unroll
-                        for (int c = 0; c < D / 32; c++) {
-                            tmem_ld32(o_at + 32 * c, s);
-                            tmem_wait_ld();
-#pragma unroll
-                            for (int i = 0; i < 32; i++) s[i] = __float_as_uint(__uint_as_float(s[i]) * al);
-                            tmem_st32(o_at + 32 * c, s);
-                        }
-                    }
-                }
-                const float mu = m == -INFINITY ? 0.f : m - LIFT;
-#pragma unroll
-                for (int c = 0; c < KEYS / 32; c++) {
-                    tmem_ld32(s_at + 32 * c, s);
-                    tmem_wait_ld();
+                // 32 keys at a time, the next 32 on their way; their weights take the place of scores that were read
+                uint32_t sa[32], sb[32];
+                auto chunk = [&](uint32_t (&s)[32], int c) {
+                    const float top = top_of(s), z = top == -INFINITY ? -INFINITY : top * row_s.f;
+                    if (__any_sync(FULL, z > row_s.limit())) row_s.raise<D>(z, k > g.t0, o_at, 16 * c, s_at);
                     uint32_t w[16];
-#pragma unroll
-                    for (int i = 0; i < 32; i += 2) {
-                        float e0 = fmaf(__uint_as_float(s[i]), f, -mu), e1 = fmaf(__uint_as_float(s[i + 1]), f, -mu);
-                        if (tail) {
-                            if (key0 + 32 * c + i > pos) e0 = -INFINITY;
-                            if (key0 + 32 * c + i + 1 > pos) e1 = -INFINITY;
-                        }
-                        e0 = ex2(e0);
-                        e1 = ex2(e1);
-                        l += e0 + e1;
-                        w[i >> 1] = half2_of(e0, e1);
-                    }
-                    tmem_st16(s_at + 16 * c, w);  // the scores there have been read
+                    row_s.weigh(s, w);
+                    tmem_st16(s_at + 16 * c, w);
+                };
+                tmem_ld32(s_at, sa);
+#pragma unroll 1
+                for (int c = 0; c < KEYS / 32; c += 2) {
+                    tmem_wait_ld(sa);
+                    tmem_ld32(s_at + 32 * c + 32, sb);
+                    chunk(sa, c);
+                    tmem_wait_ld(sb);
+                    if (c + 2 < KEYS / 32) tmem_ld32(s_at + 32 * c + 64, sa);
+                    chunk(sb, c + 1);
                 }
                 tmem_wait_st();
                 tc_fence_before();
@@ -402,13 +487,13 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prompt(PagesAttnArgs a) {
             const long long o = (static_cast<long long>(r.q0) + tok) * p.Hq + g.u.head * p.G + gq;
             const bool whole = g.begins && g.ends;
             float *rec = a.records + (2LL * blockIdx.x + g.begins) * REC;
-            const float by = l == 0.f ? 0.f : a.out_scale / l;
+            const float l = row_s.sum(), m = row_s.m, by = l == 0.f ? 0.f : a.out_scale / l;
 #pragma unroll 1
             for (int c = 0; c < D / 32; c++) {
                 uint32_t s[32];
                 if (g.t0 < g.t1) {
                     tmem_ld32(o_at + 32 * c, s);
-                    tmem_wait_ld();
+                    tmem_wait_ld(s);
                 } else {
 #pragma unroll
                     for (int i = 0; i < 32; i++) s[i] = 0;
@@ -440,6 +525,15 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prompt(PagesAttnArgs a) {
         // ---- codes to operands: a thread a key, and a thread 8 tokens of 16 value channels --------
         const int dt = tid - 256, kg = dt & 15, c16 = dt >> 4;
         const bool has_v = c16 < D / 16;
+        const int shift = 31 - __clz(p.P), in_page = p.P - 1, b = p.blk, b_shift = 31 - __clz(b), in_block = b - 1;  // powers of two
+        // this thread's rows in the operands, the row's swizzle in place: piece c is at that address ^ 16 c
+        const uint32_t k_row = smem_u32(sh.k[0]) + swizzled(dt, 0);
+        uint32_t v_row[4];
+#pragma unroll
+        for (int c = 0; c < 4; c++) v_row[c] = smem_u32(sh.v[0]) + (kg >> 3) * (D * 128) + swizzled(c16 * 16 + c, kg & 7);
+        auto store16 = [](uint32_t addr, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
+            asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};\n" ::"r"(addr), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
+        };
         struct Packed {
             uint4 k[D / 32], v[4];
             uint2 ks, vs;
@@ -451,7 +545,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prompt(PagesAttnArgs a) {
             x = g.u.end;
             auto number = [&](int at) -> int {  // page of position `at`, or none
                 if (at >= r.len || r.row < 0) return -1;
-                return p.table[static_cast<long long>(r.row) * p.M + at / p.P];
+                return p.table[static_cast<long long>(r.row) * p.M + (at >> shift)];
             };
             auto checked = [&](int id, int at) -> int {
                 if (at >= r.len || r.row < 0 || (id >= 0 && id < p.n_pages)) return id;
@@ -459,7 +553,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prompt(PagesAttnArgs a) {
                 return -1;
             };
             auto load = [&](Packed &w, int tile, int idk, int idv) {
-                const int key = tile * KEYS + dt, tok = tile * KEYS + 8 * kg, b = p.blk;
+                const int key = tile * KEYS + dt, tok = tile * KEYS + 8 * kg;
                 idk = checked(idk, key);
                 idv = checked(idv, tok);
 #pragma unroll
@@ -468,16 +562,16 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prompt(PagesAttnArgs a) {
                 for (int i = 0; i < 4; i++) w.v[i] = make_uint4(0, 0, 0, 0);
                 w.ks = w.vs = make_uint2(0, 0);
                 if (idk >= 0) {
-                    const int u = key % p.P, ub = u % b;
-                    const uint8_t *blk = page_ptr(p, idk, g.u.head) + u / b * B::size(b);
+                    const int u = key & in_page, ub = u & in_block;
+                    const uint8_t *blk = page_ptr(p, idk, g.u.head) + (u >> b_shift) * B::size(b);
 #pragma unroll
                     for (int i = 0; i < D / 32; i++) w.k[i] = *reinterpret_cast<const uint4 *>(blk + ub * (D / 2) + 16 * i);
                     if (D == 128) w.ks = *reinterpret_cast<const uint2 *>(blk + B::ks(b) + ub * (D / 16));
                     else w.ks.x = *reinterpret_cast<const uint32_t *>(blk + B::ks(b) + ub * (D / 16));
                 }
                 if (has_v && idv >= 0) {
-                    const int u = tok % p.P, ub = u % b;
-                    const uint8_t *blk = page_ptr(p, idv, g.u.head) + u / b * B::size(b);
+                    const int u = tok & in_page, ub = u & in_block;
+                    const uint8_t *blk = page_ptr(p, idv, g.u.head) + (u >> b_shift) * B::size(b);
 #pragma unroll
                     for (int i = 0; i < 4; i++) w.v[i] = *reinterpret_cast<const uint4 *>(blk + B::vc(b) + B::vcode(ub, c16) + 16 * i);
                     w.vs = *reinterpret_cast<const uint2 *>(blk + B::vs(b) + B::vscale(ub, c16));
@@ -507,8 +601,8 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prompt(PagesAttnArgs a) {
                         uint32_t h[4];
                         e2m1x8_to_half(i & 1 ? (e ? q.w : q.z) : (e ? q.y : q.x), h);
                         const int c = 2 * i + e;
-                        *reinterpret_cast<uint4 *>(sh.k[st] + (c >> 3) * (KEYS * 128) + swizzled(dt, c & 7)) =
-                            make_uint4(hmul2(h[0], s2), hmul2(h[1], s2), hmul2(h[2], s2), hmul2(h[3], s2));
+                        store16(((k_row + st * (KEYS * D * 2)) ^ ((c & 7) << 4)) + (c >> 3) * (KEYS * 128), hmul2(h[0], s2), hmul2(h[1], s2),
+                                hmul2(h[2], s2), hmul2(h[3], s2));
                     }
                 }
                 fence_proxy_async();
@@ -533,8 +627,9 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prompt(PagesAttnArgs a) {
                         }
 #pragma unroll
                         for (int c = 0; c < 4; c++)
-                            *reinterpret_cast<uint4 *>(sh.v[st] + (kg >> 3) * (D * 128) + swizzled(c16 * 16 + 4 * wd + c, kg & 7)) =
-                                make_uint4(hmul2(h[0][c], sv[0]), hmul2(h[1][c], sv[1]), hmul2(h[2][c], sv[2]), hmul2(h[3][c], sv[3]));
+                            // rows 4 wd + c: the swizzle goes by the row's last 3 bits, of which wd turns the highest
+                            store16(((v_row[c] + st * (KEYS * D * 2)) ^ ((wd & 1) << 6)) + wd * 512, hmul2(h[0][c], sv[0]), hmul2(h[1][c], sv[1]),
+                                    hmul2(h[2][c], sv[2]), hmul2(h[3][c], sv[3]));
                     }
                 }
                 fence_proxy_async();
