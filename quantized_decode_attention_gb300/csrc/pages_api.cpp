@@ -224,7 +224,8 @@ dq_status dq_pages_attention(const dq_pages_config *cfg, const dq_pages_buffers 
     a.out_scale = std::ldexp(1.0f, cfg->v_exp);
     uint8_t *ws = static_cast<uint8_t *>(bufs->workspace) + dq::pages_ws_lists(cfg->n_pages);
     a.tickets = reinterpret_cast<int *>(ws);
-    a.records = reinterpret_cast<float *>(ws + dq::PAGES_MAX_CTAS * 4);
+    a.joins = reinterpret_cast<int *>(ws + dq::PAGES_MAX_CTAS * 4);
+    a.records = reinterpret_cast<float *>(ws + dq::PAGES_MAX_CTAS * 20);
     return launched(dq::launch_pages_attention(a, device_sms(), stream), "attention launch");
 }
 

@@ -50,7 +50,7 @@ inline size_t pages_ws_lists(int n_pages) {  // bytes of the lists, a multiple o
     return (PAGES_WS_HEAD * 4 + 12 * static_cast<size_t>(n_pages) + 15) / 16 * 16;
 }
 inline size_t pages_ws_bytes(int n_pages) {
-    return pages_ws_lists(n_pages) + PAGES_MAX_CTAS * 4 + static_cast<size_t>(PAGES_MAX_CTAS) * 2 * PAGES_REC_FLOATS * 4;
+    return pages_ws_lists(n_pages) + PAGES_MAX_CTAS * 20 + static_cast<size_t>(PAGES_MAX_CTAS) * 2 * PAGES_REC_FLOATS * 4;
 }
 
 struct PagesStoreArgs {
@@ -76,6 +76,7 @@ struct PagesAttnArgs {
     float scale_log2;     // sm_scale 2^k_exp log2(e)
     float out_scale;      // 2^v_exp
     int *tickets;         // workspace: [PAGES_MAX_CTAS], 0 between calls
+    int *joins;           // workspace: [PAGES_MAX_CTAS][4], what the tensor-core kernel leaves to be joined
     float *records;       // workspace: [PAGES_MAX_CTAS][2][PAGES_REC_FLOATS]
 };
 struct PagesSelectArgs {

@@ -10,8 +10,8 @@
 // KV head, in two tiles of 128.  It walks the keys that its last token sees, 128 at a
 // time.  Units stand on a line, each as long as its keys (causal: later blocks are longer),
 // and the line is cut into equal shares, one for each CTA (one per SM); a unit that
-// crosses a border leaves its parts in the workspace, and the last CTA to arrive adds
-// them up in CTA order.
+// crosses a border leaves its parts in the workspace, and a second kernel adds them up in
+// CTA order.
 //
 // Roles of the 16 warps.  Warps 0-3 and 4-7: softmax of tile 0 and 1, a thread a query
 // row: scores come from tensor memory, weights go back there as binary16 in the place of
@@ -85,22 +85,28 @@ __device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::
 __device__ __forceinline__ void tc_commit(uint64_t *bar) {
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n" ::"r"(smem_u32(bar)) : "memory");
 }
-__device__ __forceinline__ void mma_smem(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t add) {
-    asm volatile("{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d), "l"(a), "l"(b),
-                 "r"(idesc), "r"(add)
-                 : "memory");
-}
-__device__ __forceinline__ void mma_tmem(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t add) {
-    asm volatile("{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d), "r"(a), "l"(b),
-                 "r"(idesc), "r"(add)
-                 : "memory");
-}
 __device__ __forceinline__ void mbar_arrive(uint64_t *bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];\n" ::"r"(smem_u32(bar)) : "memory");
 }
-// Descriptor of a K-major operand with 128-byte swizzle: 8 rows of 128 bytes are 1024 bytes.
-__device__ __forceinline__ uint64_t operand(uint32_t addr) {
-    return static_cast<uint64_t>(addr >> 4 & 0x3fffu) | 1ull << 16 | static_cast<uint64_t>(1024 >> 4) << 32 | 1ull << 46 | 2ull << 61;
+// Descriptor of a K-major operand with 128-byte swizzle (8 rows of 128 bytes are 1024
+// bytes): its low word holds the address in units of 16 bytes, so that an operand n bytes
+// further on is n / 16 more.
+__device__ __forceinline__ uint32_t operand(uint32_t addr) { return (addr >> 4 & 0x3fffu) | 1u << 16; }
+constexpr uint32_t OPERAND_HIGH = 1024u >> 4 | 1u << 14 | 2u << 29;
+// D += A B (D = A B where `add` is 0); descriptors by their low words.
+__device__ __forceinline__ void mma_smem(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t add) {
+    asm volatile(
+        "{\n .reg .pred p;\n .reg .b64 x, y;\n mov.b64 x, {%1, %5};\n mov.b64 y, {%2, %5};\n setp.ne.u32 p, %4, 0;\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n}\n" ::"r"(d),
+        "r"(a), "r"(b), "r"(idesc), "r"(add), "r"(OPERAND_HIGH)
+        : "memory");
+}
+__device__ __forceinline__ void mma_tmem(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t add) {
+    asm volatile(
+        "{\n .reg .pred p;\n .reg .b64 y;\n mov.b64 y, {%2, %5};\n setp.ne.u32 p, %4, 0;\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %3, p;\n}\n" ::"r"(d),
+        "r"(a), "r"(b), "r"(idesc), "r"(add), "r"(OPERAND_HIGH)
+        : "memory");
 }
 // Instruction descriptor: binary16 operands, both K-major, fp32 accumulators, M = 128.
 __host__ __device__ constexpr uint32_t product(int n) { return 1u << 4 | static_cast<uint32_t>(n / 8) << 17 | (TILE / 16u) << 24; }
@@ -228,7 +234,6 @@ struct Shared {
     long long part[THREADS / 32];
     uint64_t q_full[2], k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2], o_full[2];
     uint32_t tmem;
-    int last[2];
 };
 
 __device__ __forceinline__ long long blocks_before(long long base, int tb, int b) {  // places of blocks 0 .. b - 1 of one head
@@ -365,8 +370,17 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prompt(PagesAttnArgs a) {
     }
     int ctas = static_cast<int>(N / MIN_SHARE < gridDim.x ? N / MIN_SHARE : gridDim.x);
     if (ctas < 1) ctas = 1;
-    if (N == 0 || static_cast<int>(blockIdx.x) >= ctas) return;
+    int4 *join = reinterpret_cast<int4 *>(a.joins) + blockIdx.x;
+    if (N == 0 || static_cast<int>(blockIdx.x) >= ctas) {
+        if (tid == 0) *join = make_int4(0, 0, 0, 0);
+        return;
+    }
     const long long c0 = share(N, ctas, blockIdx.x), c1 = share(N, ctas, blockIdx.x + 1);
+    if (tid == 0) {  // the unit that begins here and goes on in other CTAs, if any
+        const Unit u = find_unit<D>(sh, a, tb, c1 - 1);
+        const bool on = u.start >= c0 && u.end > c1;
+        *join = on ? make_int4(u.i, u.head, u.b, share_of(N, ctas, u.end - 1) - static_cast<int>(blockIdx.x) + 1) : make_int4(0, 0, 0, 0);
+    }
     if (warp == 12) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;\n" ::"r"(smem_u32(&sh.tmem)) : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;\n" ::: "memory");
@@ -454,10 +468,17 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prompt(PagesAttnArgs a) {
                 // 32 keys at a time, the next 32 on their way; their weights take the place of scores that were read
                 uint32_t sa[32], sb[32];
                 auto chunk = [&](uint32_t (&s)[32], int c) {
-                    const float top = top_of(s), z = top == -INFINITY ? -INFINITY : top * row_s.f;
-                    if (__any_sync(FULL, z > row_s.limit())) row_s.raise<D>(z, k > g.t0, o_at, 16 * c, s_at);
+                    // the weights do not wait for the maximum: it seldom raises m, and then they are taken again
                     uint32_t w[16];
+                    const uint64_t l0 = row_s.l[0], l1 = row_s.l[1];
                     row_s.weigh(s, w);
+                    const float top = top_of(s), z = top == -INFINITY ? -INFINITY : top * row_s.f;
+                    if (__any_sync(FULL, z > row_s.limit())) {
+                        row_s.l[0] = l0;
+                        row_s.l[1] = l1;
+                        row_s.raise<D>(z, k > g.t0, o_at, 16 * c, s_at);
+                        row_s.weigh(s, w);
+                    }
                     tmem_st16(s_at + 16 * c, w);
                 };
                 tmem_ld32(s_at, sa);
@@ -643,16 +664,17 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prompt(PagesAttnArgs a) {
         uint32_t q_at[2], s_at[2], o_at[2];
 #pragma unroll
         for (int t = 0; t < 2; t++) {
-            q_at[t] = smem_u32(sh.q[t]);
+            q_at[t] = operand(smem_u32(sh.q[t]));
             s_at[t] = tmem + t * KEYS;
             o_at[t] = tmem + 2 * KEYS + t * D;
         }
+        const uint32_t k_at = operand(smem_u32(sh.k[0])), v_at = operand(smem_u32(sh.v[0]));
+        constexpr uint32_t STAGE = KEYS * D * 2 / 16;
         auto scores = [&](int t, int st) {
-            const uint32_t kb = smem_u32(sh.k[st]);
+            const uint32_t kb = k_at + st * STAGE;
 #pragma unroll
             for (int i = 0; i < D / 16; i++)
-                mma_smem(s_at[t], operand(q_at[t] + (i >> 2) * (TILE * 128) + (i & 3) * 32), operand(kb + (i >> 2) * (KEYS * 128) + (i & 3) * 32),
-                         product(KEYS), i > 0);
+                mma_smem(s_at[t], q_at[t] + (i >> 2) * (TILE * 8) + (i & 3) * 2, kb + (i >> 2) * (KEYS * 8) + (i & 3) * 2, product(KEYS), i > 0);
             tc_commit(&sh.s_full[t]);
         };
         for (long long x = c0; x < c1 && !late;) {
@@ -672,7 +694,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prompt(PagesAttnArgs a) {
             runs++;
             for (int k = g.t0; k < g.t1 && !late; k++, it++) {
                 const int st = it & 1, next = (it + 1) & 1;
-                const uint32_t vb = smem_u32(sh.v[st]);
+                const uint32_t vb = v_at + st * STAGE;
 #pragma unroll
                 for (int t = 0; t < 2; t++) {
                     wait(&sh.p_full[t], it & 1);
@@ -681,7 +703,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prompt(PagesAttnArgs a) {
                     tc_fence_after();
 #pragma unroll
                     for (int i = 0; i < KEYS / 16; i++)
-                        mma_tmem(o_at[t], s_at[t] + 8 * i, operand(vb + (i >> 2) * (D * 128) + (i & 3) * 32), product(D), k > g.t0 || i > 0);
+                        mma_tmem(o_at[t], s_at[t] + 8 * i, vb + (i >> 2) * (D * 8) + (i & 3) * 2, product(D), k > g.t0 || i > 0);
                     if (t == 1) tc_commit(&sh.v_empty[st]);
                     if (k + 1 < g.t1) {
                         if (t == 0) wait(&sh.k_full[next], (it + 1) >> 1 & 1);
@@ -704,50 +726,51 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prompt(PagesAttnArgs a) {
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;\n" ::"r"(tmem) : "memory");
     }
 
-    // ---- parts: of the unit that began before this CTA, and of the one that goes on after it -----
-    const Unit uf = find_unit<D>(sh, a, tb, c0), ul = find_unit<D>(sh, a, tb, c1 - 1);
-    const long long front = uf.start < c0 ? uf.start : -1, back = ul.start >= c0 && ul.end > c1 ? ul.start : -1;
-    if (lane == 0 && warp < 2) {
-        const Unit &u = warp == 0 ? uf : ul;
-        int all = 0;
-        if ((warp == 0 ? front : back) >= 0) {
-            const int cf = share_of(N, ctas, u.start), others = share_of(N, ctas, u.end - 1) - cf;
-            all = atomic_add_acq_rel_gpu(a.tickets + cf, 1) == others;
-            if (all) a.tickets[cf] = 0;  // for the next call
-        }
-        sh.last[warp] = all;
-    }
-    __syncthreads();
-#pragma unroll 1
-    for (int k = 0; k < 2; k++) {
-        if (!sh.last[k]) continue;
-        const Unit &u = k == 0 ? uf : ul;
-        const int cf = share_of(N, ctas, u.start), n = share_of(N, ctas, u.end - 1) - cf + 1;
-        for (int i = tid; i < ROWS * (D / 4); i += THREADS) {
-            const int row = i % ROWS, c4 = i / ROWS;
-            const int tok = u.b * tb + row / p.G;
-            if (row >= tb * p.G || tok >= u.r.n) continue;
-            float m = -INFINITY, l = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
-            for (int j = 0; j < n; j++) {
-                const float *rec = a.records + (2LL * (cf + j) + (j == 0)) * REC;
-                const float mk = rec[ROWS * D + row], lk = rec[ROWS * (D + 1) + row];
-                const float4 v = *reinterpret_cast<const float4 *>(rec + (c4 * ROWS + row) * 4);
-                const float mx = fmaxf(m, mk), mu = mx == -INFINITY ? 0.f : mx;
-                const float wa = ex2(m - mu), wb = ex2(mk - mu);  // 0 for a part that saw nothing
-                m = mx;
-                l = l * wa + lk * wb;
-                acc[0] = acc[0] * wa + v.x * wb;
-                acc[1] = acc[1] * wa + v.y * wb;
-                acc[2] = acc[2] * wa + v.z * wb;
-                acc[3] = acc[3] * wa + v.w * wb;
-            }
-            const long long o = (static_cast<long long>(u.r.q0) + tok) * p.Hq + u.head * p.G + row % p.G;
-            const float by = l == 0.f ? 0.f : a.out_scale / l;
-            *reinterpret_cast<uint2 *>(a.out + o * D + 4 * c4) =
-                make_uint2(pack2(to16(acc[0] * by, p.bf16), to16(acc[1] * by, p.bf16)), pack2(to16(acc[2] * by, p.bf16), to16(acc[3] * by, p.bf16)));
-            if (c4 == 0 && a.lse) a.lse[o] = l == 0.f ? -INFINITY : (m - LIFT + log2f(l)) * LN2;
+}
+
+// The units that crossed a share's border: CTA (c, y) adds up the parts of the unit that
+// began in share c and went on, 16 channels of its 256 rows, in CTA order.
+template <int D>
+__global__ void __launch_bounds__(ROWS) join_parts(PagesAttnArgs a) {
+    const int4 what = reinterpret_cast<const int4 *>(a.joins)[blockIdx.x];  // row of the call, KV head, block, parts
+    const int n = what.w, row = threadIdx.x, tb = ROWS / a.p.G, c = blockIdx.y;
+    const PagesView &p = a.p;
+    if (n == 0) return;
+    const PageRow r = page_row(p, a.r, what.x);
+    const int tok = what.z * tb + row / p.G;
+    if (row >= tb * p.G || tok >= r.n) return;
+    constexpr int REC = ROWS * (D + 2);
+    float m = -INFINITY, l = 0.f, acc[16];
+#pragma unroll
+    for (int i = 0; i < 16; i++) acc[i] = 0.f;
+#pragma unroll 2
+    for (int j = 0; j < n; j++) {
+        const float *rec = a.records + (2LL * (blockIdx.x + j) + (j == 0)) * REC;
+        const float mk = rec[ROWS * D + row], lk = rec[ROWS * (D + 1) + row];
+        float4 v[4];
+#pragma unroll
+        for (int i = 0; i < 4; i++) v[i] = *reinterpret_cast<const float4 *>(rec + ((4 * c + i) * ROWS + row) * 4);
+        const float mx = fmaxf(m, mk), mu = mx == -INFINITY ? 0.f : mx;
+        const float wa = ex2(m - mu), wb = ex2(mk - mu);  // 0 for a part that saw nothing
+        m = mx;
+        l = l * wa + lk * wb;
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            acc[4 * i] = acc[4 * i] * wa + v[i].x * wb;
+            acc[4 * i + 1] = acc[4 * i + 1] * wa + v[i].y * wb;
+            acc[4 * i + 2] = acc[4 * i + 2] * wa + v[i].z * wb;
+            acc[4 * i + 3] = acc[4 * i + 3] * wa + v[i].w * wb;
         }
     }
+    const long long o = (static_cast<long long>(r.q0) + tok) * p.Hq + what.y * p.G + row % p.G;
+    const float by = l == 0.f ? 0.f : a.out_scale / l;
+    uint32_t w[8];
+#pragma unroll
+    for (int i = 0; i < 8; i++) w[i] = pack2(to16(acc[2 * i] * by, p.bf16), to16(acc[2 * i + 1] * by, p.bf16));
+    uint4 *dst = reinterpret_cast<uint4 *>(a.out + o * D + 16 * c);
+    dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
+    dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
+    if (c == 0 && a.lse) a.lse[o] = l == 0.f ? -INFINITY : (m - LIFT + log2f(l)) * LN2;
 }
 
 template <int D>
@@ -756,6 +779,9 @@ int launch_as(const PagesAttnArgs &a, int grid, cudaStream_t st) {
     const cudaError_t e = cudaFuncSetAttribute(attn_prompt<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return static_cast<int>(e);
     attn_prompt<D><<<grid, THREADS, smem, st>>>(a);
+    const cudaError_t e1 = cudaGetLastError();
+    if (e1 != cudaSuccess) return static_cast<int>(e1);
+    join_parts<D><<<dim3(grid, D / 16), ROWS, 0, st>>>(a);
     return static_cast<int>(cudaGetLastError());
 }
 
