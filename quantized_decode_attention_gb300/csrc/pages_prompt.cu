@@ -15,8 +15,8 @@
 //
 // Roles of the 16 warps.  Warps 0-3 and 4-7: softmax of tile 0 and 1, a thread a query
 // row: scores come from tensor memory, weights go back there as binary16 in the place of
-// the scores, the accumulator is rescaled in place when a maximum grows by more than
-// 2^8.  Warps 8-11: codes of 128 keys and values from the pages to binary16 operands in
+// the scores, the accumulator is rescaled in place when a logit passes the maximum by
+// more than 2^8.  Warps 8-11: codes of 128 keys and values from the pages to binary16 operands in
 // shared memory (exact), two stages deep.  Warp 12: one thread issues all products,
 // S = Q K^T and O += P V (P from tensor memory), tile by tile in turn, so that one tile's
 // softmax runs beside the other's products.
@@ -35,7 +35,7 @@ constexpr uint64_t WAIT_NS = 2000000000ull;  // longest wait for another role
 constexpr float SLACK = 8.f, LIFT = 7.f;     // log2 units
 constexpr int TILE = 128, ROWS = 2 * TILE;   // query rows of a tile, of a unit
 constexpr int KEYS = 128;                    // keys at a time
-constexpr int UNIT_COST = 256, MIN_SHARE = 1024;  // tokens: of a unit's beginning and end; that make a CTA worth its parts
+constexpr int UNIT_COST = 512, MIN_SHARE = 1024;  // tokens: of a unit's beginning and end; that make a CTA worth its parts
 constexpr int THREADS = 512;
 
 // ---- tensor memory and tensor cores --------------------------------------------------------
@@ -85,8 +85,10 @@ __device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::
 __device__ __forceinline__ void tc_commit(uint64_t *bar) {
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n" ::"r"(smem_u32(bar)) : "memory");
 }
+// The warp arrives, once for all its lanes' work before it.
 __device__ __forceinline__ void mbar_arrive(uint64_t *bar) {
-    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];\n" ::"r"(smem_u32(bar)) : "memory");
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];\n" ::"r"(smem_u32(bar)) : "memory");
 }
 // Descriptor of a K-major operand with 128-byte swizzle (8 rows of 128 bytes are 1024
 // bytes): its low word holds the address in units of 16 bytes, so that an operand n bytes
@@ -318,13 +320,13 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prompt(PagesAttnArgs a) {
     if (tid == 0) {
 #pragma unroll
         for (int i = 0; i < 2; i++) {
-            mbar_init(&sh.q_full[i], TILE);
-            mbar_init(&sh.k_full[i], 128);
+            mbar_init(&sh.q_full[i], 4);
+            mbar_init(&sh.k_full[i], 4);
             mbar_init(&sh.k_empty[i], 1);
-            mbar_init(&sh.v_full[i], 128);
+            mbar_init(&sh.v_full[i], 4);
             mbar_init(&sh.v_empty[i], 1);
             mbar_init(&sh.s_full[i], 1);
-            mbar_init(&sh.p_full[i], TILE);
+            mbar_init(&sh.p_full[i], 4);
             mbar_init(&sh.o_full[i], 1);
         }
         fence_mbar_init();
@@ -396,6 +398,9 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prompt(PagesAttnArgs a) {
             atomicOr(p.status, PST_TIMEOUT);
         }
     };
+    // registers move from the warps that need few (of 512 x 128: 384 x 144 + 128 x 80 = 65536)
+    if (warp < 12) asm volatile("setmaxnreg.inc.sync.aligned.u32 144;\n");
+    else asm volatile("setmaxnreg.dec.sync.aligned.u32 80;\n");
     constexpr int REC = ROWS * (D + 2);  // a part: accumulators [D / 4][ROWS][4], maxima [ROWS], sums [ROWS]
 
     if (warp < 8) {
@@ -464,6 +469,17 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prompt(PagesAttnArgs a) {
                         tmem_st32(s_at + c, s);
                     }
                     tmem_wait_st();
+                }
+                if (k == g.t0) {  // m from all of the first tile: raising it later costs a pass over the accumulator
+                    float z = -INFINITY;
+#pragma unroll 1
+                    for (int c = 0; c < KEYS; c += 32) {
+                        uint32_t s[32];
+                        tmem_ld32(s_at + c, s);
+                        tmem_wait_ld(s);
+                        z = fmaxf(z, top_of(s));
+                    }
+                    row_s.m = z == -INFINITY ? -INFINITY : z * row_s.f;
                 }
                 // 32 keys at a time, the next 32 on their way; their weights take the place of scores that were read
                 uint32_t sa[32], sb[32];
