@@ -206,14 +206,21 @@ struct RowState {
         }
     }
 };
+__device__ __forceinline__ float max3(uint32_t a, uint32_t b, uint32_t c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;\n" : "=f"(r) : "f"(__uint_as_float(a)), "f"(__uint_as_float(b)), "f"(__uint_as_float(c)));
+    return r;
+}
 __device__ __forceinline__ float top_of(const uint32_t (&s)[32]) {
     float t[4];
 #pragma unroll
     for (int i = 0; i < 4; i++) {
-        t[i] = fmaxf(__uint_as_float(s[8 * i]), __uint_as_float(s[8 * i + 1]));
-#pragma unroll
-        for (int j = 2; j < 8; j += 2) t[i] = fmaxf(t[i], fmaxf(__uint_as_float(s[8 * i + j]), __uint_as_float(s[8 * i + j + 1])));
+        t[i] = max3(s[8 * i], s[8 * i + 1], s[8 * i + 2]);
+        t[i] = max3(__float_as_uint(t[i]), s[8 * i + 3], s[8 * i + 4]);
+        t[i] = max3(__float_as_uint(t[i]), s[8 * i + 5], s[8 * i + 6]);
     }
+    t[0] = max3(__float_as_uint(t[0]), s[7], s[15]);
+    t[1] = max3(__float_as_uint(t[1]), s[23], s[31]);
     return fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3]));
 }
 
@@ -563,6 +570,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prompt(PagesAttnArgs a) {
         const int dt = tid - 256, kg = dt & 15, c16 = dt >> 4;
         const bool has_v = c16 < D / 16;
         const int shift = 31 - __clz(p.P), in_page = p.P - 1, b = p.blk, b_shift = 31 - __clz(b), in_block = b - 1;  // powers of two
+        const unsigned page_stride = static_cast<unsigned>(p.Hkv) * p.page_bytes;
         // this thread's rows in the operands, the row's swizzle in place: piece c is at that address ^ 16 c
         const uint32_t k_row = smem_u32(sh.k[0]) + swizzled(dt, 0);
         uint32_t v_row[4];
@@ -580,54 +588,48 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prompt(PagesAttnArgs a) {
             const Segment g = find_segment<D>(sh, a, tb, x, c1);
             const PageRow &r = g.u.r;
             x = g.u.end;
-            auto number = [&](int at) -> int {  // page of position `at`, or none
-                if (at >= r.len || r.row < 0) return -1;
-                return p.table[static_cast<long long>(r.row) * p.M + (at >> shift)];
+            // page numbers: of the row's last page for positions behind it (len > 0: there is one)
+            const int *pages = p.table + static_cast<long long>(r.row) * p.M;
+            const int last = (r.len - 1) >> shift;
+            auto number = [&](int at) -> int { return pages[(at >> shift) < last ? at >> shift : last]; };
+            const uint8_t *of_head = p.pages + static_cast<long long>(g.u.head) * p.page_bytes;
+            auto block_of = [&](int &id, int at) -> const uint8_t * {  // the block that holds position `at`
+                if (static_cast<unsigned>(id) >= static_cast<unsigned>(p.n_pages)) {
+                    atomicOr(p.status, PST_TABLE);
+                    id = 0;
+                }
+                return of_head + static_cast<unsigned long long>(static_cast<unsigned>(id)) * page_stride + ((at & in_page) >> b_shift) * B::size(b);
             };
-            auto checked = [&](int id, int at) -> int {
-                if (at >= r.len || r.row < 0 || (id >= 0 && id < p.n_pages)) return id;
-                atomicOr(p.status, PST_TABLE);
-                return -1;
-            };
+            // what a position that is not there reads does not count: its scale is taken as 0
             auto load = [&](Packed &w, int tile, int idk, int idv) {
                 const int key = tile * KEYS + dt, tok = tile * KEYS + 8 * kg;
-                idk = checked(idk, key);
-                idv = checked(idv, tok);
+                const int uk = key & in_block, uv = tok & in_block;
+                const uint8_t *kb = block_of(idk, key);
 #pragma unroll
-                for (int i = 0; i < D / 32; i++) w.k[i] = make_uint4(0, 0, 0, 0);
-#pragma unroll
-                for (int i = 0; i < 4; i++) w.v[i] = make_uint4(0, 0, 0, 0);
-                w.ks = w.vs = make_uint2(0, 0);
-                if (idk >= 0) {
-                    const int u = key & in_page, ub = u & in_block;
-                    const uint8_t *blk = page_ptr(p, idk, g.u.head) + (u >> b_shift) * B::size(b);
-#pragma unroll
-                    for (int i = 0; i < D / 32; i++) w.k[i] = *reinterpret_cast<const uint4 *>(blk + ub * (D / 2) + 16 * i);
-                    if (D == 128) w.ks = *reinterpret_cast<const uint2 *>(blk + B::ks(b) + ub * (D / 16));
-                    else w.ks.x = *reinterpret_cast<const uint32_t *>(blk + B::ks(b) + ub * (D / 16));
+                for (int i = 0; i < D / 32; i++) w.k[i] = *reinterpret_cast<const uint4 *>(kb + uk * (D / 2) + 16 * i);
+                if (D == 128) {
+                    w.ks = *reinterpret_cast<const uint2 *>(kb + B::ks(b) + uk * (D / 16));
+                } else {
+                    w.ks.x = *reinterpret_cast<const uint32_t *>(kb + B::ks(b) + uk * (D / 16));
+                    w.ks.y = 0;
                 }
-                if (has_v && idv >= 0) {
-                    const int u = tok & in_page, ub = u & in_block;
-                    const uint8_t *blk = page_ptr(p, idv, g.u.head) + (u >> b_shift) * B::size(b);
+                if (key >= r.len) w.ks = make_uint2(0, 0);
+                if (has_v) {
+                    const uint8_t *vb = block_of(idv, tok);
 #pragma unroll
-                    for (int i = 0; i < 4; i++) w.v[i] = *reinterpret_cast<const uint4 *>(blk + B::vc(b) + B::vcode(ub, c16) + 16 * i);
-                    w.vs = *reinterpret_cast<const uint2 *>(blk + B::vs(b) + B::vscale(ub, c16));
+                    for (int i = 0; i < 4; i++) w.v[i] = *reinterpret_cast<const uint4 *>(vb + B::vc(b) + B::vcode(uv, c16) + 16 * i);
+                    w.vs = *reinterpret_cast<const uint2 *>(vb + B::vs(b) + B::vscale(uv, c16));
                 }
             };
-            // codes one tile ahead, page numbers two
-            Packed cur, nxt;
-            if (g.t0 < g.t1) load(cur, g.t0, number(g.t0 * KEYS + dt), number(g.t0 * KEYS + 8 * kg));
-            int idk = number((g.t0 + 1) * KEYS + dt), idv = number((g.t0 + 1) * KEYS + 8 * kg);
-            for (int k = g.t0; k < g.t1; k++, it++) {
-                if (k + 1 < g.t1) {
-                    load(nxt, k + 1, idk, idv);
-                    idk = number((k + 2) * KEYS + dt);
-                    idv = number((k + 2) * KEYS + 8 * kg);
-                }
+            // one tile's operands
+            auto unpack = [&](const Packed &cur, int k) {
                 const int st = it & 1;
                 const unsigned free = ((it >> 1) + 1) & 1;
                 if (it >= 2) wait(&sh.k_empty[st], free);
-                if (late) break;
+                if (__any_sync(FULL, late)) {
+                    late = true;
+                    return;
+                }
 #pragma unroll
                 for (int i = 0; i < D / 16; i++) {  // a scale block: two 16-byte pieces
                     const uint32_t sb = (i < 4 ? cur.ks.x : cur.ks.y) >> (8 * (i & 3)) & 0xffu;
@@ -645,7 +647,10 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prompt(PagesAttnArgs a) {
                 fence_proxy_async();
                 mbar_arrive(&sh.k_full[st]);
                 if (it >= 2) wait(&sh.v_empty[st], free);
-                if (late) break;
+                if (__any_sync(FULL, late)) {
+                    late = true;
+                    return;
+                }
                 if (has_v) {
                     uint32_t sv[4];
 #pragma unroll
@@ -671,7 +676,25 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prompt(PagesAttnArgs a) {
                 }
                 fence_proxy_async();
                 mbar_arrive(&sh.v_full[st]);
-                cur = nxt;
+                it++;
+            };
+            // codes one tile ahead, page numbers two
+            Packed even, odd;
+            int idk = number(g.t0 * KEYS + dt), idv = number(g.t0 * KEYS + 8 * kg);
+            auto fetch = [&](Packed &w, int k) {
+                if (k >= g.t1) return;
+                load(w, k, idk, idv);
+                idk = number((k + 1) * KEYS + dt);
+                idv = number((k + 1) * KEYS + 8 * kg);
+            };
+            fetch(even, g.t0);
+            for (int k = g.t0; k < g.t1; k += 2) {
+                fetch(odd, k + 1);
+                unpack(even, k);
+                if (k + 1 >= g.t1 || late) break;
+                fetch(even, k + 2);
+                unpack(odd, k + 1);
+                if (late) break;
             }
         }
     } else if (warp == 12 && lane == 0) {
