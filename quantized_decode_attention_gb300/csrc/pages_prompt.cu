@@ -32,7 +32,8 @@ namespace {
 
 constexpr float LN2 = 0.69314718055994530942f;
 constexpr uint64_t WAIT_NS = 2000000000ull;  // longest wait for another role
-constexpr float SLACK = 8.f, LIFT = 7.f;     // log2 units
+constexpr float LIFT = 7.f;       // log2 units: weights are 2^LIFT at a logit of m ...
+constexpr float MOST = 32768.f;   // ... and may grow to 2^15 (a logit 2^8 over m) before m is raised
 constexpr int TILE = 128, ROWS = 2 * TILE;   // query rows of a tile, of a unit
 constexpr int KEYS = 128;                    // keys at a time
 constexpr int UNIT_COST = 512, MIN_SHARE = 1024;  // tokens: of a unit's beginning and end; that make a CTA worth its parts
@@ -89,6 +90,24 @@ __device__ __forceinline__ void tc_commit(uint64_t *bar) {
 __device__ __forceinline__ void mbar_arrive(uint64_t *bar) {
     __syncwarp();
     if ((threadIdx.x & 31) == 0) asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];\n" ::"r"(smem_u32(bar)) : "memory");
+}
+// Wait for phase `parity` of an mbarrier, for `limit_ns` at most.  The hand-overs here are
+// short and frequent: no hint to sleep long, and the clock is seldom looked at.
+__device__ __forceinline__ bool mbar_spin(uint64_t *bar, unsigned parity, uint64_t limit_ns) {
+    const uint32_t addr = smem_u32(bar);
+    uint64_t t0 = 0;
+    for (unsigned it = 0;; ++it) {
+        uint32_t done;
+        asm volatile("{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
+                     : "=r"(done)
+                     : "r"(addr), "r"(parity)
+                     : "memory");
+        if (done) return true;
+        if ((it & 1023u) == 0) {
+            if (it == 0) t0 = global_ns();
+            else if (global_ns() - t0 > limit_ns) return false;
+        }
+    }
 }
 // Descriptor of a K-major operand with 128-byte swizzle (8 rows of 128 bytes are 1024
 // bytes): its low word holds the address in units of 16 bytes, so that an operand n bytes
@@ -153,12 +172,11 @@ struct RowState {
     float f, m;
     uint64_t l[2];
     __device__ __forceinline__ float mu() const { return m == -INFINITY ? 0.f : m - LIFT; }  // what a logit loses before exp2
-    __device__ __forceinline__ float limit() const { return m == -INFINITY ? -INFINITY : m + SLACK; }
     __device__ __forceinline__ float sum() const {
         const float2 a = both(l[0]), b = both(l[1]);
         return (a.x + a.y) + (b.x + b.y);
     }
-    // A logit z passed the limit (in some row of the warp): raise m; the sums, the accumulator (n_o columns at o_at)
+    // A weight grew too large (in some row of the warp), z is the largest logit: raise m; the sums, the accumulator (n_o columns at o_at)
     // and this tile's weights so far (n_p columns of two at p_at) follow.
     template <int D>
     __device__ void raise(float z, bool has_o, uint32_t o_at, int n_p, uint32_t p_at) {
@@ -193,34 +211,28 @@ struct RowState {
             tmem_st16(p_at + c, s);
         }
     }
-    // Scores of 32 keys -> weights, two a word.
-    __device__ __forceinline__ void weigh(const uint32_t (&s)[32], uint32_t (&w)[16]) {
+    // Scores of 32 keys -> weights, two a word, and their sums.
+    __device__ __forceinline__ void weigh(const uint32_t (&s)[32], uint32_t (&w)[16], uint64_t (&c)[2]) const {
         const float lose = -mu();
         const uint64_t ff = two(f, f), mm = two(lose, lose);
+        c[0] = c[1] = 0;
 #pragma unroll
         for (int i = 0; i < 16; i++) {
             const float2 e = both(fma2(two(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])), ff, mm));
             const float a = ex2(e.x), b = ex2(e.y);
-            l[i & 1] = add2(l[i & 1], two(a, b));
+            c[i & 1] = add2(c[i & 1], two(a, b));
             w[i] = half2_of(a, b);
         }
     }
 };
-__device__ __forceinline__ float max3(uint32_t a, uint32_t b, uint32_t c) {
-    float r;
-    asm("max.f32 %0, %1, %2, %3;\n" : "=f"(r) : "f"(__uint_as_float(a)), "f"(__uint_as_float(b)), "f"(__uint_as_float(c)));
-    return r;
-}
 __device__ __forceinline__ float top_of(const uint32_t (&s)[32]) {
     float t[4];
 #pragma unroll
     for (int i = 0; i < 4; i++) {
-        t[i] = max3(s[8 * i], s[8 * i + 1], s[8 * i + 2]);
-        t[i] = max3(__float_as_uint(t[i]), s[8 * i + 3], s[8 * i + 4]);
-        t[i] = max3(__float_as_uint(t[i]), s[8 * i + 5], s[8 * i + 6]);
+        t[i] = fmaxf(__uint_as_float(s[8 * i]), __uint_as_float(s[8 * i + 1]));
+#pragma unroll
+        for (int j = 2; j < 8; j += 2) t[i] = fmaxf(t[i], fmaxf(__uint_as_float(s[8 * i + j]), __uint_as_float(s[8 * i + j + 1])));
     }
-    t[0] = max3(__float_as_uint(t[0]), s[7], s[15]);
-    t[1] = max3(__float_as_uint(t[1]), s[23], s[31]);
     return fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3]));
 }
 
@@ -398,9 +410,11 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prompt(PagesAttnArgs a) {
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = sh.tmem;
-    bool late = false;  // a wait ran out
+    // After a wait that ran out a thread waits no more: every role goes through its (finite)
+    // loops, in step with its warp, and the status says that the outputs are not valid.
+    bool late = false;
     auto wait = [&](uint64_t *bar, unsigned parity) {
-        if (!late && !mbar_wait(bar, parity, WAIT_NS)) {
+        if (!late && !mbar_spin(bar, parity, WAIT_NS)) {
             late = true;
             atomicOr(p.status, PST_TIMEOUT);
         }
@@ -416,7 +430,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prompt(PagesAttnArgs a) {
         const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;  // 32 lanes of tensor memory
         const uint32_t s_at = tmem + lanes + t * KEYS, o_at = tmem + lanes + 2 * KEYS + t * D;
         unsigned runs = 0, it = 0;
-        for (long long x = c0; x < c1 && !late;) {
+        for (long long x = c0; x < c1;) {
             const Segment g = find_segment<D>(sh, a, tb, x, c1);
             const PageRow &r = g.u.r;
             x = g.u.end;
@@ -458,10 +472,6 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prompt(PagesAttnArgs a) {
             const int least = __reduce_min_sync(FULL, pos);
             for (int k = g.t0; k < g.t1; k++, it++) {
                 wait(&sh.s_full[t], it & 1);
-                if (__any_sync(FULL, late)) {
-                    late = true;
-                    break;
-                }
                 tc_fence_after();
                 const int key0 = k * KEYS;
                 const bool tail = key0 + KEYS - 1 > least;
@@ -477,7 +487,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prompt(PagesAttnArgs a) {
                     }
                     tmem_wait_st();
                 }
-                if (k == g.t0) {  // m from all of the first tile: raising it later costs a pass over the accumulator
+                if (k == g.t0) {  // m from all of the first tile (a row that sees nothing of it sees nothing later)
                     float z = -INFINITY;
 #pragma unroll 1
                     for (int c = 0; c < KEYS; c += 32) {
@@ -491,17 +501,19 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prompt(PagesAttnArgs a) {
                 // 32 keys at a time, the next 32 on their way; their weights take the place of scores that were read
                 uint32_t sa[32], sb[32];
                 auto chunk = [&](uint32_t (&s)[32], int c) {
-                    // the weights do not wait for the maximum: it seldom raises m, and then they are taken again
+                    // Weights are positive: one over MOST shows in their sum, so that the maximum is
+                    // only sought where the sum passes that (or, no harm, many smaller weights do).
                     uint32_t w[16];
-                    const uint64_t l0 = row_s.l[0], l1 = row_s.l[1];
-                    row_s.weigh(s, w);
-                    const float top = top_of(s), z = top == -INFINITY ? -INFINITY : top * row_s.f;
-                    if (__any_sync(FULL, z > row_s.limit())) {
-                        row_s.l[0] = l0;
-                        row_s.l[1] = l1;
-                        row_s.raise<D>(z, k > g.t0, o_at, 16 * c, s_at);
-                        row_s.weigh(s, w);
+                    uint64_t sum[2];
+                    row_s.weigh(s, w, sum);
+                    const float2 x0 = both(add2(sum[0], sum[1]));
+                    if (__any_sync(FULL, x0.x + x0.y > MOST)) {
+                        const float top = top_of(s);
+                        row_s.raise<D>(top == -INFINITY ? -INFINITY : top * row_s.f, k > g.t0, o_at, 16 * c, s_at);
+                        row_s.weigh(s, w, sum);
                     }
+                    row_s.l[0] = add2(row_s.l[0], sum[0]);
+                    row_s.l[1] = add2(row_s.l[1], sum[1]);
                     tmem_st16(s_at + 16 * c, w);
                 };
                 tmem_ld32(s_at, sa);
@@ -518,14 +530,9 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prompt(PagesAttnArgs a) {
                 tc_fence_before();
                 mbar_arrive(&sh.p_full[t]);
             }
-            if (late) break;
             if (g.t0 < g.t1) {
                 wait(&sh.o_full[t], runs & 1);
                 runs++;
-                if (__any_sync(FULL, late)) {
-                    late = true;
-                    break;
-                }
                 tc_fence_after();
             }
             const long long o = (static_cast<long long>(r.q0) + tok) * p.Hq + g.u.head * p.G + gq;
@@ -570,7 +577,6 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prompt(PagesAttnArgs a) {
         const int dt = tid - 256, kg = dt & 15, c16 = dt >> 4;
         const bool has_v = c16 < D / 16;
         const int shift = 31 - __clz(p.P), in_page = p.P - 1, b = p.blk, b_shift = 31 - __clz(b), in_block = b - 1;  // powers of two
-        const unsigned page_stride = static_cast<unsigned>(p.Hkv) * p.page_bytes;
         // this thread's rows in the operands, the row's swizzle in place: piece c is at that address ^ 16 c
         const uint32_t k_row = smem_u32(sh.k[0]) + swizzled(dt, 0);
         uint32_t v_row[4];
@@ -584,52 +590,57 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prompt(PagesAttnArgs a) {
             uint2 ks, vs;
         };
         unsigned it = 0;
-        for (long long x = c0; x < c1 && !late;) {
+        for (long long x = c0; x < c1;) {
             const Segment g = find_segment<D>(sh, a, tb, x, c1);
             const PageRow &r = g.u.r;
             x = g.u.end;
-            // page numbers: of the row's last page for positions behind it (len > 0: there is one)
-            const int *pages = p.table + static_cast<long long>(r.row) * p.M;
-            const int last = (r.len - 1) >> shift;
-            auto number = [&](int at) -> int { return pages[(at >> shift) < last ? at >> shift : last]; };
-            const uint8_t *of_head = p.pages + static_cast<long long>(g.u.head) * p.page_bytes;
-            auto block_of = [&](int &id, int at) -> const uint8_t * {  // the block that holds position `at`
-                if (static_cast<unsigned>(id) >= static_cast<unsigned>(p.n_pages)) {
-                    atomicOr(p.status, PST_TABLE);
-                    id = 0;
-                }
-                return of_head + static_cast<unsigned long long>(static_cast<unsigned>(id)) * page_stride + ((at & in_page) >> b_shift) * B::size(b);
+            auto number = [&](int at) -> int {  // page of position `at`, or none
+                if (at >= r.len || r.row < 0) return -1;
+                return p.table[static_cast<long long>(r.row) * p.M + (at >> shift)];
             };
-            // what a position that is not there reads does not count: its scale is taken as 0
+            auto checked = [&](int id, int at) -> int {
+                if (at >= r.len || r.row < 0 || (id >= 0 && id < p.n_pages)) return id;
+                atomicOr(p.status, PST_TABLE);
+                return -1;
+            };
             auto load = [&](Packed &w, int tile, int idk, int idv) {
                 const int key = tile * KEYS + dt, tok = tile * KEYS + 8 * kg;
-                const int uk = key & in_block, uv = tok & in_block;
-                const uint8_t *kb = block_of(idk, key);
+                idk = checked(idk, key);
+                idv = checked(idv, tok);
 #pragma unroll
-                for (int i = 0; i < D / 32; i++) w.k[i] = *reinterpret_cast<const uint4 *>(kb + uk * (D / 2) + 16 * i);
-                if (D == 128) {
-                    w.ks = *reinterpret_cast<const uint2 *>(kb + B::ks(b) + uk * (D / 16));
-                } else {
-                    w.ks.x = *reinterpret_cast<const uint32_t *>(kb + B::ks(b) + uk * (D / 16));
-                    w.ks.y = 0;
+                for (int i = 0; i < D / 32; i++) w.k[i] = make_uint4(0, 0, 0, 0);
+#pragma unroll
+                for (int i = 0; i < 4; i++) w.v[i] = make_uint4(0, 0, 0, 0);
+                w.ks = w.vs = make_uint2(0, 0);
+                if (idk >= 0) {
+                    const int u = key & in_page, ub = u & in_block;
+                    const uint8_t *blk = page_ptr(p, idk, g.u.head) + (u >> b_shift) * B::size(b);
+#pragma unroll
+                    for (int i = 0; i < D / 32; i++) w.k[i] = *reinterpret_cast<const uint4 *>(blk + ub * (D / 2) + 16 * i);
+                    if (D == 128) w.ks = *reinterpret_cast<const uint2 *>(blk + B::ks(b) + ub * (D / 16));
+                    else w.ks.x = *reinterpret_cast<const uint32_t *>(blk + B::ks(b) + ub * (D / 16));
                 }
-                if (key >= r.len) w.ks = make_uint2(0, 0);
-                if (has_v) {
-                    const uint8_t *vb = block_of(idv, tok);
+                if (has_v && idv >= 0) {
+                    const int u = tok & in_page, ub = u & in_block;
+                    const uint8_t *blk = page_ptr(p, idv, g.u.head) + (u >> b_shift) * B::size(b);
 #pragma unroll
-                    for (int i = 0; i < 4; i++) w.v[i] = *reinterpret_cast<const uint4 *>(vb + B::vc(b) + B::vcode(uv, c16) + 16 * i);
-                    w.vs = *reinterpret_cast<const uint2 *>(vb + B::vs(b) + B::vscale(uv, c16));
+                    for (int i = 0; i < 4; i++) w.v[i] = *reinterpret_cast<const uint4 *>(blk + B::vc(b) + B::vcode(ub, c16) + 16 * i);
+                    w.vs = *reinterpret_cast<const uint2 *>(blk + B::vs(b) + B::vscale(ub, c16));
                 }
             };
-            // one tile's operands
-            auto unpack = [&](const Packed &cur, int k) {
+            // codes one tile ahead, page numbers two
+            Packed cur, nxt;
+            if (g.t0 < g.t1) load(cur, g.t0, number(g.t0 * KEYS + dt), number(g.t0 * KEYS + 8 * kg));
+            int idk = number((g.t0 + 1) * KEYS + dt), idv = number((g.t0 + 1) * KEYS + 8 * kg);
+            for (int k = g.t0; k < g.t1; k++, it++) {
+                if (k + 1 < g.t1) {
+                    load(nxt, k + 1, idk, idv);
+                    idk = number((k + 2) * KEYS + dt);
+                    idv = number((k + 2) * KEYS + 8 * kg);
+                }
                 const int st = it & 1;
                 const unsigned free = ((it >> 1) + 1) & 1;
                 if (it >= 2) wait(&sh.k_empty[st], free);
-                if (__any_sync(FULL, late)) {
-                    late = true;
-                    return;
-                }
 #pragma unroll
                 for (int i = 0; i < D / 16; i++) {  // a scale block: two 16-byte pieces
                     const uint32_t sb = (i < 4 ? cur.ks.x : cur.ks.y) >> (8 * (i & 3)) & 0xffu;
@@ -647,10 +658,6 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prompt(PagesAttnArgs a) {
                 fence_proxy_async();
                 mbar_arrive(&sh.k_full[st]);
                 if (it >= 2) wait(&sh.v_empty[st], free);
-                if (__any_sync(FULL, late)) {
-                    late = true;
-                    return;
-                }
                 if (has_v) {
                     uint32_t sv[4];
 #pragma unroll
@@ -676,25 +683,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prompt(PagesAttnArgs a) {
                 }
                 fence_proxy_async();
                 mbar_arrive(&sh.v_full[st]);
-                it++;
-            };
-            // codes one tile ahead, page numbers two
-            Packed even, odd;
-            int idk = number(g.t0 * KEYS + dt), idv = number(g.t0 * KEYS + 8 * kg);
-            auto fetch = [&](Packed &w, int k) {
-                if (k >= g.t1) return;
-                load(w, k, idk, idv);
-                idk = number((k + 1) * KEYS + dt);
-                idv = number((k + 1) * KEYS + 8 * kg);
-            };
-            fetch(even, g.t0);
-            for (int k = g.t0; k < g.t1; k += 2) {
-                fetch(odd, k + 1);
-                unpack(even, k);
-                if (k + 1 >= g.t1 || late) break;
-                fetch(even, k + 2);
-                unpack(odd, k + 1);
-                if (late) break;
+                cur = nxt;
             }
         }
     } else if (warp == 12 && lane == 0) {
@@ -716,7 +705,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prompt(PagesAttnArgs a) {
                 mma_smem(s_at[t], q_at[t] + (i >> 2) * (TILE * 8) + (i & 3) * 2, kb + (i >> 2) * (KEYS * 8) + (i & 3) * 2, product(KEYS), i > 0);
             tc_commit(&sh.s_full[t]);
         };
-        for (long long x = c0; x < c1 && !late;) {
+        for (long long x = c0; x < c1;) {
             const Segment g = find_segment<D>(sh, a, tb, x, c1);
             x = g.u.end;
             if (g.t0 >= g.t1) continue;
@@ -724,21 +713,18 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prompt(PagesAttnArgs a) {
 #pragma unroll
             for (int t = 0; t < 2; t++) {
                 wait(&sh.q_full[t], runs & 1);
-                if (late) break;
                 tc_fence_after();
                 scores(t, it & 1);
             }
-            if (late) break;
             tc_commit(&sh.k_empty[it & 1]);
             runs++;
-            for (int k = g.t0; k < g.t1 && !late; k++, it++) {
+            for (int k = g.t0; k < g.t1; k++, it++) {
                 const int st = it & 1, next = (it + 1) & 1;
                 const uint32_t vb = v_at + st * STAGE;
 #pragma unroll
                 for (int t = 0; t < 2; t++) {
                     wait(&sh.p_full[t], it & 1);
                     if (t == 0) wait(&sh.v_full[st], it >> 1 & 1);
-                    if (late) break;
                     tc_fence_after();
 #pragma unroll
                     for (int i = 0; i < KEYS / 16; i++)
@@ -746,7 +732,6 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prompt(PagesAttnArgs a) {
                     if (t == 1) tc_commit(&sh.v_empty[st]);
                     if (k + 1 < g.t1) {
                         if (t == 0) wait(&sh.k_full[next], (it + 1) >> 1 & 1);
-                        if (late) break;
                         if (t == 0) tc_fence_after();
                         scores(t, next);
                         if (t == 1) tc_commit(&sh.k_empty[next]);
