@@ -2,6 +2,8 @@
 // call, the 4-bit float and scale conversions, the byte layout of a page.
 #pragma once
 
+#include <atomic>
+
 #include <cuda_runtime.h>
 
 #include "common.cuh"
@@ -21,6 +23,20 @@ struct PageBlock {
     __device__ static int vcode(int t, int c16) { return (((t >> 3) * (D / 16) + c16) * 4 + ((t >> 1) & 3)) * 16; }
     __device__ static int vscale(int t, int c16) { return (((t >> 3) * (D / 16) + c16) * 4 + ((t >> 1) & 3)) * 2 + (t & 1); }
 };
+
+// ---- launches -------------------------------------------------------------------------
+// Let kernel K take `bytes` of shared memory: once for each device and kernel (0 or a cudaError_t).
+template <auto K>
+int allow_shared(int bytes) {
+    static std::atomic<bool> done[64];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return static_cast<int>(e);
+    if (dev < 64 && done[dev].load(std::memory_order_relaxed)) return 0;
+    e = cudaFuncSetAttribute(K, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess && dev < 64) done[dev].store(true, std::memory_order_relaxed);
+    return static_cast<int>(e);
+}
 
 // ---- rows ----------------------------------------------------------------------------
 struct PageRow {

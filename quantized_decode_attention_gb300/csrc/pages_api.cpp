@@ -3,6 +3,7 @@
 // cross the C ABI.
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
@@ -52,10 +53,13 @@ dq_status check_cfg(const dq_pages_config *c) {
 int page_bytes(const dq_pages_config *c) { return c->page_size * c->head_dim * 9 / 8; }
 int sum_bytes(const dq_pages_config *c) { return 2 * c->head_dim + 16; }
 
-int device_sms() {
+int device_sms() {  // of the current device; looked up once for each device
+    static std::atomic<int> known[64];
     int dev = 0, sms = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+    if (dev < 64 && (sms = known[dev].load(std::memory_order_relaxed)) > 0) return sms;
     if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
+    if (dev < 64) known[dev].store(sms, std::memory_order_relaxed);
     return sms;
 }
 
@@ -241,7 +245,8 @@ dq_status dq_pages_select(const dq_pages_config *cfg, const dq_pages_buffers *bu
         return fail(DQ_EALIGN, "q not 16-byte aligned, or a stride is no multiple of 8 elements");
     if (!aligned4(sel)) return fail(DQ_EALIGN, "sel not aligned to 4 bytes");
     if (n_sel < 1 || n_sel > DQ_PAGES_MAX_SELECT) return fail(DQ_EINVAL, "n_sel outside [1, %d]", DQ_PAGES_MAX_SELECT);
-    if (cfg->max_pages_per_seq > 16384) return fail(DQ_EUNSUPPORTED, "select: more than 16384 pages in a row");
+    if (cfg->max_pages_per_seq > dq::PAGES_SELECT_MAX)
+        return fail(DQ_EUNSUPPORTED, "select: more than %d pages in a row", dq::PAGES_SELECT_MAX);
     if (keep_first < 0 || keep_last < 0 || static_cast<long long>(keep_first) + keep_last > n_sel)
         return fail(DQ_EINVAL, "keep_first + keep_last must be in [0, n_sel]");
     a.q = static_cast<const uint16_t *>(q);

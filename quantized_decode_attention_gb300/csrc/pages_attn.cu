@@ -708,8 +708,7 @@ __global__ void __launch_bounds__(32 * NW, 1) attn_chunks(PagesAttnArgs a) {
 template <int D, int NT, int NW, bool TWO>
 int launch_as(const PagesAttnArgs &a, int grid, cudaStream_t st) {
     const int smem = static_cast<int>(sizeof(Shared<D, NT, NW>));
-    const cudaError_t e = cudaFuncSetAttribute(attn_chunks<D, NT, NW, TWO>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess) return static_cast<int>(e);
+    if (const int e = allow_shared<attn_chunks<D, NT, NW, TWO>>(smem)) return e;
     attn_chunks<D, NT, NW, TWO><<<grid, 32 * NW, smem, st>>>(a);
     return static_cast<int>(cudaGetLastError());
 }
@@ -724,9 +723,11 @@ int launch_pages_attention(const PagesAttnArgs &a, int num_sms, void *stream) {
     auto st = static_cast<cudaStream_t>(stream);
     const int grid = num_sms < PAGES_MAX_CTAS ? num_sms : PAGES_MAX_CTAS;
     if (!a.sel && a.r.max_new * a.p.G > PROMPT_ROWS) return launch_pages_prompt(a, grid, stream);
-    // 8 query rows fill one n tile; more share the conversions of two
+    // 8 query rows fill one n tile; more share the conversions of two, with fewer warps for their
+    // registers (8 x 4 tokens over 32768 at head_dim 64: 69 us with 8 warps, 59 with 12; the
+    // same 86 with either at 128, where mma.sync itself is the limit)
     if (a.r.max_new * a.p.G <= 8) return a.p.d == 128 ? launch_chunks<128, 1, 16>(a, grid, st) : launch_chunks<64, 1, 16>(a, grid, st);
-    return a.p.d == 128 ? launch_chunks<128, 2, 8>(a, grid, st) : launch_chunks<64, 2, 8>(a, grid, st);
+    return a.p.d == 128 ? launch_chunks<128, 2, 8>(a, grid, st) : launch_chunks<64, 2, 12>(a, grid, st);
 }
 
 }  // namespace dq

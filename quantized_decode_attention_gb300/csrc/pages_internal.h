@@ -39,6 +39,8 @@ struct PagesRows {
     int n_rows, n_tok, max_new;
 };
 
+constexpr int PAGES_SELECT_MAX = 16384;  // pages of a row that a choice is made among (a key of each in shared memory)
+
 // The int part of the workspace: [0] copies or moves of the last plan, [1] live pages
 // below which moves end, then three lists of n_pages.
 constexpr int PAGES_WS_HEAD = 16;

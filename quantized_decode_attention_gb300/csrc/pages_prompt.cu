@@ -800,8 +800,7 @@ __global__ void __launch_bounds__(ROWS) join_parts(PagesAttnArgs a) {
 template <int D>
 int launch_as(const PagesAttnArgs &a, int grid, cudaStream_t st) {
     const int smem = static_cast<int>(sizeof(Shared<D>)) + 1024;  // room to put it on a 1024-byte boundary
-    const cudaError_t e = cudaFuncSetAttribute(attn_prompt<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess) return static_cast<int>(e);
+    if (const int e = allow_shared<attn_prompt<D>>(smem)) return e;
     attn_prompt<D><<<grid, THREADS, smem, st>>>(a);
     const cudaError_t e1 = cudaGetLastError();
     if (e1 != cudaSuccess) return static_cast<int>(e1);

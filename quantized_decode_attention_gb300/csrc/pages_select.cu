@@ -213,8 +213,7 @@ __global__ void __launch_bounds__(SE_THREADS) select_kernel(PagesSelectArgs a) {
 template <int D>
 int launch_as(const PagesSelectArgs &a, int ctas, cudaStream_t st) {
     const int smem = a.p.M * 4;
-    cudaError_t e = cudaFuncSetAttribute(select_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess) return static_cast<int>(e);
+    if (const int e = allow_shared<select_kernel<D>>(PAGES_SELECT_MAX * 4)) return e;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(a.r.n_rows * ctas, a.p.Hkv);
     cfg.blockDim = dim3(SE_THREADS);
@@ -226,7 +225,7 @@ int launch_as(const PagesSelectArgs &a, int ctas, cudaStream_t st) {
     at.val.clusterDim.y = at.val.clusterDim.z = 1;
     cfg.attrs = &at;
     cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, select_kernel<D>, a);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, select_kernel<D>, a);
     return static_cast<int>(e != cudaSuccess ? e : cudaGetLastError());
 }
 

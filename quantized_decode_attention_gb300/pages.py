@@ -93,7 +93,12 @@ class PagePool:
         self.tensors = given
         self._bufs = PagesBuffers(*[given[n].data_ptr() for n in PAGES_BUFFER_NAMES])
         self._c, self._b = C.byref(self.cfg), C.byref(self._bufs)
-        self._lib = _load()
+        self._index, self._hkv, self._hq, self._d = self.device.index, cfg.n_kv_heads, cfg.n_q_heads, cfg.head_dim
+        self._scale = cfg.head_dim ** -0.5
+        L = _load()
+        self._f = {n: getattr(L, "dq_pages_" + n) for n in ("resize", "fork", "compact", "append", "read", "attention", "select")}
+        self._int32, self._float32 = torch.int32, torch.float32
+        self._current_device, self._raw_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
         self._torch = torch
 
     @classmethod
@@ -116,111 +121,107 @@ class PagePool:
     # ---- marshalling ----
     def _call(self, name, stream, *args):
         """The library call with this pool's device current and on `stream` (default: the current one)."""
-        cuda = self._torch.cuda
-        index = self.device.index
         if stream is None:
-            stream = cuda.current_stream(index)
-        s = stream if isinstance(stream, int) else stream.cuda_stream
-        f = getattr(self._lib, name)
-        if cuda.current_device() == index:
-            st = f(self._c, self._b, *args, s)
+            s = self._raw_stream(self._index)
         else:
-            with cuda.device(index):
-                st = f(self._c, self._b, *args, s)
+            s = stream if isinstance(stream, int) else stream.cuda_stream
+        if self._current_device() == self._index:
+            st = self._f[name](self._c, self._b, *args, s)
+        else:
+            with self._torch.cuda.device(self._index):
+                st = self._f[name](self._c, self._b, *args, s)
         if st:
             _raise(st)
 
     def _ints(self, t, name, n=None):
         if t is None:
             return None
-        if t.dtype != self._torch.int32 or t.device != self.device or not t.is_contiguous():
+        if t.dtype is not self._int32 or t.get_device() != self._index or not t.is_contiguous():
             raise ValueError(f"{name} must be a contiguous int32 tensor on {self.device}")
         if n is not None and t.numel() != n:
             raise ValueError(f"{name} has {t.numel()} values: {n} are wanted")
         return t.data_ptr()
 
     def _tokens(self, t, name, heads, n=None):
-        """A [n_tok, heads, head_dim] tensor with contiguous channels."""
-        if t.dtype != self._dtype or t.device != self.device:
+        """(pointer, n_tok, token stride, head stride) of a [n_tok, heads, head_dim] tensor with contiguous channels."""
+        if t.dtype is not self._dtype or t.get_device() != self._index:
             raise ValueError(f"{name} must be {self._dtype} on {self.device}")
-        if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != self.cfg.head_dim or (n is not None and t.shape[0] != n):
-            raise ValueError(f"{name} must be [{'n_tok' if n is None else n}, {heads}, {self.cfg.head_dim}] (got {tuple(t.shape)})")
-        if t.stride(2) != 1:
+        shape, stride = t.shape, t.stride()
+        if len(shape) != 3 or shape[1] != heads or shape[2] != self._d or (n is not None and shape[0] != n):
+            raise ValueError(f"{name} must be [{'n_tok' if n is None else n}, {heads}, {self._d}] (got {tuple(shape)})")
+        if stride[2] != 1:
             raise ValueError(f"{name}: channels must be contiguous")
-        return t.data_ptr()
+        return t.data_ptr(), shape[0], stride[0], stride[1]
+
+    def _whole(self, t, name):
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
 
     def _rows(self, rows, cu, n_tok, max_new):
         """(rows, cu, n_rows, n_tok, max_new) of a call with n_tok new tokens."""
         if cu is None:
-            n_rows = n_tok
-            max_new = 1 if max_new is None else max_new
-        else:
-            n_rows = cu.numel() - 1
-            max_new = n_tok if max_new is None else max_new
-        return self._ints(rows, "rows", n_rows), self._ints(cu, "cu"), n_rows, n_tok, max_new
+            return self._ints(rows, "rows", n_tok), None, n_tok, n_tok, 1 if max_new is None else max_new
+        n_rows = cu.numel() - 1
+        return self._ints(rows, "rows", n_rows), self._ints(cu, "cu"), n_rows, n_tok, n_tok if max_new is None else max_new
 
     # ---- operators ----
     def resize(self, rows, lens, stream=None):
         """Set rows' lengths (int32 [n]; rows None: 0, 1, ...): frees, copies shared last pages on write, grows.
         Length 0 frees a row."""
         n = lens.numel()
-        self._call("dq_pages_resize", stream, self._ints(rows, "rows", n), self._ints(lens, "lens"), n)
+        self._call("resize", stream, self._ints(rows, "rows", n), self._ints(lens, "lens"), n)
 
     def fork(self, src, dst, stream=None):
         """Empty rows dst[i] become second holders of rows src[i]'s pages."""
-        self._call("dq_pages_fork", stream, self._ints(src, "src"), self._ints(dst, "dst", src.numel()), src.numel())
+        self._call("fork", stream, self._ints(src, "src"), self._ints(dst, "dst", src.numel()), src.numel())
 
     def compact(self, stream=None):
         """Move live pages down until they are the pool's lowest."""
-        self._call("dq_pages_compact", stream)
+        self._call("compact", stream)
 
     def append(self, layer, k, v, rows=None, cu=None, max_new=None, stream=None):
         """Quantise the rows' newest tokens (k, v: [n_tok, n_kv_heads, head_dim]) into their pages."""
-        h = self.cfg.n_kv_heads
-        kp, vp = self._tokens(k, "k", h), self._tokens(v, "v", h, k.shape[0])
-        self._call("dq_pages_append", stream, layer, kp, vp, k.stride(0), k.stride(1), v.stride(0), v.stride(1),
-                   *self._rows(rows, cu, k.shape[0], max_new))
+        kp, n, kt, kh = self._tokens(k, "k", self._hkv)
+        vp, _, vt, vh = self._tokens(v, "v", self._hkv, n)
+        self._call("append", stream, layer, kp, vp, kt, kh, vt, vh, *self._rows(rows, cu, n, max_new))
 
     def read(self, layer, k_out, v_out, rows=None, cu=None, max_new=None, stream=None):
         """The rows' newest tokens as the cache holds them, into contiguous k_out and v_out."""
-        h = self.cfg.n_kv_heads
-        kp, vp = self._tokens(k_out, "k_out", h), self._tokens(v_out, "v_out", h, k_out.shape[0])
-        if not k_out.is_contiguous() or not v_out.is_contiguous():
-            raise ValueError("k_out and v_out must be contiguous")
-        self._call("dq_pages_read", stream, layer, kp, vp, *self._rows(rows, cu, k_out.shape[0], max_new))
+        kp, n, _, _ = self._tokens(k_out, "k_out", self._hkv)
+        vp = self._tokens(v_out, "v_out", self._hkv, n)[0]
+        self._whole(k_out, "k_out")
+        self._whole(v_out, "v_out")
+        self._call("read", stream, layer, kp, vp, *self._rows(rows, cu, n, max_new))
 
     def attention(self, layer, q, out, rows=None, cu=None, max_new=None, lse=None, sel=None, sm_scale=None, stream=None):
         """Attention of the rows' newest tokens (q, out: [n_tok, n_q_heads, head_dim]) over their pages, or over the
         pages sel [n_rows, n_kv_heads, n_sel] names; lse: optional fp32 [n_tok, n_q_heads]."""
-        hq, n = self.cfg.n_q_heads, q.shape[0]
-        qp, op = self._tokens(q, "q", hq), self._tokens(out, "out", hq, n)
-        if not out.is_contiguous():
-            raise ValueError("out must be contiguous")
+        qp, n, qt, qh = self._tokens(q, "q", self._hq)
+        op = self._tokens(out, "out", self._hq, n)[0]
+        self._whole(out, "out")
         lp = sp = None
         n_sel = 0
         if lse is not None:
-            if lse.dtype != self._torch.float32 or lse.device != self.device or not lse.is_contiguous() or lse.numel() != n * hq:
-                raise ValueError(f"lse must be contiguous fp32 [{n}, {hq}] on {self.device}")
+            if lse.dtype is not self._float32 or lse.get_device() != self._index or not lse.is_contiguous() or lse.numel() != n * self._hq:
+                raise ValueError(f"lse must be contiguous fp32 [{n}, {self._hq}] on {self.device}")
             lp = lse.data_ptr()
         r = self._rows(rows, cu, n, max_new)
         if sel is not None:
             n_sel = sel.shape[-1]
-            sp = self._ints(sel, "sel", r[2] * self.cfg.n_kv_heads * n_sel)
-        if sm_scale is None:
-            sm_scale = self.cfg.head_dim ** -0.5
-        self._call("dq_pages_attention", stream, layer, qp, q.stride(0), q.stride(1), op, lp, *r, sp, n_sel, sm_scale)
+            sp = self._ints(sel, "sel", r[2] * self._hkv * n_sel)
+        self._call("attention", stream, layer, qp, qt, qh, op, lp, *r, sp, n_sel, self._scale if sm_scale is None else sm_scale)
 
     def select(self, layer, q, sel, rows=None, keep_first=1, keep_last=1, stream=None):
         """The pages that score highest for each row's one query token (q: [n_rows, n_q_heads, head_dim]) and KV head,
         into sel int32 [n_rows, n_kv_heads, n_sel], ascending, -1 behind them."""
-        n, n_sel = q.shape[0], sel.shape[-1]
-        qp = self._tokens(q, "q", self.cfg.n_q_heads)
-        self._call("dq_pages_select", stream, layer, qp, q.stride(0), q.stride(1), self._ints(rows, "rows", n), n,
-                   self._ints(sel, "sel", n * self.cfg.n_kv_heads * n_sel), n_sel, keep_first, keep_last)
+        qp, n, qt, qh = self._tokens(q, "q", self._hq)
+        n_sel = sel.shape[-1]
+        self._call("select", stream, layer, qp, qt, qh, self._ints(rows, "rows", n), n,
+                   self._ints(sel, "sel", n * self._hkv * n_sel), n_sel, keep_first, keep_last)
 
     def check(self, stream=None):
         """Synchronize and raise what earlier calls latched on the device."""
         cuda = self._torch.cuda
         with cuda.device(self.device.index):
             s = cuda.current_stream() if stream is None else stream
-            _raise(self._lib.dq_pages_check(self._b, s if isinstance(s, int) else s.cuda_stream))
+            _raise(_load().dq_pages_check(self._b, s if isinstance(s, int) else s.cuda_stream))
