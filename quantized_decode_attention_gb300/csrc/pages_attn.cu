@@ -506,9 +506,9 @@ __global__ void __launch_bounds__(32 * NW, 1) attn_chunks(PagesAttnArgs a) {
         if (sh.len[i] > 0) continue;
         const PageRow r = page_row(p, a.r, i);
         uint4 *o = reinterpret_cast<uint4 *>(a.out + static_cast<long long>(r.q0) * p.Hq * D);
-        for (int k = tid; k < r.n * p.Hq * (D / 8); k += 32 * NW) o[k] = make_uint4(0, 0, 0, 0);
+        for (long long k = tid; k < static_cast<long long>(r.n) * p.Hq * (D / 8); k += 32 * NW) o[k] = make_uint4(0, 0, 0, 0);
         if (a.lse)
-            for (int k = tid; k < r.n * p.Hq; k += 32 * NW) a.lse[static_cast<long long>(r.q0) * p.Hq + k] = -INFINITY;
+            for (long long k = tid; k < static_cast<long long>(r.n) * p.Hq; k += 32 * NW) a.lse[static_cast<long long>(r.q0) * p.Hq + k] = -INFINITY;
     }
     // this CTA's places [c0, c1), this warp's [w0, w1)
     int ctas = N / MIN_PLACES;

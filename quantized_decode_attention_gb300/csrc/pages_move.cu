@@ -47,9 +47,9 @@ __device__ __forceinline__ bool page_ok(const PagesView &p, int id) {
     return false;
 }
 
-// A plan's followers may be launched while it runs; they wait for its end before they
-// read anything (the hardware's dependency between launches of one stream).
-__device__ __forceinline__ void let_followers_start() { asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory"); }
+// A plan's copies may be launched while it runs; they wait for its end before they read
+// anything (the hardware's dependency between launches of one stream).
+__device__ __forceinline__ void let_copies_start() { asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory"); }
 __device__ __forceinline__ void await_plan() { asm volatile("griddepcontrol.wait;\n" ::: "memory"); }
 
 __global__ void __launch_bounds__(MV_THREADS) resize_kernel(PagesView p, const int *rows, const int *lens, int n, int *ws) {
@@ -59,7 +59,7 @@ __global__ void __launch_bounds__(MV_THREADS) resize_kernel(PagesView p, const i
         first_s[DQ_PAGES_MAX_ROWS];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     int *list = ws + PAGES_WS_HEAD, *src = list + p.n_pages, *dst = src + p.n_pages;
-    let_followers_start();
+    let_copies_start();
     if (tid == 0) {
         bad = found = 0;
         ws[0] = 0;
@@ -203,7 +203,7 @@ __global__ void __launch_bounds__(MV_THREADS) compact_kernel(PagesView p, int *w
     __shared__ int part[MV_WARPS + 1], n_src, n_dst;
     const int tid = threadIdx.x;
     int *map = ws + PAGES_WS_HEAD, *src = map + p.n_pages, *dst = src + p.n_pages;
-    let_followers_start();
+    let_copies_start();
     if (tid == 0) n_src = n_dst = 0;
     __syncthreads();
     int mine = 0;
@@ -241,9 +241,24 @@ __global__ void __launch_bounds__(MV_THREADS) compact_kernel(PagesView p, int *w
 // as many do; a thread has four 16-byte loads on their way before it stores.  What the
 // plan names is disjoint: a destination was free.
 constexpr int CP_THREADS = 256, CP_DEEP = 4, CP_SLICE = CP_THREADS * CP_DEEP;
+// REMAP: the plan is a compaction; the table entries of moved pages follow (map[src] = dst), a row a CTA.
+template <bool REMAP>
 __global__ void __launch_bounds__(CP_THREADS) copy_kernel(PagesView p, const int *ws) {
     await_plan();
     const int n = ws[0];
+    if (n == 0) return;
+    if (REMAP) {
+        const int *map = ws + PAGES_WS_HEAD, live = ws[1];
+        for (int i = blockIdx.x; i < p.max_seqs; i += gridDim.x) {
+            int len = p.seq_len[i];
+            if (len < 0 || len > p.M * p.P) len = 0;
+            int *t = p.table + static_cast<long long>(i) * p.M;
+            for (int j = threadIdx.x; j < pages_for(len, p.P); j += CP_THREADS) {
+                const int id = t[j];
+                if (page_ok(p, id) && id >= live) t[j] = map[id];
+            }
+        }
+    }
     const int *src = ws + PAGES_WS_HEAD + p.n_pages, *dst = src + p.n_pages;
     const int pb = p.Hkv * p.page_bytes / 16, sb = p.Hkv * p.sum_bytes / 16;  // 16-byte words of a page, of its summaries
     const int slices = (pb + sb + CP_SLICE - 1) / CP_SLICE;
@@ -268,26 +283,12 @@ __global__ void __launch_bounds__(CP_THREADS) copy_kernel(PagesView p, const int
     }
 }
 
-// Table entries of moved pages follow.
-__global__ void __launch_bounds__(256) remap_kernel(PagesView p, const int *ws) {
-    await_plan();
-    const int *map = ws + PAGES_WS_HEAD;
-    if (ws[0] == 0) return;
-    int len = p.seq_len[blockIdx.x];
-    if (len < 0 || len > p.M * p.P) len = 0;
-    int *t = p.table + static_cast<long long>(blockIdx.x) * p.M;
-    for (int j = threadIdx.x; j < pages_for(len, p.P); j += 256) {
-        const int id = t[j];
-        if (page_ok(p, id) && id >= ws[1]) t[j] = map[id];
-    }
-}
-
 }  // namespace
 
-static int launch_follower(void (*kernel)(PagesView, const int *), int grid, const PagesView &p, const int *ws, cudaStream_t st) {
+static int launch_copies(void (*kernel)(PagesView, const int *), const PagesView &p, const int *ws, int num_sms, cudaStream_t st) {
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(grid);
-    cfg.blockDim = dim3(256);
+    cfg.gridDim = dim3(6 * num_sms);
+    cfg.blockDim = dim3(CP_THREADS);
     cfg.stream = st;
     cudaLaunchAttribute at{};
     at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -301,7 +302,7 @@ int launch_pages_resize(const PagesView &p, const int *rows, const int *lens, in
     auto st = static_cast<cudaStream_t>(stream);
     resize_kernel<<<1, MV_THREADS, 0, st>>>(p, rows, lens, n, ws);
     const int e = static_cast<int>(cudaGetLastError());
-    return e ? e : launch_follower(copy_kernel, 6 * num_sms, p, ws, st);
+    return e ? e : launch_copies(copy_kernel<false>, p, ws, num_sms, st);
 }
 
 int launch_pages_fork(const PagesView &p, const int *src, const int *dst, int n, void *stream) {
@@ -312,11 +313,8 @@ int launch_pages_fork(const PagesView &p, const int *src, const int *dst, int n,
 int launch_pages_compact(const PagesView &p, int *ws, int num_sms, void *stream) {
     auto st = static_cast<cudaStream_t>(stream);
     compact_kernel<<<1, MV_THREADS, 0, st>>>(p, ws);
-    int e = static_cast<int>(cudaGetLastError());
-    // the tables first: both depend on the plan alone, and the tables are soon done
-    if (e || (e = launch_follower(remap_kernel, p.max_seqs, p, ws, st))) return e;
-    copy_kernel<<<6 * num_sms, CP_THREADS, 0, st>>>(p, ws);
-    return static_cast<int>(cudaGetLastError());
+    const int e = static_cast<int>(cudaGetLastError());
+    return e ? e : launch_copies(copy_kernel<true>, p, ws, num_sms, st);
 }
 
 }  // namespace dq

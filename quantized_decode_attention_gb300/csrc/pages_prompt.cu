@@ -385,9 +385,9 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prompt(PagesAttnArgs a) {
         if (sh.len[i] > 0) continue;
         const PageRow r = page_row(p, a.r, i);
         uint4 *o = reinterpret_cast<uint4 *>(a.out + static_cast<long long>(r.q0) * p.Hq * D);
-        for (int k = tid; k < r.n * p.Hq * (D / 8); k += THREADS) o[k] = make_uint4(0, 0, 0, 0);
+        for (long long k = tid; k < static_cast<long long>(r.n) * p.Hq * (D / 8); k += THREADS) o[k] = make_uint4(0, 0, 0, 0);
         if (a.lse)
-            for (int k = tid; k < r.n * p.Hq; k += THREADS) a.lse[static_cast<long long>(r.q0) * p.Hq + k] = -INFINITY;
+            for (long long k = tid; k < static_cast<long long>(r.n) * p.Hq; k += THREADS) a.lse[static_cast<long long>(r.q0) * p.Hq + k] = -INFINITY;
     }
     int ctas = static_cast<int>(N / MIN_SHARE < gridDim.x ? N / MIN_SHARE : gridDim.x);
     if (ctas < 1) ctas = 1;

@@ -76,13 +76,11 @@ __device__ __forceinline__ void store_first(uint32_t addr, uint32_t v) {
 
 // One cluster per (row, KV head).
 template <int D>
-__global__ void __launch_bounds__(SE_THREADS) select_kernel(PagesSelectArgs a) {
+__global__ void __launch_bounds__(SE_THREADS, 2) select_kernel(PagesSelectArgs a) {
     extern __shared__ uint32_t key[];  // [max_pages_per_seq], the first CTA's counts
     __shared__ __align__(16) int8_t qi[2 * D];
     __shared__ float red[SE_WARPS];
-    __shared__ int hist[256], above[SE_WARPS], equal[SE_WARPS];
-    __shared__ uint32_t prefix;
-    __shared__ int want;
+    __shared__ int hist[4 * 256], above[SE_WARPS], equal[SE_WARPS];
     const PagesView &p = a.p;
     const uint32_t rank = cluster_rank(), ctas = cluster_size();
     const int row = blockIdx.x / ctas, head = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -94,23 +92,42 @@ __global__ void __launch_bounds__(SE_THREADS) select_kernel(PagesSelectArgs a) {
             for (int i = tid; i < a.n_sel; i += SE_THREADS) out[i] = i < np ? i : -1;
         return;
     }
-    group_query<D>(a, r.q0, head, qi, red);
-    if (ctas > 1) cluster_sync_all();  // the first CTA is there
-    // a page's summary is D / 8 lanes' 16 bytes; each warp has 4 x 32 / (D / 8) pages on their way
+    // a page's summary is D / 8 lanes' 16 bytes; each warp has 4 x 32 / (D / 8) pages on their way, page
+    // numbers ahead of them (the first while the query is put together)
     constexpr int LANES = D / 8, PER = 32 / LANES, DEEP = 4;
     const int part = lane % LANES, sub = lane / LANES;
-    const int4 q = *reinterpret_cast<const int4 *>(qi + 16 * part);
     const int j0 = static_cast<int>(static_cast<long long>(np) * rank / ctas), j1 = static_cast<int>(static_cast<long long>(np) * (rank + 1) / ctas);
     const uint32_t keys = smem_u32(key);
-    for (int jw = j0 + warp * PER * DEEP; jw < j1; jw += SE_WARPS * PER * DEEP) {
+    const int *pages = p.table + static_cast<long long>(r.row) * p.M;
+    int ahead[DEEP];
+    auto numbers = [&](int jw) {
+#pragma unroll
+        for (int k = 0; k < DEEP; k++) {
+            const int j = jw + k * PER + sub;
+            ahead[k] = j < j1 ? pages[j] : 0;
+        }
+    };
+    int jw = j0 + warp * PER * DEEP;
+    numbers(jw);
+    for (int i = tid; i < 4 * 256; i += SE_THREADS) hist[i] = 0;
+    group_query<D>(a, r.q0, head, qi, red);
+    if (ctas > 1) cluster_sync_all();  // the first CTA is there
+    const int4 q = *reinterpret_cast<const int4 *>(qi + 16 * part);
+    for (; jw < j1; jw += SE_WARPS * PER * DEEP) {
         int id[DEEP];
         int4 s[DEEP];
         int e[DEEP];
 #pragma unroll
         for (int k = 0; k < DEEP; k++) {
-            const int j = jw + k * PER + sub;
-            id[k] = j < j1 ? page_of(p, r.row, j) : -1;
+            id[k] = ahead[k];
+            if (jw + k * PER + sub >= j1) {
+                id[k] = -1;
+            } else if (id[k] < 0 || id[k] >= p.n_pages) {
+                atomicOr(p.status, PST_TABLE);
+                id[k] = -1;
+            }
         }
+        numbers(jw + SE_WARPS * PER * DEEP);
 #pragma unroll
         for (int k = 0; k < DEEP; k++) {
             s[k] = make_int4(0, 0, 0, 0);
@@ -140,45 +157,48 @@ __global__ void __launch_bounds__(SE_THREADS) select_kernel(PagesSelectArgs a) {
     } else {
         __syncthreads();
     }
-    // the n_sel-th largest key: `prefix` holds its digits so far, `want` its place among keys that share them
+    // The n_sel-th largest key, 8 bits at a time: `last` holds its digits so far, `take` its place among the keys
+    // that share them.  Every warp reads the counts for itself.  Done early where all keys that share the digits are taken.
+    uint32_t last = 0;
+    int take = a.n_sel;
     for (int shift = 24; shift >= 0; shift -= 8) {
-        if (tid < 256) hist[tid] = 0;
-        if (shift == 24 && tid == 0) {
-            prefix = 0;
-            want = a.n_sel;
-        }
-        __syncthreads();
-        const uint32_t pre = prefix;
-        const int w = want;
+        int *h = hist + 32 * shift;
         for (int j = tid; j < np; j += SE_THREADS) {
             const uint32_t k = key[j];
-            if (shift == 24 || (k ^ pre) >> (shift + 8) == 0) atomicAdd(&hist[k >> shift & 255], 1);
+            if (shift == 24 || (k ^ last) >> (shift + 8) == 0) atomicAdd(&h[k >> shift & 255u], 1);
         }
         __syncthreads();
-        if (warp == 0) {  // lane l: digits 255 - 8 l down to 248 - 8 l
-            int c[8], sum = 0;
+        // lane l: digits 255 - 8 l down to 248 - 8 l
+        int c[8], sum = 0;
 #pragma unroll
-            for (int i = 0; i < 8; i++) sum += c[i] = hist[255 - 8 * lane - i];
-            int before = sum;
+        for (int i = 0; i < 8; i++) sum += c[i] = h[255 - 8 * lane - i];
+        int before = sum;
 #pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int t = __shfl_up_sync(FULL, before, o);
-                if (lane >= o) before += t;
-            }
-            before -= sum;
-#pragma unroll
-            for (int i = 0; i < 8; i++) {
-                if (before < w && before + c[i] >= w) {
-                    prefix = pre | static_cast<uint32_t>(255 - 8 * lane - i) << shift;
-                    want = w - before;
-                }
-                before += c[i];
-            }
+        for (int o = 1; o < 32; o <<= 1) {
+            const int t = __shfl_up_sync(FULL, before, o);
+            if (lane >= o) before += t;
         }
-        __syncthreads();
+        before -= sum;
+        const unsigned here = __ballot_sync(FULL, before < take && before + sum >= take);
+        int digit = 0, at = 0, count = 0;
+#pragma unroll
+        for (int i = 0; i < 8; i++) {
+            if (before < take && before + c[i] >= take) {
+                digit = 255 - 8 * lane - i;
+                at = take - before;
+                count = c[i];
+            }
+            before += c[i];
+        }
+        const int from = __ffs(here) - 1;
+        last |= static_cast<uint32_t>(__shfl_sync(FULL, digit, from)) << shift;
+        take = __shfl_sync(FULL, at, from);
+        if (__shfl_sync(FULL, count, from) == take && last > 0) {  // all of them: every key from `last` on
+            last--;
+            take = 0;
+            break;
+        }
     }
-    const uint32_t last = prefix;
-    const int take = want;  // of the keys equal to the last one, the first `take`
     // a warp's pages are neighbours: [b0, b1)
     const int b0 = static_cast<int>(static_cast<long long>(np) * warp / SE_WARPS), b1 = static_cast<int>(static_cast<long long>(np) * (warp + 1) / SE_WARPS);
     int na = 0, ne = 0;

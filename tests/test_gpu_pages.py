@@ -296,6 +296,25 @@ def test_attention_of_a_long_row_and_many_short_ones():
     f.verify(f.queries(counts), counts)
 
 
+def test_attention_of_very_many_rows():
+    """1024 rows of all lengths, single tokens and ragged few and many."""
+    rng = np.random.default_rng(8)
+    lens = [int(x) for x in rng.integers(0, 90, 1024)]
+    f = Filled(lens, n_pages=3000, max_pages_per_seq=6, page_size=32, n_kv_heads=1, n_q_heads=2, head_dim=64)
+    f.verify(f.queries([1] * 1024), [1] * 1024)
+    counts = [int(x) for x in rng.integers(0, 4, 1024)]
+    f.verify(f.queries(counts), counts)
+    counts = [int(x) for x in rng.integers(0, 30, 1024)]
+    f.verify(f.queries(counts), counts)
+
+
+def test_attention_of_negative_and_zero_scales():
+    f = Filled([333, 150], page_size=64)
+    for n in (1, 2, 40):
+        for s in (-0.1, 0.0):
+            f.verify(f.queries([n, n]), [n, n], scale=s)
+
+
 def test_attention_of_strided_queries_and_exponents():
     import torch
     f = Filled([90, 33], k_exp=3, v_exp=-6, page_size=32, dtype="f16")
@@ -495,6 +514,47 @@ def test_a_full_list_of_rows():
     _same(pool, m)
 
 
+def test_pages_beyond_four_gigabytes():
+    """Pages numbered so that their bytes lie past 2^32: append, copy on write, move, choice and both attentions."""
+    import torch
+    N, P = 32000, 128
+    f = Filled.__new__(Filled)
+    pool = _pool(n_pages=N, page_size=P, n_kv_heads=8, n_q_heads=32, max_seqs=3, max_pages_per_seq=4)
+    assert pool.tensors["pages"].numel() > 1 << 32
+    pool.tensors["refs"][:N - 12] = 1  # what is free lies at the end
+    rng = np.random.default_rng(4)
+    lens = [300, 130]
+    pool.resize(_i32([0, 1]), _i32(lens))
+    k, v = (torch.tensor(rng.normal(size=(430, 8, 128))).to(torch.bfloat16).cuda() for _ in range(2))
+    pool.append(0, k, v, cu=_cu(lens), max_new=300)
+    pool.fork(_i32([1]), _i32([2]))
+    pool.resize(_i32([2]), _i32([131]))  # a copy of row 1's second page
+    pool.append(0, k[:1], v[:1], rows=_i32([2]))
+    pool.check()
+    assert int(pool.tensors["table"][:, 0].min()) >= N - 12
+    hk, hv = R.quantise(_np(k), 0)[2], R.quantise(_np(v), 0)[2]
+    f.pool, f.layer, f.dtype, f.Hkv, f.G, f.d, f.P, f.rng = pool, 0, "bf16", 8, 4, 128, P, rng
+    f.lens = [300, 130, 131]
+    f.hk = [hk[:300], hk[300:], np.concatenate([hk[300:], hk[:1]])]
+    f.hv = [hv[:300], hv[300:], np.concatenate([hv[300:], hv[:1]])]
+    q = f.queries([1, 1, 1])
+    f.verify(q, [1, 1, 1])
+    counts = [40, 9, 12]
+    f.verify(f.queries(counts), counts)
+    sel = torch.empty(3, 8, 2, dtype=torch.int32, device="cuda")
+    pool.select(0, q, sel)
+    want = [[R.choose(_np(q[r, h * 4:h * 4 + 4]), [R.summary(f.hk[r][j * P:(j + 1) * P, h]) for j in range(-(-f.lens[r] // P))],
+                      -(-f.lens[r] // P), 2, 1, 1) for h in range(8)] for r in range(3)]
+    assert [[[x for x in y if x >= 0] for y in z] for z in sel.tolist()] == want
+    f.verify(q, [1, 1, 1], chosen=want, sel=sel)
+    pool.tensors["refs"][:5] = 0
+    pool.compact()  # the highest pages move below
+    pool.check()
+    low = pool.tensors["table"][pool.tensors["table"] >= 0]
+    assert low[low < 5].unique().tolist() == [0, 1, 2, 3, 4]  # five of the six pages found room (one is in two rows)
+    f.verify(q, [1, 1, 1])
+
+
 # ---- together --------------------------------------------------------------------------------------------
 @pytest.mark.parametrize("captured", [False, True])
 def test_a_beam_search_as_a_program_runs_it(captured):
@@ -581,6 +641,42 @@ def test_a_beam_search_as_a_program_runs_it(captured):
             for got, c in ((full, None), (part, chosen)):
                 want, _, tol, _ = f.expect(q[layer], [1] * 6, rows, chosen=c)
                 assert (np.abs(_np(got[layer]) - want) <= tol).all(), (t, layer, c is None)
+
+
+def test_two_graphs_with_a_workspace_each():
+    """Two captured steps that replay at the same time on two streams, and one whose lengths change between replays."""
+    import torch
+    f = Filled([2500, 1900, 40], n_pages=128, max_pages_per_seq=50)
+    q = [f.queries([1, 1, 1]) for _ in range(2)]
+    long = f.queries([30, 20, 25])
+    want, want_long = [f.attend(x, [1, 1, 1])[0] for x in q], f.attend(long, [30, 20, 25])[0]
+    handles, s, graphs, outs = [f.pool, f.pool.share()], [torch.cuda.Stream(), torch.cuda.Stream()], [], []
+    cu = _cu([30, 20, 25])
+    for i in range(2):
+        o, ol = torch.empty_like(q[i]), torch.empty_like(long)
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=s[i]):
+            for _ in range(3):
+                handles[i].attention(0, q[i], o)
+                handles[i].attention(0, long, ol, cu=cu, max_new=30)
+        graphs.append(g)
+        outs.append((o, ol))
+    for _ in range(10):
+        for i in range(2):
+            with torch.cuda.stream(s[i]):
+                graphs[i].replay()
+        torch.cuda.synchronize()
+        for i in range(2):
+            assert torch.equal(outs[i][0], want[i]) and torch.equal(outs[i][1], want_long)
+    f.pool.resize(_i32([0, 1]), _i32([700, 0]))  # shorter, and empty: the captured call follows
+    f.lens[0], f.lens[1] = 700, 0
+    for held in (f.hk, f.hv):
+        held[0], held[1] = held[0][:700], held[1][:0]
+    graphs[0].replay()
+    torch.cuda.synchronize()
+    f.pool.check()
+    exp, _, tol, _ = f.expect(q[0], [1, 1, 1])
+    assert (np.abs(_np(outs[0][0]) - exp) <= tol).all()
 
 
 def test_two_handles_on_two_streams():
