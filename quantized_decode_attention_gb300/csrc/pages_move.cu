@@ -9,33 +9,46 @@ namespace dq {
 namespace {
 
 constexpr int MV_THREADS = 1024, MV_WARPS = MV_THREADS / 32;
+constexpr int MV_FRESH = 1024;  // new pages of a call that are listed in shared memory
 
-// Exclusive prefix of v over the CTA; `total` gets the sum.  `part` holds MV_WARPS + 1 ints.
-__device__ int block_prefix(int v, int *part, int &total) {
+// Exclusive prefix of v over the CTA; `total` gets the sum.  `part` holds MV_WARPS + 1 values.
+template <class T>
+__device__ T block_prefix(T v, T *part, T &total) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    int s = v;
+    T s = v;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const int t = __shfl_up_sync(FULL, s, o);
+        const T t = __shfl_up_sync(FULL, s, o);
         if (lane >= o) s += t;
     }
     __syncthreads();
     if (lane == 31) part[warp] = s;
     __syncthreads();
-    if (warp == 0) {
-        const int w = part[lane];
-        int t = w;
+    // every warp adds the warps' sums up for itself
+    const T w = part[lane];
+    T t = w;
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int u = __shfl_up_sync(FULL, t, o);
-            if (lane >= o) t += u;
-        }
-        part[lane] = t - w;
-        if (lane == 31) part[32] = t;
+    for (int o = 1; o < 32; o <<= 1) {
+        const T u = __shfl_up_sync(FULL, t, o);
+        if (lane >= o) t += u;
     }
-    __syncthreads();
-    total = part[32];
-    return part[warp] + s - v;
+    total = __shfl_sync(FULL, t, 31);
+    return __shfl_sync(FULL, t - w, warp) + s - v;
+}
+
+// Which of the 8 pages from `base` on (a multiple of 8) are held; those past the pool are not.
+__device__ __forceinline__ unsigned held8(const PagesView &p, int base) {
+    unsigned m = 0;
+    if (base + 8 <= p.n_pages) {
+        const int4 a = *reinterpret_cast<const int4 *>(p.refs + base), b = *reinterpret_cast<const int4 *>(p.refs + base + 4);
+        m = (a.x > 0) | (a.y > 0) << 1 | (a.z > 0) << 2 | (a.w > 0) << 3 | (b.x > 0) << 4 | (b.y > 0) << 5 | (b.z > 0) << 6 | (b.w > 0) << 7;
+    } else {
+        for (int i = 0; base + i < p.n_pages; i++) m |= (p.refs[base + i] > 0) << i;
+    }
+    return m;
+}
+__device__ __forceinline__ unsigned in_pool8(const PagesView &p, int base) {
+    return base + 8 <= p.n_pages ? 0xffu : (base < p.n_pages ? (1u << (p.n_pages - base)) - 1u : 0u);
 }
 
 __device__ __forceinline__ int pages_for(int len, int P) { return (len + P - 1) / P; }
@@ -54,7 +67,8 @@ __device__ __forceinline__ void await_plan() { asm volatile("griddepcontrol.wait
 
 __global__ void __launch_bounds__(MV_THREADS) resize_kernel(PagesView p, const int *rows, const int *lens, int n, int *ws) {
     __shared__ unsigned seen[DQ_PAGES_MAX_ROWS / 32];
-    __shared__ int part[MV_WARPS + 1], bad, found;
+    __shared__ long long part[MV_WARPS];
+    __shared__ int bad, found, fresh[MV_FRESH];
     __shared__ int row_s[DQ_PAGES_MAX_ROWS], had_s[DQ_PAGES_MAX_ROWS], has_s[DQ_PAGES_MAX_ROWS], page_s[DQ_PAGES_MAX_ROWS],
         first_s[DQ_PAGES_MAX_ROWS];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -89,15 +103,16 @@ __global__ void __launch_bounds__(MV_THREADS) resize_kernel(PagesView p, const i
     row_s[tid] = row;
     had_s[tid] = had;
     has_s[tid] = has;
-    page_s[tid] = -1;
-    __syncthreads();
     // pages behind the new lengths lose a reference (given back below if the call fails)
-    for (int i = warp; i < n; i += MV_WARPS)
-        for (int j = has_s[i] + lane; j < had_s[i]; j += 32) {
-            const int id = p.table[static_cast<long long>(row_s[i]) * p.M + j];
-            if (page_ok(p, id)) atomicSub(&p.refs[id], 1);
-        }
-    __syncthreads();
+    const bool drops = __syncthreads_or(has < had);
+    if (drops) {
+        for (int i = warp; i < n; i += MV_WARPS)
+            for (int j = has_s[i] + lane; j < had_s[i]; j += 32) {
+                const int id = p.table[static_cast<long long>(row_s[i]) * p.M + j];
+                if (page_ok(p, id)) atomicSub(&p.refs[id], 1);
+            }
+        __syncthreads();
+    }
     int page = -1;
     if (row >= 0 && after > before && before % p.P) {
         page = p.table[static_cast<long long>(row) * p.M + before / p.P];
@@ -112,18 +127,30 @@ __global__ void __launch_bounds__(MV_THREADS) resize_kernel(PagesView p, const i
         copy = p.refs[page] - earlier > 1;
     }
     const int need = (copy ? 1 : 0) + (has > had ? has - had : 0);
-    int total, n_copy;
-    const int first = block_prefix(need, part, total);
+    // places among the new pages and among the copies, in one prefix
+    long long both;
+    const long long at = block_prefix(static_cast<long long>(need) << 32 | (copy ? 1 : 0), part, both);
+    const int first = static_cast<int>(at >> 32), at_copy = static_cast<int>(at), n_copy = static_cast<int>(both);
+    if (both >> 32 > p.n_pages) {  // (more than there are at all)
+        if (tid == 0) found = -1;
+    }
+    const int total = both >> 32 > p.n_pages ? p.n_pages + 1 : static_cast<int>(both >> 32);
     first_s[tid] = first;
-    const int at_copy = block_prefix(copy ? 1 : 0, part, n_copy);
-    // the lowest `total` free pages
-    for (int i0 = 0; i0 < p.n_pages && found < total; i0 += MV_THREADS) {
-        const int i = i0 + tid, f = i < p.n_pages && p.refs[i] == 0;
-        int some;
-        const int at = found + block_prefix(f, part, some);
-        if (f && at < total) list[at] = i;
+    __syncthreads();
+    // the lowest `total` free pages, 8 a thread at a time
+    auto fresh_page = [&](int k) -> int { return k < MV_FRESH ? fresh[k] : list[k]; };
+    for (int i0 = 0; i0 < p.n_pages && found >= 0 && found < total; i0 += 8 * MV_THREADS) {
+        const int base = i0 + 8 * tid;
+        unsigned f = base < p.n_pages ? in_pool8(p, base) & ~held8(p, base) : 0u;
+        long long some;
+        int k = found + static_cast<int>(block_prefix(static_cast<long long>(__popc(f)), part, some));
+        for (; f && k < total; f &= f - 1, k++) {
+            const int id = base + __ffs(f) - 1;
+            if (k < MV_FRESH) fresh[k] = id;
+            else list[k] = id;
+        }
         __syncthreads();
-        if (tid == 0) found += some;
+        if (tid == 0) found += static_cast<int>(some);
         __syncthreads();
     }
     if (found < total) {
@@ -135,12 +162,13 @@ __global__ void __launch_bounds__(MV_THREADS) resize_kernel(PagesView p, const i
         if (tid == 0) atomicOr(p.status, PST_FULL);
         return;
     }
-    for (int i = tid; i < total; i += MV_THREADS) p.refs[list[i]] = 1;
+    for (int i = tid; i < total; i += MV_THREADS) p.refs[fresh_page(i)] = 1;
     if (copy) {
+        const int to = fresh_page(first);
         atomicSub(&p.refs[page], 1);
         src[at_copy] = page;
-        dst[at_copy] = list[first];
-        p.table[static_cast<long long>(row) * p.M + before / p.P] = list[first];
+        dst[at_copy] = to;
+        p.table[static_cast<long long>(row) * p.M + before / p.P] = to;
         first_s[tid] = first + 1;
     }
     if (row >= 0) p.seq_len[row] = after;
@@ -149,7 +177,7 @@ __global__ void __launch_bounds__(MV_THREADS) resize_kernel(PagesView p, const i
     for (int i = warp; i < n; i += MV_WARPS) {
         int *t = p.table + static_cast<long long>(row_s[i]) * p.M;
         for (int j = has_s[i] + lane; j < had_s[i]; j += 32) t[j] = -1;
-        for (int j = had_s[i] + lane; j < has_s[i]; j += 32) t[j] = list[first_s[i] + j - had_s[i]];
+        for (int j = had_s[i] + lane; j < has_s[i]; j += 32) t[j] = fresh_page(first_s[i] + j - had_s[i]);
     }
 }
 
@@ -200,28 +228,34 @@ __global__ void __launch_bounds__(MV_THREADS) fork_kernel(PagesView p, const int
 // n = live pages; src: live pages numbered n or more, dst: free numbers below n, both
 // ascending (there are as many of each); map[src] = dst.
 __global__ void __launch_bounds__(MV_THREADS) compact_kernel(PagesView p, int *ws) {
-    __shared__ int part[MV_WARPS + 1], n_src, n_dst;
+    __shared__ int part[MV_WARPS], n_src, n_dst;
     const int tid = threadIdx.x;
     int *map = ws + PAGES_WS_HEAD, *src = map + p.n_pages, *dst = src + p.n_pages;
     let_copies_start();
     if (tid == 0) n_src = n_dst = 0;
     __syncthreads();
     int mine = 0;
-    for (int i = tid; i < p.n_pages; i += MV_THREADS) mine += p.refs[i] > 0;
+    for (int i = 8 * tid; i < p.n_pages; i += 8 * MV_THREADS) mine += __popc(held8(p, i));
     int total;
     block_prefix(mine, part, total);
-    for (int i0 = 0; i0 < p.n_pages; i0 += MV_THREADS) {
-        const int i = i0 + tid;
-        const int in = i < p.n_pages, used = in && p.refs[i] > 0;
-        const int s = used && i >= total, d = in && !used && i < total;
-        int ts, td;
-        const int as = n_src + block_prefix(s, part, ts), ad = n_dst + block_prefix(d, part, td);
-        if (s) src[as] = i;
-        if (d) dst[ad] = i;
+    for (int i0 = 0; i0 < p.n_pages; i0 += 8 * MV_THREADS) {
+        const int base = i0 + 8 * tid;
+        unsigned s = 0, d = 0;
+        if (base < p.n_pages) {
+            const unsigned held = held8(p, base);
+            const unsigned below = base + 8 <= total ? 0xffu : (base < total ? (1u << (total - base)) - 1u : 0u);
+            s = held & ~below;
+            d = ~held & below;
+        }
+        int some;  // both counts in one prefix: at most 8192 each
+        const int at = block_prefix(__popc(s) | __popc(d) << 16, part, some);
+        int as = n_src + (at & 0xffff), ad = n_dst + (at >> 16);
+        for (; s; s &= s - 1) src[as++] = base + __ffs(s) - 1;
+        for (; d; d &= d - 1) dst[ad++] = base + __ffs(d) - 1;
         __syncthreads();
         if (tid == 0) {
-            n_src += ts;
-            n_dst += td;
+            n_src += some & 0xffff;
+            n_dst += some >> 16;
         }
         __syncthreads();
     }
