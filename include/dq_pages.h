@@ -28,7 +28,8 @@
  * ------------------------------------------------------------------------
  * - rows: device int32 [n_rows], the table rows of this call's sequences; NULL
  *   = rows 0 .. n_rows - 1.  A negative entry is a padding row: it holds
- *   nothing, and its queries' outputs are those of an empty sequence.
+ *   nothing, and its queries' outputs are those of an empty sequence.  A call that
+ *   writes (resize, fork, append) names a row once.
  * - cu: device int32 [n_rows + 1], where each row's new tokens begin among the
  *   call's n_tok tokens; NULL = one token for each row.  A row's n new tokens are
  *   its LAST n: they stand at positions [seq_len - n, seq_len), so a call that
@@ -90,7 +91,9 @@ typedef struct {
  * seq_len int32 [max_seqs], 0 at the start.
  * refs    int32 [n_pages]: rows that hold the page; 0 = free.  0 at the start.
  * status  16 bytes, 0 at the start.
- * workspace: 0 at the start, used by every call but dq_pages_append, _read and _fork.
+ * workspace: 0 at the start (and to be zeroed again after DQ_ETIMEOUT), used by every
+ *         call but dq_pages_append, _read, _fork and _select: 12 bytes a page and
+ *         some 43 MB for the parts that attention's CTAs join.
  */
 typedef struct {
     void *pages, *summary;

@@ -72,6 +72,8 @@ __device__ __forceinline__ PageRow page_row(const PagesView &p, const PagesRows 
     return o;
 }
 
+__device__ __forceinline__ bool takes(const PagesAttnArgs &a, const PageRow &r) { return r.n * a.p.G > a.over && r.n * a.p.G <= a.most; }
+
 // Page number of ordinal j of a row (0 <= j < M), -1 (latched) where the table's entry
 // is no page of the pool.
 __device__ __forceinline__ int page_of(const PagesView &p, int row, int j) {

@@ -237,7 +237,7 @@ dq_status dq_pages_select(const dq_pages_config *cfg, const dq_pages_buffers *bu
                           long long q_tok_stride, long long q_head_stride, const int *rows, int n_rows, int *sel, int n_sel,
                           int keep_first, int keep_last, void *stream) {
     dq::PagesSelectArgs a{};
-    dq_status s = view(cfg, bufs, layer, true, a.p);
+    dq_status s = view(cfg, bufs, layer, false, a.p);
     if (s != DQ_OK) return s;
     if ((s = call_rows(cfg, layer, rows, nullptr, n_rows, n_rows, 1, a.r)) != DQ_OK) return s;
     if (!q || !sel) return fail(DQ_EINVAL, "q / sel is NULL");

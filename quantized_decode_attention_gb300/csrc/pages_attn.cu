@@ -473,7 +473,7 @@ __global__ void __launch_bounds__(32 * NW, 1) attn_chunks(PagesAttnArgs a) {
             const PageRow r = page_row(p, a.r, i);
             sh.row[i] = r.row;
             sh.len[i] = r.len;
-            if (r.len > 0) w = static_cast<long long>((r.n * p.G + 8 * NT - 1) / (8 * NT)) * p.Hkv * (row_chunks(a, r.len) + UNIT_COST);
+            if (r.len > 0 && takes(a, r)) w = static_cast<long long>((r.n * p.G + 8 * NT - 1) / (8 * NT)) * p.Hkv * (row_chunks(a, r.len) + UNIT_COST);
         }
         long long s = w;
 #pragma unroll
@@ -505,6 +505,7 @@ __global__ void __launch_bounds__(32 * NW, 1) attn_chunks(PagesAttnArgs a) {
     for (int i = blockIdx.x; i < a.r.n_rows; i += gridDim.x) {
         if (sh.len[i] > 0) continue;
         const PageRow r = page_row(p, a.r, i);
+        if (!takes(a, r)) continue;
         uint4 *o = reinterpret_cast<uint4 *>(a.out + static_cast<long long>(r.q0) * p.Hq * D);
         for (long long k = tid; k < static_cast<long long>(r.n) * p.Hq * (D / 8); k += 32 * NW) o[k] = make_uint4(0, 0, 0, 0);
         if (a.lse)
@@ -730,14 +731,25 @@ int launch_chunks(const PagesAttnArgs &a, int grid, cudaStream_t st) {
 
 }  // namespace
 
-int launch_pages_attention(const PagesAttnArgs &a, int num_sms, void *stream) {
+int launch_pages_attention(PagesAttnArgs a, int num_sms, void *stream) {
     auto st = static_cast<cudaStream_t>(stream);
     const int grid = num_sms < PAGES_MAX_CTAS ? num_sms : PAGES_MAX_CTAS;
-    if (!a.sel && a.r.max_new * a.p.G > PROMPT_ROWS) return launch_pages_prompt(a, grid, stream);
+    const int rows = a.r.max_new * a.p.G;
+    a.over = 0;
+    a.most = 0x7fffffff;
+    if (!a.sel && rows > PROMPT_ROWS) {
+        // rows with many new tokens on the tensor cores; those of a mixed batch with few, which wait
+        // for the cache and not for products, by the kernel for few (one row alone: no second launch)
+        a.over = a.r.n_rows == 1 ? 0 : PROMPT_ROWS;
+        if (const int e = launch_pages_prompt(a, grid, stream)) return e;
+        if (a.r.n_rows == 1) return 0;
+        a.over = 0;
+        a.most = PROMPT_ROWS;
+    }
     // 8 query rows fill one n tile; more share the conversions of two, with fewer warps for their
     // registers (8 x 4 tokens over 32768 at head_dim 64: 69 us with 8 warps, 59 with 12; the
     // same 86 with either at 128, where mma.sync itself is the limit)
-    if (a.r.max_new * a.p.G <= 8) return a.p.d == 128 ? launch_chunks<128, 1, 16>(a, grid, st) : launch_chunks<64, 1, 16>(a, grid, st);
+    if (rows <= 8) return a.p.d == 128 ? launch_chunks<128, 1, 16>(a, grid, st) : launch_chunks<64, 1, 16>(a, grid, st);
     return a.p.d == 128 ? launch_chunks<128, 2, 8>(a, grid, st) : launch_chunks<64, 2, 12>(a, grid, st);
 }
 

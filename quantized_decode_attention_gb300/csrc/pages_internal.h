@@ -75,6 +75,7 @@ struct PagesAttnArgs {
     float *lse;
     const int *sel;
     int n_sel;
+    int over, most;       // this launch takes the rows with over < n G <= most query rows for each KV head
     float scale_log2;     // sm_scale 2^k_exp log2(e)
     float out_scale;      // 2^v_exp
     int *tickets;         // workspace: [PAGES_MAX_CTAS], 0 between calls
@@ -96,7 +97,7 @@ int launch_pages_fork(const PagesView &p, const int *src, const int *dst, int n,
 int launch_pages_compact(const PagesView &p, int *ws, int num_sms, void *stream);
 int launch_pages_append(const PagesStoreArgs &a, void *stream);
 int launch_pages_read(const PagesReadArgs &a, void *stream);
-int launch_pages_attention(const PagesAttnArgs &a, int num_sms, void *stream);
+int launch_pages_attention(PagesAttnArgs a, int num_sms, void *stream);
 // many new tokens: the tensor-core kernel on at most `grid` CTAs
 int launch_pages_prompt(const PagesAttnArgs &a, int grid, void *stream);
 int launch_pages_select(const PagesSelectArgs &a, int num_sms, void *stream);

@@ -359,7 +359,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prompt(PagesAttnArgs a) {
             const PageRow r = page_row(p, a.r, i);
             sh.row[i] = r.row;
             sh.len[i] = r.len;
-            if (r.len > 0 && r.n > 0) w = p.Hkv * blocks_before(r.len > r.n ? r.len - r.n : 0, tb, (r.n + tb - 1) / tb);
+            if (r.len > 0 && takes(a, r)) w = p.Hkv * blocks_before(r.len > r.n ? r.len - r.n : 0, tb, (r.n + tb - 1) / tb);
         }
         long long s = w;
 #pragma unroll
@@ -384,6 +384,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prompt(PagesAttnArgs a) {
     for (int i = blockIdx.x; i < a.r.n_rows; i += gridDim.x) {
         if (sh.len[i] > 0) continue;
         const PageRow r = page_row(p, a.r, i);
+        if (!takes(a, r)) continue;
         uint4 *o = reinterpret_cast<uint4 *>(a.out + static_cast<long long>(r.q0) * p.Hq * D);
         for (long long k = tid; k < static_cast<long long>(r.n) * p.Hq * (D / 8); k += THREADS) o[k] = make_uint4(0, 0, 0, 0);
         if (a.lse)

@@ -308,6 +308,19 @@ def test_attention_of_very_many_rows():
     f.verify(f.queries(counts), counts)
 
 
+@pytest.mark.parametrize("G, d", [(4, 128), (1, 64), (16, 64)])
+def test_attention_of_a_mixed_batch(G, d):
+    """Prompts' chunks, a few tokens and single tokens in one call, empty and padding rows among them."""
+    lens = [400, 900, 0, 33, 700, 64, 0, 1300]
+    f = Filled(lens, n_pages=80, max_pages_per_seq=24, n_kv_heads=2, n_q_heads=2 * G, head_dim=d)
+    counts = [150, 1, 40, 33, 2, 9, 1, 1]
+    f.verify(f.queries(counts), counts)
+    rows = [7, -1, 1, 6, 0, 4, -3, 3]
+    f.verify(f.queries(counts), counts, rows)
+    f.verify(f.queries([70]), [70], [1])
+    f.verify(f.queries([2]), [2], [7])
+
+
 def test_attention_of_negative_and_zero_scales():
     f = Filled([333, 150], page_size=64)
     for n in (1, 2, 40):

@@ -130,7 +130,7 @@ def test_refused_calls(lib, name, args, want):
 
 
 def test_refused_calls_without_a_workspace(lib):
-    for name, args in (("dq_pages_attention", ATTEND), ("dq_pages_select", SELECT), ("dq_pages_resize", (None, Q, 2, None)),
+    for name, args in (("dq_pages_attention", ATTEND), ("dq_pages_resize", (None, Q, 2, None)),
                        ("dq_pages_compact", (None,))):
         refused(lib, name, EINVAL, b=bufs(workspace=None), args=args)
 
