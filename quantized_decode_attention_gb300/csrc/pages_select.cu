@@ -22,29 +22,41 @@ __device__ __forceinline__ uint32_t order_key(float x) {
     return (u & 0x80000000u) ? ~u : u | 0x80000000u;
 }
 
+// One channel of a group's query heads, loaded before anything else is known of the row.
+struct GroupChannel {
+    uint16_t x[16];
+    __device__ __forceinline__ void load(const PagesSelectArgs &a, int token, int head, int c) {
+        const uint16_t *q = a.q + static_cast<long long>(token) * a.qt + static_cast<long long>(head) * a.p.G * a.qh + c;
+#pragma unroll
+        for (int g = 0; g < 16; g++) x[g] = g < a.p.G ? q[g * a.qh] : 0;
+    }
+};
+
 // The whole numbers round(Q+- 127 / max|Q+-|) of a row's group of query heads as bytes
 // qi[0..D) (Q+) and qi[D..2D) (Q-).  Sums of 16-bit values in 64 bits do not depend on
 // the order of the heads.
 template <int D>
-__device__ void group_query(const PagesSelectArgs &a, int q0, int head, int8_t *qi, float *red) {
-    const PagesView &p = a.p;
+__device__ __forceinline__ void group_query(const PagesView &p, const GroupChannel &q, int8_t *qi, float *red) {
     const int tid = threadIdx.x;
     double hi = 0., lo = 0.;
-    if (tid < D)
-        for (int g = 0; g < p.G; g++) {
-            const double x = from16(a.q[static_cast<long long>(q0) * a.qt + (head * p.G + g) * a.qh + tid], p.bf16);
-            hi += x > 0. ? x : 0.;
-            lo += x < 0. ? x : 0.;
-            if (x != x) hi = x;
+    if (tid < D) {
+#pragma unroll
+        for (int g = 0; g < 16; g++) {
+            if (g >= p.G) break;
+            const float x = from16(q.x[g], p.bf16);
+            if (x > 0.f) hi += x;
+            else lo += x;  // (NaN too)
         }
-    float h = static_cast<float>(hi), l = static_cast<float>(lo);
-    float m = tid < D ? fmaxf(h, -l) : 0.f;
+    }
+    const float h = static_cast<float>(hi), l = static_cast<float>(lo);
+    float m = fmaxf(h, -l);
     if (!(fabsf(h) < INFINITY) || !(fabsf(l) < INFINITY)) m = INFINITY;
     m = warp_max(m);
     if ((tid & 31) == 0) red[tid >> 5] = m;
     __syncthreads();
     m = red[0];
-    for (int i = 1; i < SE_WARPS; i++) m = fmaxf(m, red[i]);
+#pragma unroll
+    for (int i = 1; i < D / 32; i++) m = fmaxf(m, red[i]);
     if (tid < D) {
         const bool ok = m > 0.f && m < INFINITY;
         const float inv = ok ? __fdiv_rn(127.f, m) : 0.f;
@@ -84,6 +96,8 @@ __global__ void __launch_bounds__(SE_THREADS, 2) select_kernel(PagesSelectArgs a
     const PagesView &p = a.p;
     const uint32_t rank = cluster_rank(), ctas = cluster_size();
     const int row = blockIdx.x / ctas, head = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    GroupChannel channel;
+    if (tid < D) channel.load(a, row, head, tid);  // (a token a row)
     const PageRow r = page_row(p, a.r, row);
     const int np = (r.len + p.P - 1) / p.P;
     int *out = a.sel + (static_cast<long long>(row) * p.Hkv + head) * a.n_sel;
@@ -110,7 +124,7 @@ __global__ void __launch_bounds__(SE_THREADS, 2) select_kernel(PagesSelectArgs a
     int jw = j0 + warp * PER * DEEP;
     numbers(jw);
     for (int i = tid; i < 4 * 256; i += SE_THREADS) hist[i] = 0;
-    group_query<D>(a, r.q0, head, qi, red);
+    group_query<D>(p, channel, qi, red);
     if (ctas > 1) cluster_sync_all();  // the first CTA is there
     const int4 q = *reinterpret_cast<const int4 *>(qi + 16 * part);
     for (; jw < j1; jw += SE_WARPS * PER * DEEP) {
