@@ -266,7 +266,8 @@ int launch_as(const PagesSelectArgs &a, int ctas, cudaStream_t st) {
 }  // namespace
 
 int launch_pages_select(const PagesSelectArgs &a, int num_sms, void *stream) {
-    // clusters while the card has room for them and a CTA keeps 128 pages (of a full table)
+    // clusters while the card has room for them and a CTA keeps 128 pages (of a full table): with the attention
+    // to the chosen pages, 1 row of 2048 pages 22.6 us (one CTA for each 37.0), 4 rows of 512 22.6 (25.0)
     int ctas = 1;
     while (ctas < 8 && a.r.n_rows * a.p.Hkv * ctas * 2 <= 2 * num_sms && a.p.M / (ctas * 2) >= 128) ctas *= 2;
     return a.p.d == 128 ? launch_as<128>(a, ctas, static_cast<cudaStream_t>(stream)) : launch_as<64>(a, ctas, static_cast<cudaStream_t>(stream));
