@@ -500,17 +500,21 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prompt(PagesAttnArgs a) {
                     }
                     row_s.m = z == -INFINITY ? -INFINITY : z * row_s.f;
                 }
-                // 32 keys at a time, the next 32 on their way; their weights take the place of scores that were read
+                // 32 keys at a time, the next 32 on their way; their weights take the place of scores that were read.
+                // A load's registers hold nothing before its wait: load and wait stand in one straight piece of code,
+                // with the weights of the 32 keys before between them and neither a branch nor the loop's end (so the
+                // last 32 keys' load is of columns that nobody uses; unrolled without it 468 us where this takes 430).
                 uint32_t sa[32], sb[32];
                 auto chunk = [&](uint32_t (&s)[32], uint32_t (&coming)[32], int c) {
                     // Weights are positive: one over MOST shows in their sum, so that the maximum is
                     // only sought where the sum passes that (or, no harm, many smaller weights do).
                     uint32_t w[16];
                     uint64_t sum[2];
+                    tmem_ld32(s_at + 32 * (c + 1) % KEYS, coming);
                     row_s.weigh(s, w, sum);
+                    tmem_wait_ld(coming);
                     const float2 x0 = both(add2(sum[0], sum[1]));
                     if (__any_sync(FULL, x0.x + x0.y > MOST)) {
-                        tmem_wait_ld(coming);  // no load is under way while registers may move
                         const float top = top_of(s);
                         row_s.raise<D>(top == -INFINITY ? -INFINITY : top * row_s.f, k > g.t0, o_at, 16 * c, s_at);
                         row_s.weigh(s, w, sum);
@@ -520,13 +524,10 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prompt(PagesAttnArgs a) {
                     tmem_st16(s_at + 16 * c, w);
                 };
                 tmem_ld32(s_at, sa);
+                tmem_wait_ld(sa);
 #pragma unroll 1
                 for (int c = 0; c < KEYS / 32; c += 2) {
-                    tmem_wait_ld(sa);
-                    tmem_ld32(s_at + 32 * c + 32, sb);
                     chunk(sa, sb, c);
-                    tmem_wait_ld(sb);
-                    if (c + 2 < KEYS / 32) tmem_ld32(s_at + 32 * c + 64, sa);
                     chunk(sb, sa, c + 1);
                 }
                 tmem_wait_st();
