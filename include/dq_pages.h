@@ -187,6 +187,16 @@ dq_status dq_pages_attention(const dq_pages_config *cfg, const dq_pages_buffers 
                              float sm_scale, void *stream);
 
 /*
+ * Test support for the timeout path: an attention call over rows 0 .. n_rows - 1 (sm_scale 1, no chosen pages) whose barriers
+ * wait for an arrival that nobody makes, for limit_ns at most (clamped to [1000, 10^9]) instead of the 2 s of
+ * every other call.  The kernel returns, `out` holds nothing of use, and dq_pages_check reports DQ_ETIMEOUT.
+ * Errors: as dq_pages_attention.
+ */
+dq_status dq_pages_test_expire_wait(const dq_pages_config *cfg, const dq_pages_buffers *bufs, int layer, const void *q,
+                                    long long q_tok_stride, long long q_head_stride, void *out, const int *cu, int n_rows,
+                                    int n_tok, int max_new, unsigned long long limit_ns, void *stream);
+
+/*
  * Choose pages for each row's one query token and KV head.  With the group's
  * query heads q_h, Q+ = sum_h max(q_h, 0) and Q- = sum_h min(q_h, 0) a page's score
  *   sum_c Q+_c largest_c + Q-_c smallest_c

@@ -119,6 +119,39 @@ dq_status launched(int e, const char *what) {
     return ok();
 }
 
+// Checked arguments of an attention call.
+dq_status attention_args(dq::PagesAttnArgs &a, const dq_pages_config *cfg, const dq_pages_buffers *bufs, int layer, const void *q,
+                         long long q_tok_stride, long long q_head_stride, void *out, float *lse, const int *rows, const int *cu,
+                         int n_rows, int n_tok, int max_new, const int *sel, int n_sel, float sm_scale) {
+    dq_status s = view(cfg, bufs, layer, true, a.p);
+    if (s != DQ_OK) return s;
+    if ((s = call_rows(cfg, layer, rows, cu, n_rows, n_tok, max_new, a.r)) != DQ_OK) return s;
+    if (!q || !out) return fail(DQ_EINVAL, "q / out is NULL");
+    if (!aligned16(q) || !aligned16(out) || (q_tok_stride | q_head_stride) & 7)
+        return fail(DQ_EALIGN, "q / out not 16-byte aligned, or a stride is no multiple of 8 elements");
+    if (!aligned4(lse) || !aligned4(sel)) return fail(DQ_EALIGN, "lse / sel not aligned to 4 bytes");
+    if (!std::isfinite(sm_scale)) return fail(DQ_EINVAL, "sm_scale is not finite");
+    if (sel && (n_sel < 1 || n_sel > DQ_PAGES_MAX_SELECT))
+        return fail(DQ_EINVAL, "n_sel outside [1, %d]", DQ_PAGES_MAX_SELECT);
+    if (sel && cu) return fail(DQ_EUNSUPPORTED, "chosen pages go with one query token for each row (cu must be NULL)");
+    a.q = static_cast<const uint16_t *>(q);
+    a.qt = q_tok_stride;
+    a.qh = q_head_stride;
+    a.out = static_cast<uint16_t *>(out);
+    a.lse = lse;
+    a.sel = sel;
+    a.n_sel = sel ? n_sel : 0;
+    a.scale_log2 = static_cast<float>(std::ldexp(static_cast<double>(sm_scale) * 1.4426950408889634074, cfg->k_exp));
+    a.out_scale = std::ldexp(1.0f, cfg->v_exp);
+    uint8_t *ws = static_cast<uint8_t *>(bufs->workspace) + dq::pages_ws_lists(cfg->n_pages);
+    a.tickets = reinterpret_cast<int *>(ws);
+    a.joins = reinterpret_cast<int *>(ws + dq::PAGES_MAX_CTAS * 4);
+    a.records = reinterpret_cast<float *>(ws + dq::PAGES_MAX_CTAS * 20);
+    a.wait_ns = dq::PAGES_WAIT_NS;
+    a.owed = 0;
+    return DQ_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -206,31 +239,22 @@ dq_status dq_pages_attention(const dq_pages_config *cfg, const dq_pages_buffers 
                              const int *cu, int n_rows, int n_tok, int max_new, const int *sel, int n_sel, float sm_scale,
                              void *stream) {
     dq::PagesAttnArgs a{};
-    dq_status s = view(cfg, bufs, layer, true, a.p);
+    const dq_status s = attention_args(a, cfg, bufs, layer, q, q_tok_stride, q_head_stride, out, lse, rows, cu, n_rows, n_tok,
+                                       max_new, sel, n_sel, sm_scale);
     if (s != DQ_OK) return s;
-    if ((s = call_rows(cfg, layer, rows, cu, n_rows, n_tok, max_new, a.r)) != DQ_OK) return s;
-    if (!q || !out) return fail(DQ_EINVAL, "q / out is NULL");
-    if (!aligned16(q) || !aligned16(out) || (q_tok_stride | q_head_stride) & 7)
-        return fail(DQ_EALIGN, "q / out not 16-byte aligned, or a stride is no multiple of 8 elements");
-    if (!aligned4(lse) || !aligned4(sel)) return fail(DQ_EALIGN, "lse / sel not aligned to 4 bytes");
-    if (!std::isfinite(sm_scale)) return fail(DQ_EINVAL, "sm_scale is not finite");
-    if (sel && (n_sel < 1 || n_sel > DQ_PAGES_MAX_SELECT))
-        return fail(DQ_EINVAL, "n_sel outside [1, %d]", DQ_PAGES_MAX_SELECT);
-    if (sel && cu) return fail(DQ_EUNSUPPORTED, "chosen pages go with one query token for each row (cu must be NULL)");
-    a.q = static_cast<const uint16_t *>(q);
-    a.qt = q_tok_stride;
-    a.qh = q_head_stride;
-    a.out = static_cast<uint16_t *>(out);
-    a.lse = lse;
-    a.sel = sel;
-    a.n_sel = sel ? n_sel : 0;
-    a.scale_log2 = static_cast<float>(std::ldexp(static_cast<double>(sm_scale) * 1.4426950408889634074, cfg->k_exp));
-    a.out_scale = std::ldexp(1.0f, cfg->v_exp);
-    uint8_t *ws = static_cast<uint8_t *>(bufs->workspace) + dq::pages_ws_lists(cfg->n_pages);
-    a.tickets = reinterpret_cast<int *>(ws);
-    a.joins = reinterpret_cast<int *>(ws + dq::PAGES_MAX_CTAS * 4);
-    a.records = reinterpret_cast<float *>(ws + dq::PAGES_MAX_CTAS * 20);
     return launched(dq::launch_pages_attention(a, device_sms(), stream), "attention launch");
+}
+
+dq_status dq_pages_test_expire_wait(const dq_pages_config *cfg, const dq_pages_buffers *bufs, int layer, const void *q,
+                                    long long q_tok_stride, long long q_head_stride, void *out, const int *cu, int n_rows,
+                                    int n_tok, int max_new, unsigned long long limit_ns, void *stream) {
+    dq::PagesAttnArgs a{};
+    const dq_status s = attention_args(a, cfg, bufs, layer, q, q_tok_stride, q_head_stride, out, nullptr, nullptr, cu, n_rows,
+                                       n_tok, max_new, nullptr, 0, 1.0f);
+    if (s != DQ_OK) return s;
+    a.owed = 1;
+    a.wait_ns = limit_ns < 1000ULL ? 1000ULL : (limit_ns > 1000000000ULL ? 1000000000ULL : limit_ns);
+    return launched(dq::launch_pages_attention(a, device_sms(), stream), "expire-wait launch");
 }
 
 dq_status dq_pages_select(const dq_pages_config *cfg, const dq_pages_buffers *bufs, int layer, const void *q,

@@ -33,6 +33,8 @@ struct PagesView {
     unsigned *status;
 };
 
+constexpr unsigned long long PAGES_WAIT_NS = 2000000000ull;  // a healthy wait is over in microseconds
+
 // Which rows and new tokens a call is about.
 struct PagesRows {
     const int *rows, *cu;
@@ -81,6 +83,8 @@ struct PagesAttnArgs {
     int *tickets;         // workspace: [PAGES_MAX_CTAS], 0 between calls
     int *joins;           // workspace: [PAGES_MAX_CTAS][4], what the tensor-core kernel leaves to be joined
     float *records;       // workspace: [PAGES_MAX_CTAS][2][PAGES_REC_FLOATS]
+    unsigned long long wait_ns;  // longest wait on a barrier
+    unsigned owed;        // arrivals that barriers wait for and nobody makes: 0 but in tests of waits that run out
 };
 struct PagesSelectArgs {
     PagesView p;

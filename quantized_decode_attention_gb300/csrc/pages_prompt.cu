@@ -32,7 +32,6 @@ namespace dq {
 namespace {
 
 constexpr float LN2 = 0.69314718055994530942f;
-constexpr uint64_t WAIT_NS = 2000000000ull;  // longest wait for another role
 constexpr float LIFT = 7.f;       // log2 units: weights are 2^LIFT at a logit of m ...
 constexpr float MOST = 32768.f;   // ... and may grow to 2^15 (a logit 2^8 over m) before m is raised
 constexpr int TILE = 128, ROWS = 2 * TILE;   // query rows of a tile, of a unit
@@ -254,7 +253,7 @@ struct Shared {
     long long first[DQ_PAGES_MAX_ROWS + 1];
     int row[DQ_PAGES_MAX_ROWS], len[DQ_PAGES_MAX_ROWS];
     long long part[THREADS / 32];
-    uint64_t q_full[2], k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2], o_full[2];
+    uint64_t q_full[2], k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2], o_full[2], drained;
     uint32_t tmem;
 };
 
@@ -341,7 +340,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prompt(PagesAttnArgs a) {
 #pragma unroll
         for (int i = 0; i < 2; i++) {
             mbar_init(&sh.q_full[i], 4);
-            mbar_init(&sh.k_full[i], 4);
+            mbar_init(&sh.k_full[i], 4 + a.owed);
             mbar_init(&sh.k_empty[i], 1);
             mbar_init(&sh.v_full[i], 4);
             mbar_init(&sh.v_empty[i], 1);
@@ -349,6 +348,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prompt(PagesAttnArgs a) {
             mbar_init(&sh.p_full[i], 4);
             mbar_init(&sh.o_full[i], 1);
         }
+        mbar_init(&sh.drained, 1);
         fence_mbar_init();
     }
     // places before each row
@@ -413,10 +413,11 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prompt(PagesAttnArgs a) {
     tc_fence_after();
     const uint32_t tmem = sh.tmem;
     // After a wait that ran out a thread waits no more: every role goes through its (finite)
-    // loops, in step with its warp, and the status says that the outputs are not valid.
+    // loops, in step with its warp, and the status says that the outputs are not valid.  What it
+    // did not wait for may still run: tensor memory is freed behind the last product (`drained`).
     bool late = false;
     auto wait = [&](uint64_t *bar, unsigned parity) {
-        if (!late && !mbar_spin(bar, parity, WAIT_NS)) {
+        if (!late && !mbar_spin(bar, parity, a.wait_ns)) {
             late = true;
             atomicOr(p.status, PST_TIMEOUT);
         }
@@ -745,6 +746,9 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prompt(PagesAttnArgs a) {
                 }
             }
         }
+        // (where no wait ran out, the softmax has waited for the same products)
+        tc_commit(&sh.drained);
+        if (!mbar_spin(&sh.drained, 0, a.wait_ns)) atomicOr(p.status, PST_TIMEOUT);
     }
     __syncwarp();
     tc_fence_before();

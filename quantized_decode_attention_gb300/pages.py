@@ -40,7 +40,8 @@ def _load():
         L.dq_pages_attention.argtypes = [cfg, buf, I, P, LL, LL, P, P, P, P, I, I, I, P, I, C.c_float, P]
         L.dq_pages_select.argtypes = [cfg, buf, I, P, LL, LL, P, I, P, I, I, I, P]
         L.dq_pages_check.argtypes = [buf, P]
-        for f in ("sizes", "resize", "fork", "compact", "append", "read", "attention", "select", "check"):
+        L.dq_pages_test_expire_wait.argtypes = [cfg, buf, I, P, LL, LL, P, P, I, I, I, C.c_ulonglong, P]
+        for f in ("sizes", "resize", "fork", "compact", "append", "read", "attention", "select", "check", "test_expire_wait"):
             getattr(L, "dq_pages_" + f).restype = C.c_int
         _ready = L
     return _ready
