@@ -91,9 +91,10 @@ typedef struct {
  * seq_len int32 [max_seqs], 0 at the start.
  * refs    int32 [n_pages]: rows that hold the page; 0 = free.  0 at the start.
  * status  16 bytes, 0 at the start.
- * workspace: 0 at the start (and to be zeroed again after DQ_ETIMEOUT), used by every
- *         call but dq_pages_append, _read, _fork and _select: 12 bytes a page and
- *         some 43 MB for the parts that attention's CTAs join.
+ * workspace: 0 at the start, used by every call but dq_pages_append, _read, _fork
+ *         and _select: 12 bytes a page and some 43 MB for the parts that attention's
+ *         CTAs join.  Every call leaves it fit for the next one, a call whose wait
+ *         ran out too.
  */
 typedef struct {
     void *pages, *summary;

@@ -37,7 +37,6 @@ namespace dq {
 namespace {
 
 constexpr float LN2 = 0.69314718055994530942f;
-constexpr uint64_t WAIT_NS = 2000000000ull;  // longest wait for a copy
 constexpr float SLACK = 8.f, LIFT = 7.f;   // log2 units
 constexpr int CHUNK = 32;                  // tokens
 // Query rows of a row and KV head beyond which the tensor-core kernel takes over (8 rows of 32768 tokens, 4 query
@@ -464,7 +463,7 @@ __global__ void __launch_bounds__(32 * NW, 1) attn_chunks(PagesAttnArgs a) {
     const PagesView &p = a.p;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     constexpr int ST = S::ST;
-    if (lane < ST) mbar_init(&sh.full[warp][lane], 1);
+    if (lane < ST) mbar_init(&sh.full[warp][lane], 1 + a.owed);
     fence_mbar_init();
     // places before each row: a prefix over the rows, 32 NW at a time
     long long base = 0;
@@ -544,6 +543,10 @@ __global__ void __launch_bounds__(32 * NW, 1) attn_chunks(PagesAttnArgs a) {
     const uint32_t ring = smem_u32(sh.ring[warp][0]), lane_to = ring + to, bars = smem_u32(sh.full[warp]);
     State<D, NT> st;
     unsigned sent = 0, done = 0;  // chunks of this warp's ring
+    // After a wait that ran out this warp waits for no copy more, but it goes through its units, leaves its
+    // parts and has them counted, so that the workspace is as every other call leaves it; the status says
+    // that the outputs are not valid.
+    bool late = false;
     for (int x = w0; x < w1;) {
         const Unit u = find_unit<D, NT, NW>(sh, a, x);
         const int t0 = x > u.first ? x - u.first : 0;
@@ -580,7 +583,7 @@ __global__ void __launch_bounds__(32 * NW, 1) attn_chunks(PagesAttnArgs a) {
         const uint8_t *lane_from = p.pages + static_cast<long long>(u.head) * p.page_bytes + from;
         // copy the next chunk that holds something into the ring
         auto send = [&]() {
-            while (next < t1) {
+            while (next < t1 && !late) {
                 const int c = next++;
                 int e = (TWO ? 2 * c : c >> shift) - e0;
                 if (e >= 32) {
@@ -627,9 +630,12 @@ __global__ void __launch_bounds__(32 * NW, 1) attn_chunks(PagesAttnArgs a) {
         st.reset();
         while (done != sent) {
             const int k = done % ST;
-            if (!mbar_wait(&sh.full[warp][k], done / ST & 1, WAIT_NS)) {
+            if (!__all_sync(FULL, mbar_wait(&sh.full[warp][k], done / ST & 1, a.wait_ns))) {
                 if (lane == 0) atomicOr(p.status, PST_TIMEOUT);
-                break;  // (mbar_wait had its limit: what is in flight had it too)
+                late = true;
+                while (++done != sent) mbar_wait(&sh.full[warp][done % ST], done / ST & 1, a.wait_ns);  // what is in flight has its limit too
+                __syncwarp();
+                break;
             }
             const int2 at = sh.pos[warp][k];
             st.step(sh.ring[warp][k], at.x, at.y, r.len, least);
@@ -637,7 +643,6 @@ __global__ void __launch_bounds__(32 * NW, 1) attn_chunks(PagesAttnArgs a) {
             __syncwarp();
             send();
         }
-        if (done != sent) break;
         if (t0 == 0 && t1 == u.chunks) st.to_output(a, r, u.head, u.row0);
         else {
             __syncwarp();

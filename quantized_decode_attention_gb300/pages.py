@@ -6,7 +6,7 @@ from __future__ import annotations
 
 import ctypes as C
 
-from ._lib import DTYPES, STATUS, _raise, load
+from ._lib import DTYPES, _raise, load
 
 P, I, LL = C.c_void_p, C.c_int, C.c_longlong
 
@@ -225,7 +225,4 @@ class PagePool:
         cuda = self._torch.cuda
         with cuda.device(self.device.index):
             s = cuda.current_stream() if stream is None else stream
-            st = _load().dq_pages_check(self._b, s if isinstance(s, int) else s.cuda_stream)
-            if st == STATUS.index("DQ_ETIMEOUT"):  # the call that gave up may have left counts behind
-                self.tensors["workspace"].zero_()
-            _raise(st)
+            _raise(_load().dq_pages_check(self._b, s if isinstance(s, int) else s.cuda_stream))

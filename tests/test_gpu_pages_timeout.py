@@ -51,3 +51,19 @@ def test_many_tokens_recover(d, counts):
     """Two tiles, whole units and units that CTAs share, over stages that are used again and again."""
     f = Filled([1500, 700], n_pages=64, max_pages_per_seq=24, head_dim=d)
     recovers(f, counts, [f.pool], f.pool)
+
+
+@pytest.mark.parametrize("d, P, counts", [(128, 64, [1, 1, 1, 1]), (64, 16, [1, 1, 1, 1]), (128, 128, [4, 1, 2, 3]), (64, 32, [4, 4, 3, 1])])
+def test_few_tokens_recover_on_every_handle(d, P, counts):
+    """The workspace of the call that gave up is the second handle's, the status both handles'.  Units that CTAs share,
+    units of one warp, and an empty row."""
+    f = Filled([2500, 1900, 40, 0], n_pages=5000 // P, max_pages_per_seq=2600 // P + 2, page_size=P, head_dim=d)
+    two = f.pool.share()
+    recovers(f, counts, [f.pool, two], two)
+    recovers(f, counts, [two, f.pool], f.pool)
+
+
+def test_a_mixed_batch_recovers():
+    f = Filled([2500, 1900, 40], n_pages=128, max_pages_per_seq=50)
+    two = f.pool.share()
+    recovers(f, [200, 1, 4], [f.pool, two], two)
