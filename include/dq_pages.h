@@ -219,11 +219,13 @@ dq_status dq_pages_select(const dq_pages_config *cfg, const dq_pages_buffers *bu
                           int n_sel, int keep_first, int keep_last, void *stream);
 
 /*
- * Synchronize `stream`, then return and clear what earlier calls on these buffers
- * latched: DQ_ETIMEOUT (a bounded device wait ran out: that call's output is not
- * valid), DQ_ENOMEM (a resize found too few free pages), DQ_EINVAL (a row, length,
- * count or page number out of range, a row named twice, a write to a shared page),
- * DQ_ENONFINITE, or DQ_OK; DQ_ECUDA if the stream reports an error.
+ * Synchronize `stream`, then return the gravest of what earlier calls on these buffers
+ * latched and clear that alone: what else they latched, and what calls on other
+ * streams latch meanwhile, is there for the next dq_pages_check.  In this order:
+ * DQ_ETIMEOUT (a bounded device wait ran out: that call's output is not valid),
+ * DQ_ENOMEM (a resize found too few free pages), DQ_EINVAL (a row, length, count or
+ * page number out of range, a row named twice, a write to a shared page: three
+ * reports), DQ_ENONFINITE, or DQ_OK; DQ_ECUDA if the stream reports an error.
  */
 dq_status dq_pages_check(const dq_pages_buffers *bufs, void *stream);
 

@@ -286,20 +286,29 @@ dq_status dq_pages_select(const dq_pages_config *cfg, const dq_pages_buffers *bu
 dq_status dq_pages_check(const dq_pages_buffers *bufs, void *stream) {
     if (!bufs || !bufs->status) return fail(DQ_EINVAL, "NULL argument");
     const auto st = static_cast<cudaStream_t>(stream);
+    static const struct {
+        unsigned bit;
+        dq_status status;
+        const char *what;
+    } latched[] = {  // the gravest first
+        {dq::PST_TIMEOUT, DQ_ETIMEOUT, "a bounded device wait ran out"},
+        {dq::PST_FULL, DQ_ENOMEM, "resize: too few free pages; nothing was changed"},
+        {dq::PST_ARG, DQ_EINVAL, "a row, length or count is out of range, or a row was named twice"},
+        {dq::PST_TABLE, DQ_EINVAL, "a table names no page of the pool"},
+        {dq::PST_SHARED, DQ_EINVAL, "an append met a page that several rows hold: resize after a fork"},
+        {dq::PST_NONFINITE, DQ_ENONFINITE, "non-finite K/V input"}};
     unsigned w = 0;
     cudaError_t e = cudaMemcpyAsync(&w, bufs->status, sizeof w, cudaMemcpyDeviceToHost, st);
     if (e == cudaSuccess) e = cudaStreamSynchronize(st);
-    if (e == cudaSuccess && w) {
-        e = cudaMemsetAsync(bufs->status, 0, sizeof w, st);
-        if (e == cudaSuccess) e = cudaStreamSynchronize(st);
-    }
     if (e != cudaSuccess) return fail(DQ_ECUDA, "status: %s", cudaGetErrorString(e));
-    if (w & dq::PST_TIMEOUT) return fail(DQ_ETIMEOUT, "a bounded device wait ran out");
-    if (w & dq::PST_FULL) return fail(DQ_ENOMEM, "resize: too few free pages; nothing was changed");
-    if (w & dq::PST_ARG) return fail(DQ_EINVAL, "a row, length or count is out of range, or a row was named twice");
-    if (w & dq::PST_TABLE) return fail(DQ_EINVAL, "a table names no page of the pool");
-    if (w & dq::PST_SHARED) return fail(DQ_EINVAL, "an append met a page that several rows hold: resize after a fork");
-    if (w & dq::PST_NONFINITE) return fail(DQ_ENONFINITE, "non-finite K/V input");
+    for (const auto &l : latched) {
+        if (!(w & l.bit)) continue;
+        // the reported bit alone is cleared: what another stream latches meanwhile stays
+        e = static_cast<cudaError_t>(dq::launch_pages_clear(static_cast<unsigned *>(bufs->status), l.bit, stream));
+        if (e == cudaSuccess) e = cudaStreamSynchronize(st);
+        if (e != cudaSuccess) return fail(DQ_ECUDA, "status: %s", cudaGetErrorString(e));
+        return fail(l.status, "%s", l.what);
+    }
     return ok();
 }
 

@@ -97,6 +97,7 @@ struct PagesSelectArgs {
 
 // launchers (return cudaError_t as int)
 int launch_pages_resize(const PagesView &p, const int *rows, const int *lens, int n, int *ws, int num_sms, void *stream);
+int launch_pages_clear(unsigned *status, unsigned bits, void *stream);
 int launch_pages_fork(const PagesView &p, const int *src, const int *dst, int n, void *stream);
 int launch_pages_compact(const PagesView &p, int *ws, int num_sms, void *stream);
 int launch_pages_append(const PagesStoreArgs &a, void *stream);

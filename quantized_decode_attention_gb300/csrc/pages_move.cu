@@ -318,7 +318,14 @@ __global__ void __launch_bounds__(CP_THREADS) copy_kernel(PagesView p, const int
     }
 }
 
+__global__ void clear_kernel(unsigned *status, unsigned bits) { atomicAnd(status, ~bits); }
+
 }  // namespace
+
+int launch_pages_clear(unsigned *status, unsigned bits, void *stream) {
+    clear_kernel<<<1, 1, 0, static_cast<cudaStream_t>(stream)>>>(status, bits);
+    return static_cast<int>(cudaGetLastError());
+}
 
 static int launch_copies(void (*kernel)(PagesView, const int *), const PagesView &p, const int *ws, int num_sms, cudaStream_t st) {
     cudaLaunchConfig_t cfg{};

@@ -221,7 +221,8 @@ class PagePool:
                    self._ints(sel, "sel", n * self._hkv * n_sel), n_sel, keep_first, keep_last)
 
     def check(self, stream=None):
-        """Synchronize and raise what earlier calls latched on the device."""
+        """Synchronize and raise the gravest of what earlier calls latched on the device; the rest is left for the next
+        check()."""
         cuda = self._torch.cuda
         with cuda.device(self.device.index):
             s = cuda.current_stream() if stream is None else stream
