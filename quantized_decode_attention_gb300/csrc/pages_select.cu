@@ -59,9 +59,11 @@ __device__ __forceinline__ void group_query(const PagesView &p, const GroupChann
     for (int i = 1; i < D / 32; i++) m = fmaxf(m, red[i]);
     if (tid < D) {
         const bool ok = m > 0.f && m < INFINITY;
-        const float inv = ok ? __fdiv_rn(127.f, m) : 0.f;
-        qi[tid] = ok ? static_cast<int8_t>(__float2int_rn(__fmul_rn(h, inv))) : 0;
-        qi[D + tid] = ok ? static_cast<int8_t>(__float2int_rn(__fmul_rn(l, inv))) : 0;
+        // (127 / m passes fp32 for m below 2^-121: such queries go by 2^100 first, which changes none of their bits)
+        const float up = m < 0x1p-100f ? 0x1p100f : 1.f;
+        const float inv = ok ? __fdiv_rn(127.f, m * up) : 0.f;
+        qi[tid] = ok ? static_cast<int8_t>(__float2int_rn(__fmul_rn(h * up, inv))) : 0;
+        qi[D + tid] = ok ? static_cast<int8_t>(__float2int_rn(__fmul_rn(l * up, inv))) : 0;
     }
     __syncthreads();
 }
