@@ -151,7 +151,8 @@ dq_status dq_pages_compact(const dq_pages_config *cfg, const dq_pages_buffers *b
  *   k, v : device, dtype, [n_tok][n_kv_heads][head_dim] with the given strides in
  *          elements (multiples of 8; channels are contiguous)
  * A page that more than one row holds is not written (DQ_EINVAL from
- * dq_pages_check: the row was forked after it was resized).  A non-finite value
+ * dq_pages_check: the row was forked after it was resized), nor is a row that
+ * `rows` names twice with new tokens (DQ_EINVAL).  A non-finite value
  * latches DQ_ENONFINITE; its block's held values are then finite but unspecified.
  * Errors: DQ_EINVAL, DQ_EALIGN, DQ_ECUDA.
  */

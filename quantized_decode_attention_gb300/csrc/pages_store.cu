@@ -108,11 +108,20 @@ __global__ void __launch_bounds__(ST_THREADS) append_kernel(PagesStoreArgs a) {
     const int lo = r.len - r.n < 0 ? 0 : r.len - r.n;  // first position written
     const int j = lo / p.P + blockIdx.x;
     if (r.row < 0 || r.n == 0 || j * p.P >= r.len) return;
+    // does the call bring tokens of this row a second time?  (two CTAs would write the same bytes)
+    bool twice = false;
+    if (a.r.rows)
+        for (int i = tid; i < a.r.n_rows; i += ST_THREADS)
+            twice |= a.r.rows[i] == r.row && i != static_cast<int>(blockIdx.y) && (!a.r.cu || a.r.cu[i + 1] > a.r.cu[i]);
     const int id = page_of(p, r.row, j);
     if (id < 0) return;
     const int t0 = lo > j * p.P ? lo - j * p.P : 0;  // new tokens of the page: [t0, t1)
     const int t1 = r.len - j * p.P < p.P ? r.len - j * p.P : p.P;
     const bool shared = p.refs[id] != 1;
+    if (a.r.rows && __syncthreads_or(twice)) {
+        if (tid == 0) atomicOr(p.status, PST_ARG);
+        return;
+    }
     if (shared) {
         if (tid == 0) atomicOr(p.status, PST_SHARED);
         return;

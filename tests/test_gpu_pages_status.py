@@ -1,7 +1,8 @@
 """What the paged cache's calls latch on the device, and how it is reported."""
 import pytest
 
-from test_gpu_pages import Filled, _i32
+import pages_ref as R
+from test_gpu_pages import Filled, _cu, _i32, _np
 
 pytestmark = pytest.mark.gpu
 
@@ -38,3 +39,35 @@ def test_check_names_each_bit_once_the_gravest_first():
     assert names(f.pool) == ["DQ_ETIMEOUT", "DQ_ENOMEM", "DQ_EINVAL", "DQ_EINVAL", "DQ_EINVAL", "DQ_ENONFINITE"]
     assert int(status[0]) == 0
 
+
+@pytest.mark.parametrize("rows, counts", [([0, 1, 0], [1, 1, 1]), ([1, 0, 0], [2, 1, 70]), ([0] * 130 + [1], [0] * 128 + [3, 2, 2])])
+def test_append_refuses_a_row_that_is_named_twice(rows, counts):
+    """Its pages and summaries stay as they are; the other row's token is written."""
+    import torch
+    f = Filled([200, 100], n_pages=20)
+    p = f.pool
+    before = [p.tensors[n].clone() for n in ("pages", "summary")]
+    n, at = sum(counts), sum(counts[:rows.index(1)])
+    x = torch.randn(n, 2, 128, device="cuda").to(torch.bfloat16)
+    p.append(0, x, x, rows=_i32(rows), cu=None if counts == [1] * 3 else _cu(counts), max_new=max(counts))
+    assert names(p) == ["DQ_EINVAL"]
+    own = p.tensors["table"][0, :4].tolist()
+    for t, b in zip((p.tensors[n] for n in ("pages", "summary")), before):
+        assert torch.equal(t.view(20, -1)[own], b.view(20, -1)[own])
+    new = counts[rows.index(1)]
+    k, v = (torch.empty(new, 2, 128, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    p.read(0, k, v, rows=_i32([1]), cu=_cu([new]), max_new=new)
+    p.check()
+    want = torch.tensor(R.quantise(_np(x[at:at + new]), 0)[2]).to(torch.bfloat16)
+    assert torch.equal(k.cpu(), want) and torch.equal(v.cpu(), want)
+
+
+def test_append_takes_a_row_that_is_named_again_without_tokens():
+    import torch
+    f = Filled([200, 100], n_pages=20)
+    x = torch.randn(3, 2, 128, device="cuda").to(torch.bfloat16)
+    f.pool.append(0, x, x, rows=_i32([0, 1, 0, -1, -1]), cu=_cu([2, 1, 0, 0, 0]), max_new=2)
+    k, v = torch.empty_like(x), torch.empty_like(x)
+    f.pool.read(0, k, v, cu=_cu([2, 1]), max_new=2)
+    f.pool.check()
+    assert torch.equal(k.cpu(), torch.tensor(R.quantise(_np(x), 0)[2]).to(torch.bfloat16)) and torch.equal(k, v)
