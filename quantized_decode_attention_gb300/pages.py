@@ -66,7 +66,10 @@ class PagePool:
     names): ``PagePool.allocate(cfg)`` makes them all; the constructor takes the caller's
     and makes status and workspace where none are given.  ``share()`` gives a second
     handle on the same sequences with a workspace of its own, for calls that may run at
-    the same time as this handle's (another stream, another captured graph).
+    the same time as this handle's (another stream, another captured graph); a handle
+    is kept until its calls have run.  Making one waits for the current stream, so that
+    the first call may be on any other (not while a graph is captured: there, the fill is
+    part of the graph).
 
     rows, cu, max_new as in dq_pages.h: int32 device tensors naming the call's table rows
     (None: 0, 1, ...) and where each row's new tokens begin (None: one token each);
@@ -101,6 +104,10 @@ class PagePool:
         self._int32, self._float32 = torch.int32, torch.float32
         self._current_device, self._raw_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
         self._torch = torch
+        # what was filled on the current stream (here, by allocate()) is there for a call on any other
+        with torch.cuda.device(self._index):
+            if not torch.cuda.is_current_stream_capturing():
+                torch.cuda.current_stream().synchronize()
 
     @classmethod
     def allocate(cls, cfg: PagesConfig, device="cuda") -> "PagePool":

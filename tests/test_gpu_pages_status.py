@@ -71,3 +71,43 @@ def test_append_takes_a_row_that_is_named_again_without_tokens():
     f.pool.read(0, k, v, cu=_cu([2, 1]), max_new=2)
     f.pool.check()
     assert torch.equal(k.cpu(), torch.tensor(R.quantise(_np(x), 0)[2]).to(torch.bfloat16)) and torch.equal(k, v)
+
+
+def test_a_new_handle_is_ready_on_every_stream():
+    """Memory that held something else, a long fill of the current stream, and the first call at once on another stream."""
+    import torch
+    f = Filled([2500, 1900, 40], n_pages=128, max_pages_per_seq=50)
+    q = f.queries([1, 1, 1])
+    want = f.attend(q, [1, 1, 1])
+    out, lse = torch.empty_like(q), torch.empty(3, 8, device="cuda")
+    side, size = torch.cuda.Stream(), f.pool.tensors["workspace"].numel()
+    x = torch.zeros(1 << 28, device="cuda")
+    for _ in range(3):
+        used = torch.full((size,), 255, dtype=torch.uint8, device="cuda")
+        torch.cuda.synchronize()
+        del used
+        for _ in range(20):
+            x.add_(1.0)
+        two = f.pool.share()
+        two.attention(0, q, out, lse=lse, stream=side)
+        torch.cuda.synchronize()
+        assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+        del two
+    f.pool.check()
+
+
+def test_a_handle_made_while_a_graph_is_captured():
+    import torch
+    f = Filled([2500, 1900, 40], n_pages=128, max_pages_per_seq=50)
+    q = f.queries([1, 1, 1])
+    want = f.attend(q, [1, 1, 1])[0]
+    out = torch.empty_like(q)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        two = f.pool.share()
+        two.attention(0, q, out)
+    for _ in range(3):
+        out.zero_()
+        g.replay()
+        assert torch.equal(out, want)
+    f.pool.check()
