@@ -117,12 +117,6 @@ __device__ __forceinline__ float e4m3_to_float(uint8_t s) {
     const uint32_t h = e4m3x2_to_half2(s);
     return __half2float(__ushort_as_half(static_cast<uint16_t>(h)));
 }
-// Value of one code: its sign and magnitude bits are binary16's with an exponent
-// smaller by 14 (binary16's subnormal .5 2^-14 among them).
-__device__ __forceinline__ float e2m1_to_float(uint32_t code) {
-    const uint32_t h = ((code & 7u) << 9) | ((code & 8u) << 12);
-    return __half2float(__ushort_as_half(static_cast<uint16_t>(h))) * 16384.f;
-}
 __device__ __forceinline__ uint8_t float_to_e4m3(float x) {
     uint16_t r;
     asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;\n" : "=h"(r) : "f"(0.f), "f"(x));
