@@ -38,7 +38,8 @@
  * - What only the device can see (row numbers, counts and page numbers out of
  *   range, a pool without free pages, non-finite input) is skipped there,
  *   latched in the status word and returned by dq_pages_check().  Nothing is
- *   read or written out of range for it.
+ *   read or written out of range for it; outputs that depend on it are
+ *   unspecified (a table's entry that names no page: those of the row's queries).
  * - Nothing is allocated: the caller owns all buffers.  Calls that share a
  *   workspace must be ordered (one stream, or events between streams; two
  *   captured graphs that may run at the same time need a workspace each).
@@ -85,7 +86,10 @@ typedef struct {
  *         int32 e, 12 unused bytes.  In units of 2^k_exp the largest is at most
  *         2^e times its byte and the smallest at least 2^e times its: bytes are
  *         rounded up and down, e = E - 7 for the largest magnitude m 2^E,
- *         m in [1/2, 1) (0 where every key is 0).
+ *         m in [1/2, 1) (0 where every key is 0).  dq_pages_append works it out
+ *         anew from all tokens that the page holds then; a copy or a move takes
+ *         it along.  A row that is shortened leaves it: until the next append to
+ *         the page it bounds the tokens that are left, and those that are gone.
  * table   int32 [max_seqs][max_pages_per_seq]: the pages of each row in order; -1
  *         behind the last.  All -1 at the start.
  * seq_len int32 [max_seqs], 0 at the start.
@@ -181,6 +185,14 @@ dq_status dq_pages_read(const dq_pages_config *cfg, const dq_pages_buffers *bufs
  *         of the row alone (ordinals, distinct, -1 ignored; cu must be NULL).
  *         Ordinals behind the row's last page are ignored.
  * A query that no key is visible to gives out = 0 and lse = -inf.
+ * Precision: logits, sums and accumulators are fp32.  Queries are held in binary16 after a
+ * scaling by a power of two (a bf16 channel below 2^-38 of its query's largest loses bits);
+ * exponentials are off by up to 2^-22; a weight is rounded to binary16 (11 bits) for its
+ * product with the value, once more at each raise of the running maximum within its 128 keys
+ * (rows of many new tokens), while the sum that divides takes it unrounded.  An output is so within about
+ * 2^-11 of sum_j weight_j |v_j| beside its own rounding.  The result is the same every time.
+ * A call over more than 2^35 (row, KV head, token) triples may be refused (DQ_EINVAL from
+ * dq_pages_check).
  * Errors: DQ_EINVAL, DQ_EALIGN, DQ_ECUDA.
  */
 dq_status dq_pages_attention(const dq_pages_config *cfg, const dq_pages_buffers *bufs, int layer, const void *q,
@@ -204,8 +216,10 @@ dq_status dq_pages_test_expire_wait(const dq_pages_config *cfg, const dq_pages_b
  *   sum_c Q+_c largest_c + Q-_c smallest_c
  * bounds sum_h q_h . k from above for every key k of the page.  It is computed in
  * whole numbers, so that it is the same in every order: Q+- (summed in 64 bits,
- * rounded to 32) go to round(Q+- 127 / max|Q+-|), ties to even, the page's bytes
- * are used as they are, and the sum is scaled by 2^e.
+ * rounded to fp32) go to the nearest whole number, ties to even, of Q+- r with
+ * r = 127 / max|Q+-|, quotient and product rounded to fp32; the page's bytes
+ * are used as they are, and the sum is scaled by 2^e.  With the rounded Q+- the score
+ * is a bound up to half a unit of Q+- for each channel's byte.
  *   sel : device int32 [n_rows][n_kv_heads][n_sel]: the ordinals of the first
  *         keep_first and the last keep_last pages and of those with the highest
  *         scores (the lower ordinal where scores are equal), n_sel in all,

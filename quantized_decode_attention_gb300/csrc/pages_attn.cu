@@ -40,7 +40,7 @@ constexpr float LN2 = 0.69314718055994530942f;
 constexpr float SLACK = 8.f, LIFT = 7.f;   // log2 units
 constexpr int CHUNK = 32;                  // tokens
 // Query rows of a row and KV head beyond which the tensor-core kernel takes over (8 rows of 32768 tokens, 4 query
-// heads a KV head; this kernel against that: 16 query rows 88 / 231 us, 32 160 / 231, 48 231 / 231, 64 303 / 231).
+// heads a KV head; this kernel against that: 16 query rows 88 / 237 us, 32 160 / 237, 48 232 / 237, 64 304 / 237).
 constexpr int PROMPT_ROWS = 32;
 constexpr int UNIT_COST = 2;               // chunks that a unit's beginning and end are worth (40 ragged rows: 76 us, with 0 94)
 constexpr int SHORT = 64;                  // places of a unit that CTAs do not share

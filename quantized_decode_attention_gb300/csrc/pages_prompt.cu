@@ -5,7 +5,7 @@
 // out = (sum p v) / (sum p).  4 D products and one exponential for each (query, key)
 // pair: the kernel is bound by the tensor cores and, nearly as much, by the exponentials
 // and their conversions.  2048 new tokens over 16384 (32 / 8 heads, head_dim 128) take
-// 431 us, 1.2 PFLOP/s; over 131072, 3.3 ms, 1.32.
+// 433 us, 1.19 PFLOP/s; over 131072, 3.3 ms, 1.32.
 //
 // Work.  A unit is 256 query rows (256 / G tokens with their G query heads) of one row and
 // KV head, in two tiles of 128.  It walks the keys that its last token sees, 128 at a

@@ -188,7 +188,8 @@ class PagePool:
         self._call("compact", stream)
 
     def append(self, layer, k, v, rows=None, cu=None, max_new=None, stream=None):
-        """Quantise the rows' newest tokens (k, v: [n_tok, n_kv_heads, head_dim]) into their pages."""
+        """Quantise the rows' newest tokens (k, v: [n_tok, n_kv_heads, head_dim]) into their pages; `rows` names a row
+        with new tokens once."""
         kp, n, kt, kh = self._tokens(k, "k", self._hkv)
         vp, _, vt, vh = self._tokens(v, "v", self._hkv, n)
         self._call("append", stream, layer, kp, vp, kt, kh, vt, vh, *self._rows(rows, cu, n, max_new))
