@@ -201,6 +201,48 @@ dq_status dq_pages_attention(const dq_pages_config *cfg, const dq_pages_buffers 
                              float sm_scale, void *stream);
 
 /*
+ * Cross attention: queries that are not tokens of the row (a decoder's over an encoder's
+ * states, appended once) see ALL of it:
+ *   out_h = sum_j softmax_j(sm_scale q_h . k_j) v_j,  j < seq_len
+ * cu and max_new count queries: a row may have any number of them, more than it has
+ * tokens (the beams of a request are best one row's queries: the row is then read once),
+ * and `rows` may name a row more than once.  Otherwise as dq_pages_attention without sel.
+ * Errors: DQ_EINVAL, DQ_EALIGN, DQ_ECUDA.
+ */
+dq_status dq_pages_cross(const dq_pages_config *cfg, const dq_pages_buffers *bufs, int layer, const void *q, long long q_tok_stride,
+                         long long q_head_stride, void *out, float *lse, const int *rows, const int *cu, int n_rows, int n_tok,
+                         int max_new, float sm_scale, void *stream);
+
+/*
+ * Attention of rows that share the beginning of their pages (forks of one row): what a
+ * group of rows has in common is read and computed once for all its queries.
+ *   groups : device int32 [n_groups + 1], ascending: group g is the call's rows
+ *            [groups[g], groups[g + 1]); NULL = one group of all (n_groups 1)
+ *   plan   : device int32 [n_rows][2], 8-byte aligned.  dq_pages_common writes it: for
+ *            each row the tokens that its group has in common and a table row that holds
+ *            them.  Common are the whole leading pages that the tables of all rows of the
+ *            group name alike and that every new token sees all of; none in a group of one
+ *            row, or for a row in no group.  Rows that hold or bring nothing do not count.
+ *            It stays true until a row of the call is resized, forked into, moved by
+ *            dq_pages_compact or brings other tokens: one plan serves all layers.
+ * dq_pages_shared gives what dq_pages_attention of the same rows does (to rounding: the
+ * parts are added up in another order), whatever the groups have in common.
+ *   max_group : a bound on the new tokens of one group (the host plans the launches with
+ *               it; n_tok always is one).  A group that brings more is DQ_EINVAL from
+ *               dq_pages_check.
+ *   scratch   : device, dq_pages_shared_bytes(n_tok), need not be initialised; not to be
+ *               shared by calls that may run at the same time
+ * Errors: DQ_EINVAL, DQ_EALIGN, DQ_ECUDA.
+ */
+dq_status dq_pages_common(const dq_pages_config *cfg, const dq_pages_buffers *bufs, const int *rows, const int *cu, int n_rows,
+                          const int *groups, int n_groups, int *plan, void *stream);
+dq_status dq_pages_shared_bytes(const dq_pages_config *cfg, int n_tok, size_t *bytes); /* host only */
+dq_status dq_pages_shared(const dq_pages_config *cfg, const dq_pages_buffers *bufs, int layer, const void *q, long long q_tok_stride,
+                          long long q_head_stride, void *out, float *lse, const int *rows, const int *cu, int n_rows, int n_tok,
+                          int max_new, const int *groups, int n_groups, int max_group, const int *plan, void *scratch,
+                          float sm_scale, void *stream);
+
+/*
  * Test support for the timeout path: an attention call over rows 0 .. n_rows - 1 (sm_scale 1, no chosen pages) whose barriers
  * wait for an arrival that nobody makes, for limit_ns at most (clamped to [1000, 10^9]) instead of the 2 s of
  * every other call.  The kernel returns, `out` holds nothing of use, and dq_pages_check reports DQ_ETIMEOUT.
@@ -232,6 +274,42 @@ dq_status dq_pages_test_expire_wait(const dq_pages_config *cfg, const dq_pages_b
 dq_status dq_pages_select(const dq_pages_config *cfg, const dq_pages_buffers *bufs, int layer, const void *q,
                           long long q_tok_stride, long long q_head_stride, const int *rows, int n_rows, int *sel,
                           int n_sel, int keep_first, int keep_last, void *stream);
+
+/*
+ * Scores of held tokens by the attention weight that they get, and the eviction of those
+ * with low ones.
+ *   scores : device fp32 [max_seqs][n_kv_heads][cap] for one layer, by table row; for
+ *            dq_pages_evict those of all layers, [n_layers][max_seqs][n_kv_heads][cap].
+ *            cap bounds the length of the rows in question (a longer one is left alone,
+ *            DQ_EINVAL from dq_pages_check).
+ *
+ * dq_pages_weigh, after the attention of the same queries, which gives lse
+ * [n_tok][n_q_heads]: with w_j the sum of exp(sm_scale q_h . k_j - lse_h) over the row's n
+ * new tokens that see token j (j <= their position) and the query heads of j's KV head,
+ *   score_j = w_j for the n new tokens, score_j + w_j for those before them.
+ * (So scores need no clearing where every token is weighed in the call that brings it.)
+ * Scores behind seq_len are left as they are, those of rows that bring nothing too.  A query
+ * whose lse is -inf adds nothing.  `rows` names a row that brings tokens once: otherwise its
+ * scores are left as they are (DQ_EINVAL from dq_pages_check).  Precision: as
+ * dq_pages_attention's logits; the sums are fp32 in an order that is the same every time.
+ *
+ * dq_pages_evict, for all layers at once: row dst[i], of k = its seq_len tokens, which a
+ * dq_pages_resize has given room, receives for each layer and KV head k tokens of row
+ * src[i] in their order, as they are held: the first keep_first, the last keep_last, and of
+ * those between them the ones with the highest scores (the earlier one where scores are
+ * equal; NaN is below all numbers), with their scores; the pages' summaries are as
+ * dq_pages_append would have them.  src stays as it is (dq_pages_resize to 0 frees it), and
+ * may share its pages with others.  Every dst is named once and is no src of the call,
+ * 0 <= k <= the length of src, and keep_first + keep_last <= k unless k is that length: else
+ * nothing is written for the pair (DQ_EINVAL from dq_pages_check).  A page of dst that more
+ * than one row holds is not written (the same).  Pairs with a negative row are skipped.
+ * Errors: DQ_EINVAL, DQ_EALIGN, DQ_ECUDA.
+ */
+dq_status dq_pages_weigh(const dq_pages_config *cfg, const dq_pages_buffers *bufs, int layer, const void *q, long long q_tok_stride,
+                         long long q_head_stride, const float *lse, float *scores, int cap, const int *rows, const int *cu,
+                         int n_rows, int n_tok, int max_new, float sm_scale, void *stream);
+dq_status dq_pages_evict(const dq_pages_config *cfg, const dq_pages_buffers *bufs, float *scores, int cap, const int *src,
+                         const int *dst, int n, int keep_first, int keep_last, void *stream);
 
 /*
  * Synchronize `stream`, then return the gravest of what earlier calls on these buffers

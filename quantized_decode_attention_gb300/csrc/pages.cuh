@@ -43,6 +43,7 @@ struct PageRow {
     int row;    // table row, -1: padding (nothing held)
     int len;    // tokens held
     int q0, n;  // the call's tokens [q0, q0 + n) are positions [len - n, len)
+    int from;   // attention: the first position that is looked at, a page's first
 };
 
 // Row i of the call, checked: whatever is out of range is latched and holds nothing.
@@ -56,7 +57,7 @@ __device__ __forceinline__ PageRow page_row(const PagesView &p, const PagesRows 
         bad = true;
         o.q0 = o.n = 0;
     }
-    o.len = 0;
+    o.len = o.from = 0;
     if (o.row >= p.max_seqs) {
         bad = true;
         o.row = -1;
@@ -72,7 +73,84 @@ __device__ __forceinline__ PageRow page_row(const PagesView &p, const PagesRows 
     return o;
 }
 
-__device__ __forceinline__ bool takes(const PagesAttnArgs &a, const PageRow &r) { return r.n * a.p.G > a.over && r.n * a.p.G <= a.most; }
+// The arguments of a kernel for launches of one kind; step: positions from one query token of a row
+// to the next, 0 where all see the whole row.
+template <int MODE>
+struct InMode : PagesAttnArgs {
+    static constexpr int mode = MODE, step = MODE == PAGES_NEWEST || MODE == PAGES_OWN;
+};
+
+// The last position that the first of a row's query tokens sees.
+template <class A>
+__device__ __forceinline__ int first_sees(const A &a, const PageRow &r) { return a.step ? r.len - r.n : r.len - 1; }
+
+// Row i of an attention launch, checked.  A group's row is the one that its common pages are read
+// from, as long as they are, and its tokens are those of all its rows.
+template <class A>
+__device__ __forceinline__ PageRow attn_row(const A &a, int i) {
+    PageRow o;
+    if (a.mode == PAGES_COMMON) {
+        const int g0 = a.groups ? a.groups[i] : 0, g1 = a.groups ? a.groups[i + 1] : a.call_rows;
+        o = PageRow{-1, 0, 0, 0, 0};
+        if (g0 < 0 || g1 > a.call_rows || g0 > g1) {
+            atomicOr(a.p.status, PST_ARG);
+            return o;
+        }
+        if (g0 == g1) return o;
+        const int2 what = reinterpret_cast<const int2 *>(a.plan)[g0];
+        const int q0 = a.r.cu ? a.r.cu[g0] : g0, n = (a.r.cu ? a.r.cu[g1] : g1) - q0;
+        if (what.x == 0) return o;
+        if (q0 < 0 || n < 0 || n > a.r.max_new || q0 > a.r.n_tok - n || what.x < 0 || what.x % a.p.P || what.y < 0 || what.y >= a.p.max_seqs ||
+            what.x > a.p.seq_len[what.y] || what.x > a.p.M * a.p.P) {
+            atomicOr(a.p.status, PST_ARG);
+            return o;
+        }
+        return PageRow{what.y, what.x, q0, n, 0};
+    }
+    o = page_row(a.p, a.r, i);
+    if (a.mode == PAGES_OWN && o.len > 0) {
+        o.from = a.plan[2 * i];
+        if (o.from < 0 || o.from % a.p.P || (o.from > 0 && o.from > o.len - o.n)) {
+            atomicOr(a.p.status, PST_ARG);
+            o.from = 0;
+        }
+    }
+    return o;
+}
+// The same, known to be in order: `row` and `keys` (len - from) are what the check found.
+template <class A>
+__device__ __forceinline__ PageRow known_row(const A &a, int i, int row, int keys) {
+    PageRow o;
+    o.row = row;
+    if (a.mode == PAGES_COMMON) {
+        const int g0 = a.groups ? a.groups[i] : 0, g1 = a.groups ? a.groups[i + 1] : a.call_rows;
+        o.q0 = a.r.cu ? a.r.cu[g0] : g0;
+        o.n = (a.r.cu ? a.r.cu[g1] : g1) - o.q0;
+        o.len = keys;
+        o.from = 0;
+        return o;
+    }
+    o.q0 = a.r.cu ? a.r.cu[i] : i;
+    o.n = a.r.cu ? a.r.cu[i + 1] - o.q0 : 1;
+    o.len = a.mode == PAGES_OWN && row >= 0 ? a.p.seq_len[row] : keys;
+    o.from = o.len - keys;
+    return o;
+}
+
+// Where query row `row` (token, query head of the group) of a row and KV head stands among the call's queries.
+template <class A>
+__device__ __forceinline__ long long query_of(const A &a, const PageRow &r, int head, int row) {
+    const int tok = row / a.p.G;
+    return (static_cast<long long>(r.q0) + tok) * a.p.Hq + head * a.p.G + row - tok * a.p.G;
+}
+// Maxima and sums of the parts, behind their accumulators.
+template <int D, class A>
+__device__ __forceinline__ float *part_sums(const A &a) {
+    return a.part + static_cast<long long>(a.r.n_tok) * a.p.Hq * D;
+}
+
+template <class A>
+__device__ __forceinline__ bool takes(const A &a, const PageRow &r) { return r.n * a.p.G > a.over && r.n * a.p.G <= a.most; }
 
 // Page number of ordinal j of a row (0 <= j < M), -1 (latched) where the table's entry
 // is no page of the pool.

@@ -119,6 +119,26 @@ dq_status launched(int e, const char *what) {
     return ok();
 }
 
+// What turns a product of a query and a key's code values into a logit in log2 units.
+float logit_scale(const dq_pages_config *c, float sm_scale) {
+    return static_cast<float>(std::ldexp(static_cast<double>(sm_scale) * 1.4426950408889634074, c->k_exp));
+}
+
+constexpr int PAGES_MAX_TOKENS = 1 << 22;  // of a row
+
+dq_status check_cap(int cap) {
+    if (cap < 1 || cap > PAGES_MAX_TOKENS) return fail(DQ_EINVAL, "cap outside [1, 2^22]");
+    return DQ_OK;
+}
+
+dq_status check_groups(const int *groups, int n_groups, int n_rows, const int *plan) {
+    if (n_groups < 1 || n_groups > n_rows || (!groups && n_groups != 1))
+        return fail(DQ_EINVAL, "n_groups outside [1, n_rows], or more than 1 without groups");
+    if (!plan) return fail(DQ_EINVAL, "plan is NULL");
+    if (!aligned4(groups) || (reinterpret_cast<uintptr_t>(plan) & 7u)) return fail(DQ_EALIGN, "groups not aligned to 4 bytes, or plan to 8");
+    return DQ_OK;
+}
+
 // Checked arguments of an attention call.
 dq_status attention_args(dq::PagesAttnArgs &a, const dq_pages_config *cfg, const dq_pages_buffers *bufs, int layer, const void *q,
                          long long q_tok_stride, long long q_head_stride, void *out, float *lse, const int *rows, const int *cu,
@@ -141,7 +161,7 @@ dq_status attention_args(dq::PagesAttnArgs &a, const dq_pages_config *cfg, const
     a.lse = lse;
     a.sel = sel;
     a.n_sel = sel ? n_sel : 0;
-    a.scale_log2 = static_cast<float>(std::ldexp(static_cast<double>(sm_scale) * 1.4426950408889634074, cfg->k_exp));
+    a.scale_log2 = logit_scale(cfg, sm_scale);
     a.out_scale = std::ldexp(1.0f, cfg->v_exp);
     uint8_t *ws = static_cast<uint8_t *>(bufs->workspace) + dq::pages_ws_lists(cfg->n_pages);
     a.tickets = reinterpret_cast<int *>(ws);
@@ -242,7 +262,103 @@ dq_status dq_pages_attention(const dq_pages_config *cfg, const dq_pages_buffers 
     const dq_status s = attention_args(a, cfg, bufs, layer, q, q_tok_stride, q_head_stride, out, lse, rows, cu, n_rows, n_tok,
                                        max_new, sel, n_sel, sm_scale);
     if (s != DQ_OK) return s;
-    return launched(dq::launch_pages_attention(a, device_sms(), stream), "attention launch");
+    return launched(dq::launch_pages_attention(a, dq::PAGES_NEWEST, device_sms(), stream), "attention launch");
+}
+
+dq_status dq_pages_cross(const dq_pages_config *cfg, const dq_pages_buffers *bufs, int layer, const void *q, long long q_tok_stride,
+                         long long q_head_stride, void *out, float *lse, const int *rows, const int *cu, int n_rows, int n_tok,
+                         int max_new, float sm_scale, void *stream) {
+    dq::PagesAttnArgs a{};
+    const dq_status s = attention_args(a, cfg, bufs, layer, q, q_tok_stride, q_head_stride, out, lse, rows, cu, n_rows, n_tok,
+                                       max_new, nullptr, 0, sm_scale);
+    if (s != DQ_OK) return s;
+    return launched(dq::launch_pages_attention(a, dq::PAGES_ALL, device_sms(), stream), "cross attention launch");
+}
+
+dq_status dq_pages_common(const dq_pages_config *cfg, const dq_pages_buffers *bufs, const int *rows, const int *cu, int n_rows,
+                          const int *groups, int n_groups, int *plan, void *stream) {
+    dq::PagesCommonArgs a{};
+    dq_status s = view(cfg, bufs, -1, false, a.p);
+    if (s != DQ_OK) return s;
+    constexpr int any = 1 << 24;  // tokens: none of them is looked at
+    if ((s = call_rows(cfg, 0, rows, cu, n_rows, cu ? any : n_rows, cu ? any : 1, a.r)) != DQ_OK) return s;
+    if ((s = check_groups(groups, n_groups, n_rows, plan)) != DQ_OK) return s;
+    a.groups = groups;
+    a.n_groups = n_groups;
+    a.plan = plan;
+    return launched(dq::launch_pages_common(a, stream), "common launch");
+}
+
+dq_status dq_pages_shared_bytes(const dq_pages_config *cfg, int n_tok, size_t *bytes) {
+    if (!cfg || !bytes) return fail(DQ_EINVAL, "NULL argument");
+    const dq_status s = check_cfg(cfg);
+    if (s != DQ_OK) return s;
+    if (n_tok < 1 || n_tok > (1 << 24)) return fail(DQ_EINVAL, "n_tok outside [1, 2^24]");
+    *bytes = static_cast<size_t>(n_tok) * cfg->n_q_heads * (cfg->head_dim + 2) * 4;
+    return ok();
+}
+
+dq_status dq_pages_shared(const dq_pages_config *cfg, const dq_pages_buffers *bufs, int layer, const void *q, long long q_tok_stride,
+                          long long q_head_stride, void *out, float *lse, const int *rows, const int *cu, int n_rows, int n_tok,
+                          int max_new, const int *groups, int n_groups, int max_group, const int *plan, void *scratch,
+                          float sm_scale, void *stream) {
+    dq::PagesAttnArgs a{};
+    dq_status s = attention_args(a, cfg, bufs, layer, q, q_tok_stride, q_head_stride, out, lse, rows, cu, n_rows, n_tok, max_new,
+                                 nullptr, 0, sm_scale);
+    if (s != DQ_OK) return s;
+    if ((s = check_groups(groups, n_groups, n_rows, plan)) != DQ_OK) return s;
+    if (max_group < 1 || max_group > n_tok) return fail(DQ_EINVAL, "max_group outside [1, n_tok]");
+    if (!scratch) return fail(DQ_EINVAL, "scratch is NULL");
+    if (!aligned16(scratch)) return fail(DQ_EALIGN, "scratch not 16-byte aligned");
+    a.groups = groups;
+    a.plan = plan;
+    a.call_rows = n_rows;
+    a.part = static_cast<float *>(scratch);
+    return launched(dq::launch_pages_shared(a, n_groups, max_group, device_sms(), stream), "shared attention launch");
+}
+
+dq_status dq_pages_weigh(const dq_pages_config *cfg, const dq_pages_buffers *bufs, int layer, const void *q, long long q_tok_stride,
+                         long long q_head_stride, const float *lse, float *scores, int cap, const int *rows, const int *cu,
+                         int n_rows, int n_tok, int max_new, float sm_scale, void *stream) {
+    dq::PagesWeighArgs a{};
+    dq_status s = view(cfg, bufs, layer, false, a.p);
+    if (s != DQ_OK) return s;
+    if ((s = call_rows(cfg, layer, rows, cu, n_rows, n_tok, max_new, a.r)) != DQ_OK) return s;
+    if (!q || !lse || !scores) return fail(DQ_EINVAL, "q / lse / scores is NULL");
+    if (!aligned16(q) || (q_tok_stride | q_head_stride) & 7)
+        return fail(DQ_EALIGN, "q not 16-byte aligned, or a stride is no multiple of 8 elements");
+    if (!aligned4(lse) || !aligned4(scores)) return fail(DQ_EALIGN, "lse / scores not aligned to 4 bytes");
+    if ((s = check_cap(cap)) != DQ_OK) return s;
+    if (!std::isfinite(sm_scale)) return fail(DQ_EINVAL, "sm_scale is not finite");
+    a.q = static_cast<const uint16_t *>(q);
+    a.qt = q_tok_stride;
+    a.qh = q_head_stride;
+    a.lse = lse;
+    a.scores = scores;
+    a.cap = cap;
+    a.scale_log2 = logit_scale(cfg, sm_scale);
+    return launched(dq::launch_pages_weigh(a, device_sms(), stream), "weigh launch");
+}
+
+dq_status dq_pages_evict(const dq_pages_config *cfg, const dq_pages_buffers *bufs, float *scores, int cap, const int *src,
+                         const int *dst, int n, int keep_first, int keep_last, void *stream) {
+    dq::PagesEvictArgs a{};
+    dq_status s = view(cfg, bufs, -1, false, a.p);
+    if (s != DQ_OK) return s;
+    if (!scores || !src || !dst) return fail(DQ_EINVAL, "scores / src / dst is NULL");
+    if (!aligned4(scores) || !aligned4(src) || !aligned4(dst)) return fail(DQ_EALIGN, "scores / src / dst not aligned to 4 bytes");
+    if ((s = check_cap(cap)) != DQ_OK) return s;
+    if (n < 1 || n > DQ_PAGES_MAX_ROWS) return fail(DQ_EINVAL, "n outside [1, %d]", DQ_PAGES_MAX_ROWS);
+    if (keep_first < 0 || keep_last < 0 || keep_first > PAGES_MAX_TOKENS || keep_last > PAGES_MAX_TOKENS)
+        return fail(DQ_EINVAL, "keep_first / keep_last outside [0, 2^22]");
+    a.scores = scores;
+    a.cap = cap;
+    a.src = src;
+    a.dst = dst;
+    a.n = n;
+    a.keep_first = keep_first;
+    a.keep_last = keep_last;
+    return launched(dq::launch_pages_evict(a, device_sms(), stream), "evict launch");
 }
 
 dq_status dq_pages_test_expire_wait(const dq_pages_config *cfg, const dq_pages_buffers *bufs, int layer, const void *q,
@@ -254,7 +370,7 @@ dq_status dq_pages_test_expire_wait(const dq_pages_config *cfg, const dq_pages_b
     if (s != DQ_OK) return s;
     a.owed = 1;
     a.wait_ns = limit_ns < 1000ULL ? 1000ULL : (limit_ns > 1000000000ULL ? 1000000000ULL : limit_ns);
-    return launched(dq::launch_pages_attention(a, device_sms(), stream), "expire-wait launch");
+    return launched(dq::launch_pages_attention(a, dq::PAGES_NEWEST, device_sms(), stream), "expire-wait launch");
 }
 
 dq_status dq_pages_select(const dq_pages_config *cfg, const dq_pages_buffers *bufs, int layer, const void *q,

@@ -68,9 +68,21 @@ struct PagesReadArgs {
     PagesRows r;
     uint16_t *k, *v;
 };
+// Which queries an attention launch answers, over which of a row's tokens: a constant of each kernel
+// (as a variable it costs attention of single tokens 7 %).
+enum : int {
+    PAGES_NEWEST = 0,  // the call's rows' newest tokens, over what they hold up to them
+    PAGES_ALL = 1,     // queries of the call's rows, over all they hold
+    PAGES_COMMON = 2,  // the tokens of groups of rows, over the pages that a group has in common: parts
+    PAGES_OWN = 3      // the call's rows' newest tokens, over what is behind those pages, from their parts on
+};
 struct PagesAttnArgs {
     PagesView p;
-    PagesRows r;
+    PagesRows r;          // (PAGES_COMMON: of the groups)
+    const int *groups;    // where each group begins among call_rows rows (NULL: one group of all)
+    const int *plan;      // [call_rows][2]: tokens in common, the table row that they are read from
+    int call_rows;
+    float *part;          // the parts of all queries: accumulators [n_tok Hq][d], then [n_tok Hq][2] maximum and sum
     const uint16_t *q;
     long long qt, qh;
     uint16_t *out;
@@ -85,6 +97,30 @@ struct PagesAttnArgs {
     float *records;       // workspace: [PAGES_MAX_CTAS][2][PAGES_REC_FLOATS]
     unsigned long long wait_ns;  // longest wait on a barrier
     unsigned owed;        // arrivals that barriers wait for and nobody makes: 0 but in tests of waits that run out
+};
+struct PagesCommonArgs {
+    PagesView p;
+    PagesRows r;
+    const int *groups;
+    int n_groups;
+    int *plan;
+};
+struct PagesWeighArgs {
+    PagesView p;
+    PagesRows r;
+    const uint16_t *q;
+    long long qt, qh;
+    const float *lse;
+    float *scores;        // [max_seqs][Hkv][cap] of the layer
+    int cap;
+    float scale_log2;
+};
+struct PagesEvictArgs {
+    PagesView p;          // of the pool
+    float *scores;        // [n_layers][max_seqs][Hkv][cap]
+    int cap;
+    const int *src, *dst;
+    int n, keep_first, keep_last;
 };
 struct PagesSelectArgs {
     PagesView p;
@@ -102,9 +138,15 @@ int launch_pages_fork(const PagesView &p, const int *src, const int *dst, int n,
 int launch_pages_compact(const PagesView &p, int *ws, int num_sms, void *stream);
 int launch_pages_append(const PagesStoreArgs &a, void *stream);
 int launch_pages_read(const PagesReadArgs &a, void *stream);
-int launch_pages_attention(PagesAttnArgs a, int num_sms, void *stream);
+int launch_pages_attention(PagesAttnArgs a, int mode, int num_sms, void *stream);
+int launch_pages_few_shared(const PagesAttnArgs &a, int mode, int grid, void *stream);
 // many new tokens: the tensor-core kernel on at most `grid` CTAs
-int launch_pages_prompt(const PagesAttnArgs &a, int grid, void *stream);
+int launch_pages_prompt(const PagesAttnArgs &a, int mode, int grid, void *stream);
+int launch_pages_prompt_shared(const PagesAttnArgs &a, int mode, int grid, void *stream);
 int launch_pages_select(const PagesSelectArgs &a, int num_sms, void *stream);
+int launch_pages_common(const PagesCommonArgs &a, void *stream);
+int launch_pages_shared(const PagesAttnArgs &a, int n_groups, int max_group, int num_sms, void *stream);
+int launch_pages_weigh(const PagesWeighArgs &a, int num_sms, void *stream);
+int launch_pages_evict(const PagesEvictArgs &a, int num_sms, void *stream);
 
 }  // namespace dq

@@ -39,9 +39,16 @@ def _load():
         L.dq_pages_read.argtypes = [cfg, buf, I, P, P, P, P, I, I, I, P]
         L.dq_pages_attention.argtypes = [cfg, buf, I, P, LL, LL, P, P, P, P, I, I, I, P, I, C.c_float, P]
         L.dq_pages_select.argtypes = [cfg, buf, I, P, LL, LL, P, I, P, I, I, I, P]
+        L.dq_pages_cross.argtypes = [cfg, buf, I, P, LL, LL, P, P, P, P, I, I, I, C.c_float, P]
+        L.dq_pages_common.argtypes = [cfg, buf, P, P, I, P, I, P, P]
+        L.dq_pages_shared_bytes.argtypes = [cfg, I, C.POINTER(C.c_size_t)]
+        L.dq_pages_shared.argtypes = [cfg, buf, I, P, LL, LL, P, P, P, P, I, I, I, P, I, I, P, P, C.c_float, P]
+        L.dq_pages_weigh.argtypes = [cfg, buf, I, P, LL, LL, P, P, I, P, P, I, I, I, C.c_float, P]
+        L.dq_pages_evict.argtypes = [cfg, buf, P, I, P, P, I, I, I, P]
         L.dq_pages_check.argtypes = [buf, P]
         L.dq_pages_test_expire_wait.argtypes = [cfg, buf, I, P, LL, LL, P, P, I, I, I, C.c_ulonglong, P]
-        for f in ("sizes", "resize", "fork", "compact", "append", "read", "attention", "select", "check", "test_expire_wait"):
+        for f in ("sizes", "resize", "fork", "compact", "append", "read", "attention", "cross", "common", "shared_bytes", "shared",
+                  "select", "weigh", "evict", "check", "test_expire_wait"):
             getattr(L, "dq_pages_" + f).restype = C.c_int
         _ready = L
     return _ready
@@ -100,7 +107,8 @@ class PagePool:
         self._index, self._hkv, self._hq, self._d = self.device.index, cfg.n_kv_heads, cfg.n_q_heads, cfg.head_dim
         self._scale = cfg.head_dim ** -0.5
         L = _load()
-        self._f = {n: getattr(L, "dq_pages_" + n) for n in ("resize", "fork", "compact", "append", "read", "attention", "select")}
+        self._f = {n: getattr(L, "dq_pages_" + n) for n in ("resize", "fork", "compact", "append", "read", "attention", "cross",
+                                                            "common", "shared", "select", "weigh", "evict")}
         self._int32, self._float32 = torch.int32, torch.float32
         self._current_device, self._raw_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
         self._torch = torch
@@ -172,6 +180,24 @@ class PagePool:
         n_rows = cu.numel() - 1
         return self._ints(rows, "rows", n_rows), self._ints(cu, "cu"), n_rows, n_tok, n_tok if max_new is None else max_new
 
+    def _lse(self, lse, n):
+        if lse.dtype is not self._float32 or lse.get_device() != self._index or not lse.is_contiguous() or lse.numel() != n * self._hq:
+            raise ValueError(f"lse must be contiguous fp32 [{n}, {self._hq}] on {self.device}")
+        return lse.data_ptr()
+
+    def _scores(self, scores, *lead):
+        """(pointer, cap) of scores [*lead, max_seqs, n_kv_heads, cap]."""
+        if scores.dtype is not self._float32 or scores.get_device() != self._index or not scores.is_contiguous():
+            raise ValueError(f"scores must be contiguous fp32 on {self.device}")
+        want = (*lead, self.cfg.max_seqs, self._hkv)
+        if tuple(scores.shape[:-1]) != want:
+            raise ValueError(f"scores must be {[*want, 'cap']} (got {tuple(scores.shape)})")
+        return scores.data_ptr(), scores.shape[-1]
+
+    def _groups(self, groups, plan, n_rows):
+        """(groups, n_groups, plan) of a call with n_rows rows."""
+        return self._ints(groups, "groups"), 1 if groups is None else groups.numel() - 1, self._ints(plan, "plan", 2 * n_rows)
+
     # ---- operators ----
     def resize(self, rows, lens, stream=None):
         """Set rows' lengths (int32 [n]; rows None: 0, 1, ...): frees, copies shared last pages on write, grows.
@@ -208,17 +234,69 @@ class PagePool:
         qp, n, qt, qh = self._tokens(q, "q", self._hq)
         op = self._tokens(out, "out", self._hq, n)[0]
         self._whole(out, "out")
-        lp = sp = None
+        sp = None
         n_sel = 0
-        if lse is not None:
-            if lse.dtype is not self._float32 or lse.get_device() != self._index or not lse.is_contiguous() or lse.numel() != n * self._hq:
-                raise ValueError(f"lse must be contiguous fp32 [{n}, {self._hq}] on {self.device}")
-            lp = lse.data_ptr()
+        lp = None if lse is None else self._lse(lse, n)
         r = self._rows(rows, cu, n, max_new)
         if sel is not None:
             n_sel = sel.shape[-1]
             sp = self._ints(sel, "sel", r[2] * self._hkv * n_sel)
         self._call("attention", stream, layer, qp, qt, qh, op, lp, *r, sp, n_sel, self._scale if sm_scale is None else sm_scale)
+
+    def cross(self, layer, q, out, rows=None, cu=None, max_new=None, lse=None, sm_scale=None, stream=None):
+        """Cross attention: queries that are not the row's tokens (q, out: [n_tok, n_q_heads, head_dim]; cu and max_new
+        count them; None: one for each row) over all that their rows hold; lse: optional fp32 [n_tok, n_q_heads]."""
+        qp, n, qt, qh = self._tokens(q, "q", self._hq)
+        op = self._tokens(out, "out", self._hq, n)[0]
+        self._whole(out, "out")
+        self._call("cross", stream, layer, qp, qt, qh, op, None if lse is None else self._lse(lse, n), *self._rows(rows, cu, n, max_new),
+                   self._scale if sm_scale is None else sm_scale)
+
+    def common(self, plan, groups=None, rows=None, cu=None, stream=None):
+        """What the rows of each group have in common (whole leading pages that all of them hold and all their new tokens
+        see), into plan int32 [n_rows, 2] for shared(), in every layer.  groups: int32 [n_groups + 1], where each group's
+        rows begin among the call's (None: one group of all)."""
+        n = plan.shape[0]
+        g, n_groups, pp = self._groups(groups, plan, n)
+        self._call("common", stream, self._ints(rows, "rows", n), None if cu is None else self._ints(cu, "cu", n + 1), n, g, n_groups, pp)
+
+    def shared_scratch(self, n_tok):
+        """The buffer that shared() takes for calls of up to n_tok tokens."""
+        n = C.c_size_t()
+        _raise(_load().dq_pages_shared_bytes(self._c, n_tok, C.byref(n)))
+        return self._torch.empty(n.value, dtype=self._torch.uint8, device=self.device)
+
+    def shared(self, layer, q, out, plan, scratch, groups=None, max_group=None, rows=None, cu=None, max_new=None, lse=None,
+               sm_scale=None, stream=None):
+        """attention() of rows whose groups begin with the same pages: what plan (of common(), the same groups, rows and
+        cu) says that a group has in common is read once for all its queries.  max_group: a bound on one group's new
+        tokens; scratch: of shared_scratch()."""
+        qp, n, qt, qh = self._tokens(q, "q", self._hq)
+        op = self._tokens(out, "out", self._hq, n)[0]
+        self._whole(out, "out")
+        self._whole(scratch, "scratch")
+        if scratch.get_device() != self._index or scratch.numel() * scratch.element_size() < n * self._hq * (self._d + 2) * 4:
+            raise ValueError(f"scratch: the buffer that shared_scratch({n}) gives is needed")
+        r = self._rows(rows, cu, n, max_new)
+        g, n_groups, pp = self._groups(groups, plan, r[2])
+        self._call("shared", stream, layer, qp, qt, qh, op, None if lse is None else self._lse(lse, n), *r, g, n_groups,
+                   n if max_group is None else max_group, pp, scratch.data_ptr(), self._scale if sm_scale is None else sm_scale)
+
+    def weigh(self, layer, q, lse, scores, rows=None, cu=None, max_new=None, sm_scale=None, stream=None):
+        """The attention weight that the rows' newest tokens (q: [n_tok, n_q_heads, head_dim], with the lse of their
+        attention) give to each held token, summed over them and a KV head's query heads: set for the newest tokens
+        themselves, added for those before.  scores: fp32 [max_seqs, n_kv_heads, cap], by table row."""
+        qp, n, qt, qh = self._tokens(q, "q", self._hq)
+        self._call("weigh", stream, layer, qp, qt, qh, self._lse(lse, n), *self._scores(scores), *self._rows(rows, cu, n, max_new),
+                   self._scale if sm_scale is None else sm_scale)
+
+    def evict(self, scores, src, dst, keep_first=0, keep_last=0, stream=None):
+        """Rows dst (int32 [n], resized to the number of tokens that are to stay) receive, in every layer and KV head, the
+        first keep_first and the last keep_last tokens of rows src and those with the highest scores (fp32 [n_layers,
+        max_seqs, n_kv_heads, cap]) between them, in order, with their scores.  Rows src stay as they are."""
+        n = src.numel()
+        self._call("evict", stream, *self._scores(scores, self.cfg.n_layers), self._ints(src, "src"), self._ints(dst, "dst", n), n,
+                   keep_first, keep_last)
 
     def select(self, layer, q, sel, rows=None, keep_first=1, keep_last=1, stream=None):
         """The pages that score highest for each row's one query token (q: [n_rows, n_q_heads, head_dim]) and KV head,
