@@ -321,7 +321,7 @@ dq_status dq_pages_weigh(const dq_pages_config *cfg, const dq_pages_buffers *buf
                          long long q_head_stride, const float *lse, float *scores, int cap, const int *rows, const int *cu,
                          int n_rows, int n_tok, int max_new, float sm_scale, void *stream) {
     dq::PagesWeighArgs a{};
-    dq_status s = view(cfg, bufs, layer, false, a.p);
+    dq_status s = view(cfg, bufs, layer, true, a.p);
     if (s != DQ_OK) return s;
     if ((s = call_rows(cfg, layer, rows, cu, n_rows, n_tok, max_new, a.r)) != DQ_OK) return s;
     if (!q || !lse || !scores) return fail(DQ_EINVAL, "q / lse / scores is NULL");
@@ -337,6 +337,10 @@ dq_status dq_pages_weigh(const dq_pages_config *cfg, const dq_pages_buffers *buf
     a.scores = scores;
     a.cap = cap;
     a.scale_log2 = logit_scale(cfg, sm_scale);
+    uint8_t *ws = static_cast<uint8_t *>(bufs->workspace) + dq::pages_ws_lists(cfg->n_pages);
+    a.tickets = reinterpret_cast<int *>(ws);
+    a.records = reinterpret_cast<float *>(ws + dq::PAGES_MAX_CTAS * 20);
+    a.wait_ns = dq::PAGES_WAIT_NS;
     return launched(dq::launch_pages_weigh(a, device_sms(), stream), "weigh launch");
 }
 

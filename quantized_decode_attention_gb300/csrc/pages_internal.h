@@ -114,6 +114,10 @@ struct PagesWeighArgs {
     float *scores;        // [max_seqs][Hkv][cap] of the layer
     int cap;
     float scale_log2;
+    int over, most;       // this launch takes the rows with over < n G <= most query rows for each KV head
+    int *tickets;         // workspace, as attention has them
+    float *records;       // workspace: [PAGES_MAX_CTAS][2][256]
+    unsigned long long wait_ns;
 };
 struct PagesEvictArgs {
     PagesView p;          // of the pool
@@ -146,7 +150,9 @@ int launch_pages_prompt_shared(const PagesAttnArgs &a, int mode, int grid, void 
 int launch_pages_select(const PagesSelectArgs &a, int num_sms, void *stream);
 int launch_pages_common(const PagesCommonArgs &a, void *stream);
 int launch_pages_shared(const PagesAttnArgs &a, int n_groups, int max_group, int num_sms, void *stream);
-int launch_pages_weigh(const PagesWeighArgs &a, int num_sms, void *stream);
+int launch_pages_weigh(PagesWeighArgs a, int num_sms, void *stream);
+// many query rows: the tensor-core kernel on at most `grid` CTAs
+int launch_pages_weigh_many(const PagesWeighArgs &a, int grid, void *stream);
 int launch_pages_evict(const PagesEvictArgs &a, int num_sms, void *stream);
 
 }  // namespace dq

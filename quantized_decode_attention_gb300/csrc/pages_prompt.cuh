@@ -5,7 +5,7 @@
 // out = (sum p v) / (sum p).  4 D products and one exponential for each (query, key)
 // pair: the kernel is bound by the tensor cores and, nearly as much, by the exponentials
 // and their conversions.  2048 new tokens over 16384 (32 / 8 heads, head_dim 128) take
-// 433 us, 1.19 PFLOP/s; over 131072, 3.3 ms, 1.32.
+// 404 us, 1.28 PFLOP/s.
 //
 // Work.  A unit is 256 query rows (256 / G tokens with their G query heads) of one row and
 // KV head, in two tiles of 128.  It walks the keys that its last token sees, 128 at a
@@ -28,7 +28,7 @@
 
 #include <cuda_runtime.h>
 
-#include "pages.cuh"
+#include "pages_tc.cuh"
 
 namespace dq {
 namespace {
@@ -41,101 +41,6 @@ constexpr int KEYS = 128;                    // keys at a time
 constexpr int UNIT_COST = 512, MIN_SHARE = 1024;  // tokens: of a unit's beginning and end; that make a CTA worth its parts
 constexpr int THREADS = 512;
 
-// ---- tensor memory and tensor cores --------------------------------------------------------
-__device__ __forceinline__ void tmem_ld32(uint32_t addr, uint32_t (&r)[32]) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,"
-        "%25,%26,%27,%28,%29,%30,%31}, [%32];\n"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]),
-          "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]),
-          "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]),
-          "=r"(r[31])
-        : "r"(addr));
-}
-__device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t (&r)[32]) {
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,"
-        "%25,%26,%27,%28,%29,%30,%31,%32};\n" ::"r"(addr),
-        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]),
-        "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]),
-        "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
-        : "memory");
-}
-__device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t (&r)[16]) {
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};\n" ::"r"(addr), "r"(r[0]),
-        "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]),
-        "r"(r[13]), "r"(r[14]), "r"(r[15])
-        : "memory");
-}
-// Wait for the loads so far; nothing that uses r moves before it.
-template <int N>
-__device__ __forceinline__ void tmem_wait_ld(uint32_t (&r)[N]) {
-    asm volatile("tcgen05.wait::ld.sync.aligned;\n" ::: "memory");
-#pragma unroll
-    for (int i = 0; i < N; i++) asm volatile("" : "+r"(r[i]));
-}
-__device__ __forceinline__ void tmem_ld16(uint32_t addr, uint32_t (&r)[16]) {
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]),
-                   "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-                 : "r"(addr));
-}
-__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory"); }
-__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;\n" ::: "memory"); }
-__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;\n" ::: "memory"); }
-// Arrive on `bar` when every product issued so far is done.
-__device__ __forceinline__ void tc_commit(uint64_t *bar) {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n" ::"r"(smem_u32(bar)) : "memory");
-}
-// The warp arrives, once for all its lanes' work before it.
-__device__ __forceinline__ void mbar_arrive(uint64_t *bar) {
-    __syncwarp();
-    if ((threadIdx.x & 31) == 0) asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];\n" ::"r"(smem_u32(bar)) : "memory");
-}
-// Wait for phase `parity` of an mbarrier, for `limit_ns` at most.  The hand-overs here are
-// short and frequent: no hint to sleep long, and the clock is seldom looked at.
-__device__ __forceinline__ bool mbar_spin(uint64_t *bar, unsigned parity, uint64_t limit_ns) {
-    const uint32_t addr = smem_u32(bar);
-    uint64_t t0 = 0;
-    for (unsigned it = 0;; ++it) {
-        uint32_t done;
-        asm volatile("{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
-                     : "=r"(done)
-                     : "r"(addr), "r"(parity)
-                     : "memory");
-        if (done) return true;
-        if ((it & 1023u) == 0) {
-            if (it == 0) t0 = global_ns();
-            else if (global_ns() - t0 > limit_ns) return false;
-        }
-    }
-}
-// Descriptor of a K-major operand with 128-byte swizzle (8 rows of 128 bytes are 1024
-// bytes): its low word holds the address in units of 16 bytes, so that an operand n bytes
-// further on is n / 16 more.
-__device__ __forceinline__ uint32_t operand(uint32_t addr) { return (addr >> 4 & 0x3fffu) | 1u << 16; }
-constexpr uint32_t OPERAND_HIGH = 1024u >> 4 | 1u << 14 | 2u << 29;
-// D += A B (D = A B where `add` is 0); descriptors by their low words.
-__device__ __forceinline__ void mma_smem(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t add) {
-    asm volatile(
-        "{\n .reg .pred p;\n .reg .b64 x, y;\n mov.b64 x, {%1, %5};\n mov.b64 y, {%2, %5};\n setp.ne.u32 p, %4, 0;\n"
-        " tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n}\n" ::"r"(d),
-        "r"(a), "r"(b), "r"(idesc), "r"(add), "r"(OPERAND_HIGH)
-        : "memory");
-}
-__device__ __forceinline__ void mma_tmem(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t add) {
-    asm volatile(
-        "{\n .reg .pred p;\n .reg .b64 y;\n mov.b64 y, {%2, %5};\n setp.ne.u32 p, %4, 0;\n"
-        " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %3, p;\n}\n" ::"r"(d),
-        "r"(a), "r"(b), "r"(idesc), "r"(add), "r"(OPERAND_HIGH)
-        : "memory");
-}
-// Instruction descriptor: binary16 operands, both K-major, fp32 accumulators, M = 128.
-__host__ __device__ constexpr uint32_t product(int n) { return 1u << 4 | static_cast<uint32_t>(n / 8) << 17 | (TILE / 16u) << 24; }
-// Byte offset of 16-byte piece c (8 elements) of row r, in a panel of 64 elements a row.
-__device__ __forceinline__ int swizzled(int r, int c) { return r * 128 + ((c ^ (r & 7)) << 4); }
-
 __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
     uint32_t r;
     asm("mul.rn.f16x2 %0, %1, %2;\n" : "=r"(r) : "r"(a), "r"(b));
@@ -144,28 +49,6 @@ __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
 __device__ __forceinline__ uint32_t half2_of(float a, float b) {
     uint32_t r;
     asm("cvt.rn.f16x2.f32 %0, %1, %2;\n" : "=r"(r) : "f"(b), "f"(a));
-    return r;
-}
-
-// Two fp32 numbers at a time.
-__device__ __forceinline__ uint64_t two(float a, float b) {
-    uint64_t r;
-    asm("mov.b64 %0, {%1, %2};\n" : "=l"(r) : "f"(a), "f"(b));
-    return r;
-}
-__device__ __forceinline__ float2 both(uint64_t x) {
-    float2 r;
-    asm("mov.b64 {%0, %1}, %2;\n" : "=f"(r.x), "=f"(r.y) : "l"(x));
-    return r;
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-    uint64_t r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;\n" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-    return r;
-}
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-    uint64_t r;
-    asm("add.rn.f32x2 %0, %1, %2;\n" : "=l"(r) : "l"(a), "l"(b));
     return r;
 }
 
@@ -514,7 +397,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prompt(const InMode<MODE> a) 
                 // 32 keys at a time, the next 32 on their way; their weights take the place of scores that were read.
                 // A load's registers hold nothing before its wait: load and wait stand in one straight piece of code,
                 // with the weights of the 32 keys before between them and neither a branch nor the loop's end (so the
-                // last 32 keys' load is of columns that nobody uses; unrolled without it 468 us where this takes 430).
+                // last 32 keys' load is of columns that nobody uses; unrolled without it 9 % slower).
                 uint32_t sa[32], sb[32];
                 auto chunk = [&](uint32_t (&s)[32], uint32_t (&coming)[32], int c) {
                     // Weights are positive: one over MOST shows in their sum, so that the maximum is
@@ -713,8 +596,10 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prompt(const InMode<MODE> a) 
                 cur = nxt;
             }
         }
-    } else if (warp == 12 && lane == 0) {
+    } else if (warp == 12) {
         // ---- products -----------------------------------------------------------------------------
+        // The warp goes through them together and one lane issues them: a branch of one lane's own keeps the descriptors out
+        // of the uniform registers that the instruction takes (2048 tokens over 16384: 404 us, so 433).
         unsigned runs = 0, it = 0;
         uint32_t q_at[2], s_at[2], o_at[2];
 #pragma unroll
@@ -725,12 +610,19 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prompt(const InMode<MODE> a) 
         }
         const uint32_t k_at = operand(smem_u32(sh.k[0])), v_at = operand(smem_u32(sh.v[0]));
         constexpr uint32_t STAGE = KEYS * D * 2 / 16;
+        auto commit = [](uint64_t *bar) {
+            if (elect_one()) tc_commit(bar);
+            __syncwarp();
+        };
         auto scores = [&](int t, int st) {
             const uint32_t kb = k_at + st * STAGE;
+            if (elect_one()) {
 #pragma unroll
-            for (int i = 0; i < D / 16; i++)
-                mma_smem(s_at[t], q_at[t] + (i >> 2) * (TILE * 8) + (i & 3) * 2, kb + (i >> 2) * (KEYS * 8) + (i & 3) * 2, product(KEYS), i > 0);
-            tc_commit(&sh.s_full[t]);
+                for (int i = 0; i < D / 16; i++)
+                    mma_smem(s_at[t], q_at[t] + (i >> 2) * (TILE * 8) + (i & 3) * 2, kb + (i >> 2) * (KEYS * 8) + (i & 3) * 2, product(KEYS), i > 0);
+                tc_commit(&sh.s_full[t]);
+            }
+            __syncwarp();
         };
         for (long long x = c0; x < c1;) {
             const Segment g = find_segment<D>(sh, a, tb, x, c1);
@@ -743,7 +635,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prompt(const InMode<MODE> a) 
                 tc_fence_after();
                 scores(t, it & 1);
             }
-            tc_commit(&sh.k_empty[it & 1]);
+            commit(&sh.k_empty[it & 1]);
             runs++;
             for (int k = g.t0; k < g.t1; k++, it++) {
                 const int st = it & 1, next = (it + 1) & 1;
@@ -753,23 +645,26 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prompt(const InMode<MODE> a) 
                     wait(&sh.p_full[t], it & 1);
                     if (t == 0) wait(&sh.v_full[st], it >> 1 & 1);
                     tc_fence_after();
+                    if (elect_one()) {
 #pragma unroll
-                    for (int i = 0; i < KEYS / 16; i++)
-                        mma_tmem(o_at[t], s_at[t] + 8 * i, vb + (i >> 2) * (D * 8) + (i & 3) * 2, product(D), k > g.t0 || i > 0);
-                    if (t == 1) tc_commit(&sh.v_empty[st]);
+                        for (int i = 0; i < KEYS / 16; i++)
+                            mma_tmem(o_at[t], s_at[t] + 8 * i, vb + (i >> 2) * (D * 8) + (i & 3) * 2, product(D), k > g.t0 || i > 0);
+                        if (t == 1) tc_commit(&sh.v_empty[st]);
+                    }
+                    __syncwarp();
                     if (k + 1 < g.t1) {
                         if (t == 0) wait(&sh.k_full[next], (it + 1) >> 1 & 1);
                         if (t == 0) tc_fence_after();
                         scores(t, next);
-                        if (t == 1) tc_commit(&sh.k_empty[next]);
+                        if (t == 1) commit(&sh.k_empty[next]);
                     } else {
-                        tc_commit(&sh.o_full[t]);
+                        commit(&sh.o_full[t]);
                     }
                 }
             }
         }
         // (where no wait ran out, the softmax has waited for the same products)
-        tc_commit(&sh.drained);
+        commit(&sh.drained);
         if (!mbar_spin(&sh.drained, 0, a.wait_ns)) atomicOr(p.status, PST_TIMEOUT);
     }
     __syncwarp();

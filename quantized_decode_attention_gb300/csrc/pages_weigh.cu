@@ -15,13 +15,13 @@
 // first stored.
 #include <cuda_runtime.h>
 
-#include "pages.cuh"
+#include "pages_weigh.cuh"
 
 namespace dq {
 namespace {
 
-constexpr float LOG2E = 1.4426950408889634f;
 constexpr int CHUNK = 32;
+constexpr int MANY_ROWS = 32;  // query rows of a row and KV head beyond which the tensor-core kernel takes over
 
 __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
     uint32_t r;
@@ -31,17 +31,6 @@ __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
 __device__ __forceinline__ uint32_t half2_of(float a, float b) {
     uint32_t r;
     asm("cvt.rn.f16x2.f32 %0, %1, %2;\n" : "=r"(r) : "f"(b), "f"(a));
-    return r;
-}
-
-// Row i of the call as weigh takes it: in order, named once where it brings tokens.
-__device__ __forceinline__ PageRow weigh_row(const PagesWeighArgs &a, int i) {
-    PageRow r = page_row(a.p, a.r, i);
-    if (r.len > a.cap) {
-        atomicOr(a.p.status, PST_ARG);
-        r.len = 0;
-    }
-    if (r.n == 0) r.len = 0;
     return r;
 }
 
@@ -192,68 +181,23 @@ constexpr int WARPS = 8;
 template <int D, int NT>
 __global__ void __launch_bounds__(32 * WARPS) weigh_chunks(PagesWeighArgs a) {
     __shared__ long long first[DQ_PAGES_MAX_ROWS + 1], part[WARPS];
-    __shared__ int row_s[DQ_PAGES_MAX_ROWS], len_s[DQ_PAGES_MAX_ROWS];
+    __shared__ int row_s[DQ_PAGES_MAX_ROWS], keys_s[DQ_PAGES_MAX_ROWS];
     const PagesView &p = a.p;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, n = a.r.n_rows;
-    // chunks before each row
-    long long base = 0;
-    for (int i0 = 0; i0 < n; i0 += 32 * WARPS) {
-        const int i = i0 + tid;
-        long long w = 0;
-        if (i < n) {
-            const PageRow r = weigh_row(a, i);
-            row_s[i] = r.row;
-            len_s[i] = r.len;
-            w = static_cast<long long>((r.len + CHUNK - 1) / CHUNK) * p.Hkv;
-        }
-        long long s = w;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const long long t = __shfl_up_sync(FULL, s, o);
-            if (lane >= o) s += t;
-        }
-        if (lane == 31) part[warp] = s;
-        __syncthreads();
-        long long before = base;
-#pragma unroll
-        for (int k = 0; k < WARPS; k++) {
-            const long long t = part[k];
-            if (k < warp) before += t;
-            base += t;
-        }
-        if (i < n) first[i] = before + s - w;
-        __syncthreads();
-    }
-    if (tid == 0) first[n] = base;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const long long base = weigh_rows<32 * WARPS>(a, row_s, keys_s, first, part, [&](const PageRow &r) {
+        return static_cast<long long>((r.len + CHUNK - 1) / CHUNK) * p.Hkv;
+    });
     __syncthreads();
     const long long all = static_cast<long long>(gridDim.x) * WARPS, me = static_cast<long long>(blockIdx.x) * WARPS + warp;
     const long long x0 = base * me / all, x1 = base * (me + 1) / all;
     for (long long x = x0; x < x1;) {
-        int lo = 0, hi = n - 1;
-        while (lo < hi) {  // the last row that begins at or before x
-            const int mid = (lo + hi + 1) >> 1;
-            if (first[mid] <= x) lo = mid;
-            else hi = mid - 1;
-        }
-        PageRow r;
-        r.row = row_s[lo];
-        r.len = len_s[lo];
-        r.q0 = a.r.cu ? a.r.cu[lo] : lo;
-        r.n = a.r.cu ? a.r.cu[lo + 1] - r.q0 : 1;
-        const int chunks = (r.len + CHUNK - 1) / CHUNK;
-        const int head = static_cast<int>((x - first[lo]) / chunks), t0 = static_cast<int>((x - first[lo]) % chunks);
+        int i;
+        const PageRow r = weigh_row_at(a, row_s, keys_s, first, x, i);
+        const int chunks = (r.len + CHUNK - 1) / CHUNK, at = static_cast<int>(x - first[i]);
+        const int head = at / chunks, t0 = at % chunks;
         const int t1 = x1 - x < chunks - t0 ? t0 + static_cast<int>(x1 - x) : chunks;
         x += t1 - t0;
-        // is the row named a second time with new tokens?  (two warps would add to the same scores)
-        bool twice = false;
-        if (a.r.rows)
-            for (int i = lane; i < n; i += 32) twice |= row_s[i] == r.row && i != lo && len_s[i] > 0;
-        if (__any_sync(FULL, twice)) {
-            if (lane == 0) atomicOr(p.status, PST_ARG);
-            continue;
-        }
-        float *scores = a.scores + (static_cast<long long>(r.row) * p.Hkv + head) * a.cap;
-        const int *table = p.table + static_cast<long long>(r.row) * p.M;
+        float *scores = scores_of(a, r.row, head);
         const int rows = r.n * p.G, old = r.len - r.n, mine = (lane >> 2) + 8 * (lane & 3);
         for (int row0 = 0; row0 < rows; row0 += 8 * NT) {
             Queries<D, NT> q;
@@ -296,7 +240,6 @@ __global__ void __launch_bounds__(32 * WARPS) weigh_chunks(PagesWeighArgs a) {
                 was = next_was;
             }
         }
-        (void)table;
     }
 }
 
@@ -308,9 +251,18 @@ int launch_as(const PagesWeighArgs &a, int num_sms, cudaStream_t st) {
 
 }  // namespace
 
-int launch_pages_weigh(const PagesWeighArgs &a, int num_sms, void *stream) {
+int launch_pages_weigh(PagesWeighArgs a, int num_sms, void *stream) {
     auto st = static_cast<cudaStream_t>(stream);
     const int rows = a.r.max_new * a.p.G;
+    a.over = 0;
+    a.most = 0x7fffffff;
+    if (rows > MANY_ROWS) {  // rows with many query rows on the tensor cores, the others of a mixed batch here
+        a.over = a.r.n_rows == 1 ? 0 : MANY_ROWS;
+        if (const int e = launch_pages_weigh_many(a, num_sms < PAGES_MAX_CTAS ? num_sms : PAGES_MAX_CTAS, stream)) return e;
+        if (a.r.n_rows == 1) return 0;
+        a.over = 0;
+        a.most = MANY_ROWS;
+    }
     if (rows <= 8) return a.p.d == 128 ? launch_as<128, 1>(a, num_sms, st) : launch_as<64, 1>(a, num_sms, st);
     return a.p.d == 128 ? launch_as<128, 2>(a, num_sms, st) : launch_as<64, 2>(a, num_sms, st);
 }
