@@ -347,7 +347,7 @@ dq_status dq_pages_weigh(const dq_pages_config *cfg, const dq_pages_buffers *buf
 dq_status dq_pages_evict(const dq_pages_config *cfg, const dq_pages_buffers *bufs, float *scores, int cap, const int *src,
                          const int *dst, int n, int keep_first, int keep_last, void *stream) {
     dq::PagesEvictArgs a{};
-    dq_status s = view(cfg, bufs, -1, false, a.p);
+    dq_status s = view(cfg, bufs, -1, true, a.p);
     if (s != DQ_OK) return s;
     if (!scores || !src || !dst) return fail(DQ_EINVAL, "scores / src / dst is NULL");
     if (!aligned4(scores) || !aligned4(src) || !aligned4(dst)) return fail(DQ_EALIGN, "scores / src / dst not aligned to 4 bytes");
@@ -362,6 +362,7 @@ dq_status dq_pages_evict(const dq_pages_config *cfg, const dq_pages_buffers *buf
     a.n = n;
     a.keep_first = keep_first;
     a.keep_last = keep_last;
+    a.keeps = reinterpret_cast<int *>(static_cast<uint8_t *>(bufs->workspace) + dq::pages_ws_lists(cfg->n_pages) + dq::PAGES_MAX_CTAS * 20);
     return launched(dq::launch_pages_evict(a, device_sms(), stream), "evict launch");
 }
 

@@ -5,12 +5,15 @@
 // k - keep_first - keep_last with the highest scores (the earlier where scores are equal),
 // with their scores and the pages' summaries.
 //
-// One CTA per (pair, KV head, layer).  The border between kept and evicted scores is found
-// digit by digit (8 bits a pass over the scores, counts in shared memory).  Then the
-// tokens are walked once more: kept ones queue up in shared memory, and whenever the queue
-// holds a block of the destination page its bytes are put together, a 16-byte piece a
-// thread, straight from the source pages: keys and scales as they are, values two tokens a
-// byte.
+// choose_kernel, one CTA per (pair, KV head, layer): the border between kept and evicted
+// scores, found digit by digit (2048 counts a digit; the scores are held in shared memory as
+// far as they fit), then the kept positions in order.
+// They go where the kept tokens' scores are to stand, so that no list needs room.
+// gather_kernel, a CTA a page of dst at a time: positions, page numbers, then 16-byte
+// pieces straight from the source pages to the destination's (keys and scales as they are,
+// values two tokens a byte), the scores over the positions, and the page's summary.  The
+// pages are independent, so that it is bound by memory: what it reads is scattered, two
+// tokens' halves of a 16-byte piece of values often in different sectors.
 #include <cuda_runtime.h>
 
 #include "pages.cuh"
@@ -18,7 +21,9 @@
 namespace dq {
 namespace {
 
-constexpr int EV_THREADS = 256, EV_WARPS = EV_THREADS / 32, EV_PER = 4, EV_TURN = EV_THREADS * EV_PER;
+constexpr int CH_THREADS = 512, CH_WARPS = CH_THREADS / 32;
+constexpr int CH_HELD = 48 << 10;  // keys of scores that shared memory holds, at most
+constexpr int BIN_BITS = 11, BINS = 1 << BIN_BITS;
 
 // Keys that order like the scores, as unsigned: NaN lowest, -0 as 0.
 __device__ __forceinline__ uint32_t order_key(float x) {
@@ -43,314 +48,435 @@ __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
     return r;
 }
 
-struct Border {
-    uint32_t last;  // keys above it are kept
-    int take;       // and the first `take` of those equal to it
+struct ChooseShared {
+    int hist[BINS];
+    int above[CH_WARPS], equal[CH_WARPS];
+    uint32_t digit;
+    int digit_above, digit_count;
 };
 
-// The `take`-th largest key of scores [lo, hi), 1 <= take <= hi - lo.  `hist` holds 256 counts.
-__device__ Border find_border(const float *scores, int lo, int hi, int take, int *hist) {
-    const int tid = threadIdx.x, lane = tid & 31;
-    uint32_t last = 0;
-    for (int shift = 24; shift >= 0; shift -= 8) {
-        for (int i = tid; i < 256; i += EV_THREADS) hist[i] = 0;
-        __syncthreads();
-        for (int j = lo + tid; j < hi; j += EV_THREADS) {
-            const uint32_t k = order_key(scores[j]);
-            if (shift == 24 || (k ^ last) >> (shift + 8) == 0) atomicAdd(&hist[k >> shift & 255u], 1);
+// `held`: keys that the dynamic shared memory has room for behind the struct.
+__global__ void __launch_bounds__(CH_THREADS) choose_kernel(PagesEvictArgs a, int held) {
+    extern __shared__ __align__(16) uint8_t raw[];
+    ChooseShared &sh = *reinterpret_cast<ChooseShared *>(raw);
+    uint32_t *key = reinterpret_cast<uint32_t *>(raw + sizeof(ChooseShared));
+    const PagesView &p = a.p;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int head = blockIdx.y, layer = blockIdx.z, src = a.src[blockIdx.x], dst = a.dst[blockIdx.x];
+    asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
+    for (int i = tid; i < BINS; i += CH_THREADS) sh.hist[i] = 0;
+    // is dst in order: a row of its own, named once?
+    bool bad = src >= p.max_seqs || dst >= p.max_seqs || src == dst;
+    for (int i = tid; i < a.n; i += CH_THREADS) {
+        if (a.src[i] < 0 || a.dst[i] < 0) continue;
+        bad |= a.src[i] == dst || (a.dst[i] == dst && i != static_cast<int>(blockIdx.x));
+    }
+    int len = 0, keep = 0;
+    if (src >= 0 && dst >= 0) {
+        if (!bad) {
+            len = p.seq_len[src];
+            keep = p.seq_len[dst];
+            bad = len < 0 || len > p.M * p.P || keep < 0 || keep > len || len > a.cap || (keep < len && a.keep_first + a.keep_last > keep);
+        }
+        bad = __syncthreads_or(bad);
+        if (bad && tid == 0) atomicOr(p.status, PST_ARG);
+    } else {
+        bad = true;
+    }
+    if (bad) keep = 0;
+    if (tid == 0 && head == 0 && layer == 0) a.keeps[blockIdx.x] = keep;
+    if (keep == 0) return;
+    const long long at = static_cast<long long>(layer) * p.max_seqs;
+    const float *scores = a.scores + ((at + src) * p.Hkv + head) * a.cap;
+    int *out = reinterpret_cast<int *>(a.scores) + ((at + dst) * p.Hkv + head) * a.cap;
+    if (keep == len) {
+        for (int j = tid; j < len; j += CH_THREADS) out[j] = j;
+        return;
+    }
+    // the tokens between the ones that are kept anyway
+    const int lo = a.keep_first, n = len - a.keep_last - lo;
+    const float *mid = scores + lo;
+    auto key_at = [&](int j) { return j < held ? key[j] : order_key(mid[j]); };
+    // The take-th largest key, a digit at a time: it is in [least, least + range], whose keys above it are counted off.
+    uint32_t least = 0, range = 0xffffffffu;
+    int take = keep - a.keep_first - a.keep_last, count = n;
+    for (int shift = 32 - BIN_BITS; take > 0 && take < count;) {
+        if (range == 0xffffffffu) {  // the first digit, as the scores come in
+#pragma unroll 8
+            for (int j = tid; j < n; j += CH_THREADS) {
+                const uint32_t k = order_key(mid[j]);
+                if (j < held) key[j] = k;
+                atomicAdd(&sh.hist[k >> shift], 1);
+            }
+        } else {
+#pragma unroll 4
+            for (int j = tid; j < n; j += CH_THREADS) {
+                const uint32_t k = key_at(j) - least;
+                if (k <= range) atomicAdd(&sh.hist[k >> shift], 1);
+            }
         }
         __syncthreads();
-        // lane l: digits 255 - 8 l down to 248 - 8 l
-        int c[8], sum = 0;
+        // thread t: bins BINS - 1 - 4 t and the three below it
+        constexpr int PER = BINS / CH_THREADS;
+        int c[PER], sum = 0;
 #pragma unroll
-        for (int i = 0; i < 8; i++) sum += c[i] = hist[255 - 8 * lane - i];
+        for (int i = 0; i < PER; i++) sum += c[i] = sh.hist[BINS - 1 - PER * tid - i];
         int before = sum;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const int t = __shfl_up_sync(FULL, before, o);
             if (lane >= o) before += t;
         }
+        if (lane == 31) sh.above[warp] = before;
+        __syncthreads();
         before -= sum;
-        const unsigned here = __ballot_sync(FULL, before < take && before + sum >= take);
-        int digit = 0, at = 0;
 #pragma unroll
-        for (int i = 0; i < 8; i++) {
+        for (int w = 0; w < CH_WARPS; w++) before += w < warp ? sh.above[w] : 0;
+#pragma unroll
+        for (int i = 0; i < PER; i++) {
             if (before < take && before + c[i] >= take) {
-                digit = 255 - 8 * lane - i;
-                at = take - before;
+                sh.digit = BINS - 1 - PER * tid - i;
+                sh.digit_above = before;
+                sh.digit_count = c[i];
             }
             before += c[i];
+            sh.hist[BINS - 1 - PER * tid - i] = 0;
         }
-        const int from = __ffs(here) - 1;
-        last |= static_cast<uint32_t>(__shfl_sync(FULL, digit, from)) << shift;
-        take = __shfl_sync(FULL, at, from);
         __syncthreads();
+        least += sh.digit << shift;
+        take -= sh.digit_above;
+        count = sh.digit_count;
+        range = (1u << shift) - 1u;
+        if (shift == 0) break;
+        shift = shift > BIN_BITS ? shift - BIN_BITS : 0;
     }
-    return Border{last, take};
-}
-
-// Exclusive prefix of v over the CTA; `total` gets the sum.
-__device__ __forceinline__ int block_prefix(int v, int *part, int &total) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    int s = v;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int t = __shfl_up_sync(FULL, s, o);
-        if (lane >= o) s += t;
+    // Kept: keys over least + range, and of those in [least, least + range], of which there are `count`, the first `take` (all of
+    // them, or all are equal).
+    // A warp's tokens are neighbours: [b0, b1).
+    const int b0 = static_cast<int>(static_cast<long long>(len) * warp / CH_WARPS), b1 = static_cast<int>(static_cast<long long>(len) * (warp + 1) / CH_WARPS);
+    const bool none = take == 0 && range == 0xffffffffu;  // of those between
+    auto look = [&](int j, bool &above, bool &equal) {
+        const bool in = j >= lo && j < lo + n, is = j < b1;
+        const uint32_t k = is && in && !none ? key_at(j - lo) : 0u;
+        equal = is && in && !none && k - least <= range;
+        above = is && (!in || (!none && !equal && k > least));
+    };
+    int na = 0, ne = 0;
+#pragma unroll 4
+    for (int j = b0; j < b1; j += 32) {
+        bool above, equal;
+        look(j + lane, above, equal);
+        na += __popc(__ballot_sync(FULL, above));
+        ne += __popc(__ballot_sync(FULL, equal));
     }
     __syncthreads();
-    if (lane == 31) part[warp] = s;
-    __syncthreads();
-    int before = 0;
-    total = 0;
-#pragma unroll
-    for (int w = 0; w < EV_WARPS; w++) {
-        const int t = part[w];
-        if (w < warp) before += t;
-        total += t;
+    if (lane == 0) {
+        sh.above[warp] = na;
+        sh.equal[warp] = ne;
     }
-    return before + s - v;
+    __syncthreads();
+    na = ne = 0;
+    for (int w = 0; w < warp; w++) {
+        na += sh.above[w];
+        ne += sh.equal[w];
+    }
+    const unsigned below = (1u << lane) - 1u;
+#pragma unroll 4
+    for (int j = b0; j < b1; j += 32) {
+        bool above, equal;
+        look(j + lane, above, equal);
+        const unsigned ma = __ballot_sync(FULL, above), me = __ballot_sync(FULL, equal);
+        const int before_a = na + __popc(ma & below), before_e = ne + __popc(me & below);
+        const int to = before_a + (before_e < take ? before_e : take);
+        if ((above || (equal && before_e < take)) && to < keep) out[to] = j + lane;  // (to < keep unless scores change under the call)
+        na += __popc(ma);
+        ne += __popc(me);
+    }
 }
 
-template <int D>
-__global__ void __launch_bounds__(EV_THREADS) evict_kernel(PagesEvictArgs a) {
+constexpr int GA_THREADS = 128, GA_WARPS = GA_THREADS / 32;
+
+// One CTA row of the grid per (KV head, layer), which walks the pages of all pairs, a block of B = min(P, 64) tokens
+// at a time.  Two blocks ahead the positions are on their way, one ahead the page numbers and scores.
+template <int D, int B>
+__global__ void __launch_bounds__(GA_THREADS, 6) gather_kernel(PagesEvictArgs a) {
     using L = PageBlock<D>;
-    constexpr int C = D / 16, QUEUE = 64 + EV_TURN;
-    __shared__ __align__(16) uint8_t img[64 * D * 9 / 16];  // a block's key codes, then their scales
-    __shared__ float top_s[EV_WARPS][D], low_s[EV_WARPS][D], red[EV_WARPS];
-    __shared__ int hist[256], part[EV_WARPS];
-    __shared__ int page_q[QUEUE];     // kept tokens that wait: their pages,
-    __shared__ uint8_t token_q[QUEUE];  // and their places in them
-    PagesView p = a.p;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int src = a.src[blockIdx.x], dst = a.dst[blockIdx.x], head = blockIdx.y, layer = blockIdx.z;
-    if (src < 0 || dst < 0) return;
-    // is dst in order: a row of its own, named once?
-    bool bad = src >= p.max_seqs || dst >= p.max_seqs || src == dst;
-    for (int i = tid; i < a.n; i += EV_THREADS) {
-        if (a.src[i] < 0 || a.dst[i] < 0) continue;
-        bad |= a.src[i] == dst || (a.dst[i] == dst && i != static_cast<int>(blockIdx.x));
+    constexpr int C = D / 16;
+    extern __shared__ __align__(16) uint8_t dyn[];         // [n] src, dst, keep, pages before the pair
+    __shared__ __align__(16) uint8_t img[B * D * 9 / 16];  // a block's key codes, then their scales
+    __shared__ float red[GA_WARPS];
+    __shared__ long long from_s[B];                        // where a token's block is in the pool: -1 none
+    __shared__ int place_s[B], part[GA_WARPS];             // its place there
+    const PagesView &p = a.p;
+    int4 *pair = reinterpret_cast<int4 *>(dyn);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, head = blockIdx.y, layer = blockIdx.z;
+    asm volatile("griddepcontrol.wait;\n" ::: "memory");
+    int pages = 0;
+    for (int i0 = 0; i0 < a.n; i0 += GA_THREADS) {
+        const int i = i0 + tid, keep = i < a.n ? a.keeps[i] : 0, w = (keep + p.P - 1) / p.P;
+        int s = w;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int t = __shfl_up_sync(FULL, s, o);
+            if (lane >= o) s += t;
+        }
+        if (lane == 31) part[warp] = s;
+        __syncthreads();
+        int before = pages;
+#pragma unroll
+        for (int k = 0; k < GA_WARPS; k++) {
+            if (k < warp) before += part[k];
+            pages += part[k];
+        }
+        if (i < a.n) pair[i] = make_int4(a.src[i], a.dst[i], keep, before + s - w);
+        __syncthreads();
     }
-    int len = 0, keep = 0;
-    if (!bad) {
-        len = p.seq_len[src];
-        keep = p.seq_len[dst];
-        bad = len < 0 || len > p.M * p.P || keep < 0 || keep > len || len > a.cap || (keep < len && a.keep_first + a.keep_last > keep);
-    }
-    if (__syncthreads_or(bad)) {
-        if (tid == 0) atomicOr(p.status, PST_ARG);
-        return;
-    }
-    if (keep == 0) return;
-    const long long at_layer = static_cast<long long>(layer) * p.n_pages * p.Hkv;
-    p.pages += at_layer * p.page_bytes;
-    p.summary += at_layer * p.sum_bytes;
-    const float *scores = a.scores + ((static_cast<long long>(layer) * p.max_seqs + src) * p.Hkv + head) * a.cap;
-    float *to_scores = a.scores + ((static_cast<long long>(layer) * p.max_seqs + dst) * p.Hkv + head) * a.cap;
-    // the tokens between the ones kept anyway
-    const int lo = keep < len ? a.keep_first : len, hi = keep < len ? len - a.keep_last : len;
-    const int want = keep < len ? keep - a.keep_first - a.keep_last : 0;
-    Border border{0xffffffffu, 0};
-    if (want > 0) border = find_border(scores, lo, hi, want, hist);
+    const long long at_layer = static_cast<long long>(layer) * p.max_seqs, pool = static_cast<long long>(layer) * p.n_pages;
+    auto scores_of = [&](int row) { return a.scores + ((at_layer + row) * p.Hkv + head) * a.cap; };
+    const int shift = 31 - __clz(p.P);  // (a power of two)
+    struct Step {
+        int x, src, dst, keep, ord, b0;  // page of all pairs' pages; its pair; its ordinal; the block's first token in it
+    };
+    auto seek = [&](Step &s) {
+        if (s.x >= pages) return;
+        int lo = 0, hi = a.n - 1;
+        while (lo < hi) {  // the last pair that begins at or before x
+            const int mid = (lo + hi + 1) >> 1;
+            if (pair[mid].w <= s.x) lo = mid;
+            else hi = mid - 1;
+        }
+        const int4 q = pair[lo];
+        s.src = q.x;
+        s.dst = q.y;
+        s.keep = q.z;
+        s.ord = s.x - q.w;
+        s.b0 = 0;
+    };
+    auto tokens = [&](const Step &s) {  // from the block's first token to the page's end
+        const int left = s.keep - (s.ord << shift);
+        return (left < p.P ? left : p.P) - s.b0;
+    };
+    auto step = [&](Step &s) {
+        if (tokens(s) > B) {
+            s.b0 += B;
+        } else {
+            s.x += gridDim.x;
+            seek(s);
+        }
+    };
+    auto position = [&](const Step &s) {  // of this thread's token
+        return s.x < pages && tid < B && tid < tokens(s) ? __float_as_int(scores_of(s.dst)[(s.ord << shift) + s.b0 + tid]) : -1;
+    };
+    struct Found {
+        int id, refs, page, place;
+        float score;
+    };
+    auto look = [&](const Step &s, int j, int page, Found &f) {
+        f.id = -1;
+        f.refs = 0;
+        f.page = page;
+        f.place = 0;
+        if (s.x >= pages) return;
+        if (j >= 0 && j < p.M * p.P && j < a.cap) {  // (it is what choose_kernel wrote)
+            f.id = p.table[static_cast<long long>(s.src) * p.M + (j >> shift)];
+            f.place = j & (p.P - 1);
+            f.score = scores_of(s.src)[j];
+            if (f.id < 0 || f.id >= p.n_pages) f.id = -2;
+        }
+        if (page >= 0 && page < p.n_pages) f.refs = p.refs[page];
+    };
+    auto number = [&](const Step &s) { return s.x < pages ? p.table[static_cast<long long>(s.dst) * p.M + s.ord] : -1; };
 
-    int queued = 0, written = 0, equals = 0, page = -1;
+    constexpr int PAIRS = B / 2 * C, KEYS = B * (D / 32), SCALES = B * (D / 64);  // pieces of values and keys, words of scales
+    constexpr int NV = (PAIRS + GA_THREADS - 1) / GA_THREADS, NK = (KEYS + GA_THREADS - 1) / GA_THREADS;
+    static_assert(SCALES <= GA_THREADS, "a thread a word");
+    // summary: a warp's COLS columns of 8 channels, each over every 32 / COLS-th token
+    constexpr int COLS = D / 8 / GA_WARPS;
+    const int col = warp * COLS + lane % COLS;
     uint32_t top[4], low[4];
-    const int col = tid % (D / 8);
-    const int B = p.blk;
-    for (int j0 = 0; j0 < len; j0 += EV_TURN) {
-        {  // up to EV_TURN more tokens, EV_PER neighbours a thread
-            bool above[EV_PER], equal[EV_PER];
-            float score[EV_PER];
-            int n_above = 0, n_equal = 0;
+    Step now, next;
+    now.x = blockIdx.x;
+    seek(now);
+    Found f;
+    look(now, position(now), number(now), f);
+    next = now;
+    if (now.x < pages) step(next);
+    int j = position(next), page_next = number(next);
+    while (now.x < pages) {
+        const int left = tokens(now), n = left < B ? left : B;
+        int page = f.page;
+        if (page < 0 || page >= p.n_pages || f.refs != 1) {
+            if (tid == 0) atomicOr(p.status, page < 0 || page >= p.n_pages ? PST_TABLE : PST_SHARED);
+            page = -1;
+        }
+        if (now.b0 == 0) {
 #pragma unroll
-            for (int i = 0; i < EV_PER; i++) {
-                const int j = j0 + tid * EV_PER + i;
-                above[i] = equal[i] = false;
-                score[i] = j < len ? scores[j] : 0.f;
-                if (j >= len) continue;
-                if (j < lo || j >= hi) above[i] = true;
-                else {
-                    const uint32_t k = order_key(score[i]);
-                    above[i] = k > border.last;
-                    equal[i] = k == border.last;
-                }
-                n_above += above[i];
-                n_equal += equal[i];
+            for (int i = 0; i < 4; i++) {
+                top[i] = 0xfc00fc00u;
+                low[i] = 0x7c007c00u;
             }
-            int some;
-            const int before = block_prefix(n_above | n_equal << 16, part, some);
-            int na = before & 0xffff, ne = equals + (before >> 16);
-            // equals that are kept come first: those so far are min(ne, take)
-            const int base = queued - (equals < border.take ? equals : border.take);
-#pragma unroll
-            for (int i = 0; i < EV_PER; i++) {
-                const int j = j0 + tid * EV_PER + i;
-                if (above[i] || (equal[i] && ne < border.take)) {
-                    const int at = base + na + (ne < border.take ? ne : border.take);
-                    if (written + at >= keep) break;  // (scores that change under the call)
-                    page_q[at] = page_of(p, src, j / p.P);
-                    token_q[at] = static_cast<uint8_t>(j % p.P);
-                    to_scores[written + at] = score[i];
-                }
-                na += above[i];
-                ne += equal[i];
-            }
-            const int all_equal = equals + (some >> 16);
-            queued = base + (some & 0xffff) + (all_equal < border.take ? all_equal : border.take);
-            queued = queued < keep - written ? queued : keep - written;
-            equals = all_equal;
+        }
+        uint8_t *blk = page < 0 ? nullptr : p.pages + ((pool + page) * p.Hkv + head) * p.page_bytes + now.b0 / B * L::size(B);
+        if (tid < B) {
+            if (f.id == -2) atomicOr(p.status, PST_TABLE);
+            from_s[tid] = f.id < 0 ? -1 : ((pool + f.id) * p.Hkv + head) * p.page_bytes + f.place / B * L::size(B);
+            place_s[tid] = f.place % B;
+            if (f.id != -1) scores_of(now.dst)[(now.ord << shift) + now.b0 + tid] = f.score;
         }
         __syncthreads();
-        // whole blocks of the destination, and what is left at the end
-        int done = 0;
-        while (queued - done >= B || (j0 + EV_TURN >= len && queued > done)) {
-            const int n = queued - done < B ? queued - done : B;
-            const int at = written % p.P;  // the block's first token in its page
-            if (at == 0) {
-                page = page_of(p, dst, written / p.P);
-                if (page >= 0 && p.refs[page] != 1) {
-                    if (tid == 0) atomicOr(p.status, PST_SHARED);
-                    page = -1;
-                }
+        // everything that the block needs is loaded before anything is stored
+        uint4 v[NV], w[NV], k[NK];
+        uint32_t s0[NV], s1[NV], ks = 0;
 #pragma unroll
-                for (int i = 0; i < 4; i++) {
-                    top[i] = 0xfc00fc00u;
-                    low[i] = 0x7c007c00u;
-                }
+        for (int e = 0; e < NV; e++) {  // values: (8 tokens, scale block, pair) in the order of the bytes
+            const int i = tid + e * GA_THREADS, in = i % (4 * C), c = in >> 2, pr = 4 * (i / (4 * C)) + (in & 3);
+            v[e] = w[e] = make_uint4(0, 0, 0, 0);
+            s0[e] = s1[e] = 0;
+            if (i >= PAIRS) continue;
+            const long long f0 = from_s[2 * pr], f1 = from_s[2 * pr + 1];
+            if (f0 >= 0) {
+                const int t0 = place_s[2 * pr];
+                v[e] = *reinterpret_cast<const uint4 *>(p.pages + f0 + L::vc(B) + L::vcode(t0, c));
+                s0[e] = p.pages[f0 + L::vs(B) + L::vscale(t0, c)];
             }
-            uint8_t *blk = page < 0 ? nullptr : page_ptr(p, page, head) + at / B * L::size(B);
-            auto from = [&](int u, const uint8_t *&b) -> int {  // block and place of the u-th waiting token
-                const int id = page_q[done + u], t = token_q[done + u];
-                b = id < 0 ? nullptr : page_ptr(p, id, head) + t / B * L::size(B);
-                return t % B;
-            };
-            for (int i = tid; i < n * (D / 32); i += EV_THREADS) {
-                const uint8_t *b;
-                const int u = i / (D / 32), c = i % (D / 32), t = from(u, b);
-                const uint4 w = b ? *reinterpret_cast<const uint4 *>(b + t * (D / 2) + 16 * c) : make_uint4(0, 0, 0, 0);
-                reinterpret_cast<uint4 *>(img)[i] = w;
-                if (blk) reinterpret_cast<uint4 *>(blk)[i] = w;
+            if (f1 >= 0) {
+                const int t1 = place_s[2 * pr + 1];
+                w[e] = *reinterpret_cast<const uint4 *>(p.pages + f1 + L::vc(B) + L::vcode(t1, c));
+                s1[e] = p.pages[f1 + L::vs(B) + L::vscale(t1, c)];
             }
-            for (int i = tid; i < n * (D / 64); i += EV_THREADS) {  // four scales
-                const uint8_t *b;
-                const int u = i / (D / 64), c = i % (D / 64), t = from(u, b);
-                const uint32_t w = b ? *reinterpret_cast<const uint32_t *>(b + L::ks(B) + t * C + 4 * c) : 0u;
-                reinterpret_cast<uint32_t *>(img + 64 * D / 2)[i] = w;
-                if (blk) reinterpret_cast<uint32_t *>(blk + L::ks(B))[i] = w;
-            }
-            // values: (8 tokens, scale block, pair) in the order of the bytes
-            for (int i = tid; i < (n + 1) / 2 * C; i += EV_THREADS) {
-                // the last group of 8 may be short of pairs
-                const int pairs = (n + 1) / 2, g = i / (4 * C), left = pairs - 4 * g < 4 ? pairs - 4 * g : 4;
-                const int in = i - g * 4 * C, c = in / left, pr = 4 * g + in % left;
-                const uint8_t *b0, *b1 = nullptr;
-                const bool two = 2 * pr + 1 < n;
-                const int t0 = from(2 * pr, b0), t1 = two ? from(2 * pr + 1, b1) : 0;
-                const uint4 x = b0 ? *reinterpret_cast<const uint4 *>(b0 + L::vc(B) + L::vcode(t0, c)) : make_uint4(0, 0, 0, 0);
-                const uint32_t s0 = b0 ? b0[L::vs(B) + L::vscale(t0, c)] : 0u;
-                if (!blk) continue;
-                uint4 *to = reinterpret_cast<uint4 *>(blk + L::vc(B) + L::vcode(2 * pr, c));
-                uint8_t *to_s = blk + L::vs(B) + L::vscale(2 * pr, c);
-                uint4 y;
-                uint32_t s1;
-                int odd;
-                if (two) {
-                    y = b1 ? *reinterpret_cast<const uint4 *>(b1 + L::vc(B) + L::vcode(t1, c)) : make_uint4(0, 0, 0, 0);
-                    s1 = b1 ? b1[L::vs(B) + L::vscale(t1, c)] : 0u;
-                    odd = t1 & 1;
-                } else {  // the place behind the last token stays as it is
-                    y = *to;
-                    s1 = to_s[1];
-                    odd = 1;
-                }
-                const int sx = 4 * (t0 & 1), sy = 4 * odd;
-                auto both = [&](uint32_t u, uint32_t v) { return (u >> sx & 0x0f0f0f0fu) | (v >> sy & 0x0f0f0f0fu) << 4; };
-                *to = make_uint4(both(x.x, y.x), both(x.y, y.y), both(x.z, y.z), both(x.w, y.w));
-                *reinterpret_cast<uint16_t *>(to_s) = static_cast<uint16_t>(s0 | s1 << 8);
-            }
-            __syncthreads();
-            for (int t = tid / (D / 8); t < n; t += EV_THREADS / (D / 8)) {
-                uint32_t h[4];
-                e2m1x8_to_half(*reinterpret_cast<const uint32_t *>(img + t * (D / 2) + 4 * col), h);
-                const uint32_t s = e4m3x2_to_half2(img[64 * D / 2 + t * C + (col >> 1)]), s2 = __byte_perm(s, s, 0x1010);
-#pragma unroll
-                for (int i = 0; i < 4; i++) {
-                    h[i] = hmul2(h[i], s2);  // exact
-                    top[i] = hmax2(top[i], h[i]);
-                    low[i] = hmin2(low[i], h[i]);
-                }
-            }
-            written += n;
-            done += n;
-            if (written % p.P == 0 || written == keep) {  // the page is done: its summary
-#pragma unroll
-                for (int i = 0; i < 4; i++) {
-#pragma unroll
-                    for (int o = D / 8; o < 32; o <<= 1) {
-                        top[i] = hmax2(top[i], __shfl_xor_sync(FULL, top[i], o));
-                        low[i] = hmin2(low[i], __shfl_xor_sync(FULL, low[i], o));
-                    }
-                    if (lane < D / 8) {
-                        const float2 h = __half22float2(*reinterpret_cast<const __half2 *>(&top[i])), l = __half22float2(*reinterpret_cast<const __half2 *>(&low[i]));
-                        top_s[warp][8 * lane + 2 * i] = h.x;
-                        top_s[warp][8 * lane + 2 * i + 1] = h.y;
-                        low_s[warp][8 * lane + 2 * i] = l.x;
-                        low_s[warp][8 * lane + 2 * i + 1] = l.y;
-                    }
-                }
-                __syncthreads();
-                float mx = -INFINITY, mn = INFINITY;
-                if (tid < D)
-#pragma unroll
-                    for (int i = 0; i < EV_WARPS; i++) {
-                        mx = fmaxf(mx, top_s[i][tid]);
-                        mn = fminf(mn, low_s[i][tid]);
-                    }
-                const float w = warp_max(tid < D ? fmaxf(fabsf(mx), fabsf(mn)) : 0.f);
-                if (lane == 0) red[warp] = w;
-                __syncthreads();
-                float most = red[0];
-#pragma unroll
-                for (int i = 1; i < EV_WARPS; i++) most = fmaxf(most, red[i]);
-                // (held keys are multiples of 2^-10 below 2^12: as append has it)
-                const int e = most > 0.f ? static_cast<int>(__float_as_uint(most) >> 23) - 126 - 7 : 0;
-                if (page >= 0) {
-                    uint8_t *sum = summary_ptr(p, page, head);
-                    if (tid < D) {
-                        const float unit = pow2i(-e);
-                        reinterpret_cast<int8_t *>(sum)[tid] = static_cast<int8_t>(ceilf(mx * unit));
-                        reinterpret_cast<int8_t *>(sum)[D + tid] = static_cast<int8_t>(floorf(mn * unit));
-                    }
-                    if (tid == 0) *reinterpret_cast<int *>(sum + 2 * D) = e;
-                }
-            }
-            __syncthreads();
         }
-        // what waits moves to the front
-        const int left = queued - done;
-        int id = 0, t = 0;
-        if (tid < left) {
-            id = page_q[done + tid];
-            t = token_q[done + tid];
+#pragma unroll
+        for (int e = 0; e < NK; e++) {
+            const int i = tid + e * GA_THREADS, u = i / (D / 32);
+            k[e] = make_uint4(0, 0, 0, 0);
+            if (i < KEYS && from_s[u] >= 0) k[e] = *reinterpret_cast<const uint4 *>(p.pages + from_s[u] + place_s[u] * (D / 2) + 16 * (i % (D / 32)));
+        }
+        if (tid < SCALES) {  // four scales
+            const int u = tid / (D / 64);
+            if (from_s[u] >= 0) ks = *reinterpret_cast<const uint32_t *>(p.pages + from_s[u] + L::ks(B) + place_s[u] * C + 4 * (tid % (D / 64)));
+        }
+        const bool last = left <= B;
+        look(next, j, page_next, f);
+        now = next;
+        if (next.x < pages) step(next);
+        j = position(next);
+        page_next = number(next);
+#pragma unroll
+        for (int e = 0; e < NV; e++) {
+            const int i = tid + e * GA_THREADS, in = i % (4 * C), c = in >> 2, pr = 4 * (i / (4 * C)) + (in & 3);
+            if (i >= PAIRS || 2 * pr >= n || !blk) continue;
+            uint4 *to = reinterpret_cast<uint4 *>(blk + L::vc(B) + L::vcode(2 * pr, c));
+            uint8_t *to_s = blk + L::vs(B) + L::vscale(2 * pr, c);
+            int odd = place_s[2 * pr + 1] & 1;
+            if (2 * pr + 1 >= n) {  // the place behind the last token stays as it is
+                w[e] = *to;
+                s1[e] = to_s[1];
+                odd = 1;
+            }
+            const int sv = 4 * (place_s[2 * pr] & 1), sw = 4 * odd;
+            auto both = [&](uint32_t x, uint32_t y) { return (x >> sv & 0x0f0f0f0fu) | (y >> sw & 0x0f0f0f0fu) << 4; };
+            *to = make_uint4(both(v[e].x, w[e].x), both(v[e].y, w[e].y), both(v[e].z, w[e].z), both(v[e].w, w[e].w));
+            *reinterpret_cast<uint16_t *>(to_s) = static_cast<uint16_t>(s0[e] | s1[e] << 8);
+        }
+#pragma unroll
+        for (int e = 0; e < NK; e++) {
+            const int i = tid + e * GA_THREADS;
+            if (i >= n * (D / 32)) continue;
+            reinterpret_cast<uint4 *>(img)[i] = k[e];
+            if (blk) reinterpret_cast<uint4 *>(blk)[i] = k[e];
+        }
+        if (tid < n * (D / 64)) {
+            reinterpret_cast<uint32_t *>(img + B * D / 2)[tid] = ks;
+            if (blk) reinterpret_cast<uint32_t *>(blk + L::ks(B))[tid] = ks;
         }
         __syncthreads();
-        if (done > 0 && tid < left) {
-            page_q[tid] = id;
-            token_q[tid] = static_cast<uint8_t>(t);
+#pragma unroll 2
+        for (int t = lane / COLS; t < n; t += 32 / COLS) {
+            uint32_t h[4];
+            e2m1x8_to_half(*reinterpret_cast<const uint32_t *>(img + t * (D / 2) + 4 * col), h);
+            const uint32_t sc = e4m3x2_to_half2(img[B * D / 2 + t * C + (col >> 1)]), sc2 = __byte_perm(sc, sc, 0x1010);
+#pragma unroll
+            for (int i = 0; i < 4; i++) {
+                h[i] = hmul2(h[i], sc2);  // exact
+                top[i] = hmax2(top[i], h[i]);
+                low[i] = hmin2(low[i], h[i]);
+            }
         }
-        queued = left;
+        if (!last) {
+            __syncthreads();  // (the next block's keys take the place of these)
+            continue;
+        }
+        // the page's summary, as append has it
+        float mx[8], mn[8], most = 0.f;
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+#pragma unroll
+            for (int o = COLS; o < 32; o <<= 1) {
+                top[i] = hmax2(top[i], __shfl_xor_sync(FULL, top[i], o));
+                low[i] = hmin2(low[i], __shfl_xor_sync(FULL, low[i], o));
+            }
+            const float2 h = __half22float2(*reinterpret_cast<const __half2 *>(&top[i])), l = __half22float2(*reinterpret_cast<const __half2 *>(&low[i]));
+            mx[2 * i] = h.x;
+            mx[2 * i + 1] = h.y;
+            mn[2 * i] = l.x;
+            mn[2 * i + 1] = l.y;
+            most = fmaxf(most, fmaxf(fmaxf(fabsf(h.x), fabsf(h.y)), fmaxf(fabsf(l.x), fabsf(l.y))));
+        }
+        most = warp_max(most);
+        if (lane == 0) red[warp] = most;
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < GA_WARPS; i++) most = fmaxf(most, red[i]);
+        // (held keys are multiples of 2^-10 below 2^12)
+        const int e = most > 0.f ? static_cast<int>(__float_as_uint(most) >> 23) - 126 - 7 : 0;
+        if (page >= 0) {
+            uint8_t *sum = p.summary + ((pool + page) * p.Hkv + head) * p.sum_bytes;
+            if (lane < COLS) {
+                const float unit = pow2i(-e);
+                uint32_t b[4] = {0, 0, 0, 0};
+#pragma unroll
+                for (int i = 0; i < 8; i++) {
+                    b[i >> 2] |= (static_cast<uint32_t>(static_cast<int>(ceilf(mx[i] * unit))) & 0xffu) << (8 * (i & 3));
+                    b[2 + (i >> 2)] |= (static_cast<uint32_t>(static_cast<int>(floorf(mn[i] * unit))) & 0xffu) << (8 * (i & 3));
+                }
+                *reinterpret_cast<uint2 *>(sum + 8 * col) = make_uint2(b[0], b[1]);
+                *reinterpret_cast<uint2 *>(sum + D + 8 * col) = make_uint2(b[2], b[3]);
+            }
+            if (tid == 0) *reinterpret_cast<int *>(sum + 2 * D) = e;
+        }
     }
+}
+
+template <int D, int B>
+int launch_gather(const PagesEvictArgs &a, int num_sms, cudaStream_t st) {
+    cudaLaunchConfig_t cfg{};
+    const long long units = static_cast<long long>(a.p.Hkv) * a.p.n_layers, room = 6LL * num_sms;
+    cfg.gridDim = dim3(static_cast<unsigned>(units < room ? room / units : 1), a.p.Hkv, a.p.n_layers);
+    cfg.blockDim = dim3(GA_THREADS);
+    cfg.dynamicSmemBytes = a.n * 16;
+    cfg.stream = st;
+    cudaLaunchAttribute at{};
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    return static_cast<int>(cudaLaunchKernelEx(&cfg, gather_kernel<D, B>, a));
+}
+template <int D>
+int launch_gather_of(const PagesEvictArgs &a, int num_sms, cudaStream_t st) {
+    return a.p.blk == 64 ? launch_gather<D, 64>(a, num_sms, st) : (a.p.blk == 32 ? launch_gather<D, 32>(a, num_sms, st) : launch_gather<D, 16>(a, num_sms, st));
 }
 
 }  // namespace
 
 int launch_pages_evict(const PagesEvictArgs &a, int num_sms, void *stream) {
-    (void)num_sms;
-    const dim3 grid(a.n, a.p.Hkv, a.p.n_layers);
     auto st = static_cast<cudaStream_t>(stream);
-    if (a.p.d == 128) evict_kernel<128><<<grid, EV_THREADS, 0, st>>>(a);
-    else evict_kernel<64><<<grid, EV_THREADS, 0, st>>>(a);
-    return static_cast<int>(cudaGetLastError());
+    const int held = a.cap < CH_HELD ? a.cap : CH_HELD, smem = static_cast<int>(sizeof(ChooseShared));
+    if (const int e = allow_shared<choose_kernel>(smem + CH_HELD * 4)) return e;
+    choose_kernel<<<dim3(a.n, a.p.Hkv, a.p.n_layers), CH_THREADS, smem + held * 4, st>>>(a, held);
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return static_cast<int>(e);
+    return a.p.d == 128 ? launch_gather_of<128>(a, num_sms, st) : launch_gather_of<64>(a, num_sms, st);
 }
 
 }  // namespace dq

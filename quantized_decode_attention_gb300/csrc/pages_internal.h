@@ -125,6 +125,7 @@ struct PagesEvictArgs {
     int cap;
     const int *src, *dst;
     int n, keep_first, keep_last;
+    int *keeps;           // workspace: [n], the tokens that each pair keeps, 0 for one that is refused
 };
 struct PagesSelectArgs {
     PagesView p;
