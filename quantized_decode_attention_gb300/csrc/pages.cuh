@@ -38,6 +38,26 @@ int allow_shared(int bytes) {
     return static_cast<int>(e);
 }
 
+// A kernel launched by launch_overlapping may start while the one before it in the stream still runs, once all of that
+// one's CTAs have called let_next_start or ended; it waits for its end with await_previous.  Every CTA of it does, so that its
+// own end is behind that one's too.
+__device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory"); }
+__device__ __forceinline__ void await_previous() { asm volatile("griddepcontrol.wait;\n" ::: "memory"); }
+template <class K, class A>
+int launch_overlapping(K kernel, dim3 grid, int threads, int smem, cudaStream_t st, const A &args) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute at{};
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    return static_cast<int>(cudaLaunchKernelEx(&cfg, kernel, args));
+}
+
 // ---- rows ----------------------------------------------------------------------------
 struct PageRow {
     int row;    // table row, -1: padding (nothing held)

@@ -314,6 +314,9 @@ dq_status dq_pages_shared(const dq_pages_config *cfg, const dq_pages_buffers *bu
     a.plan = plan;
     a.call_rows = n_rows;
     a.part = static_cast<float *>(scratch);
+    uint8_t *ws = static_cast<uint8_t *>(bufs->workspace) + dq::pages_ws_own(cfg->n_pages);
+    a.own_tickets = reinterpret_cast<int *>(ws);
+    a.own_records = reinterpret_cast<float *>(ws + dq::PAGES_MAX_CTAS * 4);
     return launched(dq::launch_pages_shared(a, n_groups, max_group, device_sms(), stream), "shared attention launch");
 }
 

@@ -289,9 +289,9 @@ struct State {
         }
     }
 
-    // The state that an earlier launch left for the unit's rows: their maxima, sums and accumulators as they were.
+    // What an earlier launch left for the unit's rows, their maxima, sums and accumulators as they were, beside this state.
     template <class A>
-    __device__ __forceinline__ void resume(const A &a, const PageRow &r, int head, int row0) {
+    __device__ __forceinline__ void take_in(const A &a, const PageRow &r, int head, int row0) {
         const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
 #pragma unroll
         for (int n = 0; n < NT; n++)
@@ -301,13 +301,15 @@ struct State {
                 if (row >= r.n * a.p.G) continue;
                 const long long o = query_of(a, r, head, row);
                 const float2 ml = reinterpret_cast<const float2 *>(part_sums<D>(a))[o];
-                m[n][e] = ml.x;
-                l[n][e] = g == 0 ? ml.y : 0.f;
+                const float mx = fmaxf(m[n][e], ml.x), by = mx == -INFINITY ? 0.f : mx;
+                const float keep = ex2(m[n][e] - by), take = ex2(ml.x - by);  // 0 for a part that saw nothing
+                m[n][e] = mx;
+                l[n][e] = l[n][e] * keep + (g == 0 ? ml.y * take : 0.f);
 #pragma unroll
                 for (int i = 0; i < D / 16; i++) {
                     const float2 x = *reinterpret_cast<const float2 *>(a.part + o * D + g * (D / 8) + 2 * i);
-                    acc[n][i][e] = x.x;
-                    acc[n][i][e + 2] = x.y;
+                    acc[n][i][e] = acc[n][i][e] * keep + x.x * take;
+                    acc[n][i][e + 2] = acc[n][i][e + 2] * keep + x.y * take;
                 }
             }
     }
@@ -494,6 +496,9 @@ __global__ void __launch_bounds__(32 * NW, 1) attn_chunks(const InMode<MODE> a) 
     const PagesView &p = a.p;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     constexpr int ST = S::ST;
+    if (a.mode == PAGES_COMMON) let_next_start();
+    int *tickets = a.mode == PAGES_OWN ? a.own_tickets : a.tickets;
+    float *records = a.mode == PAGES_OWN ? a.own_records : a.records;
     if (lane < ST) mbar_init(&sh.full[warp][lane], 1 + a.owed);
     fence_mbar_init();
     // places before each row: a prefix over the rows, 32 NW at a time
@@ -528,6 +533,7 @@ __global__ void __launch_bounds__(32 * NW, 1) attn_chunks(const InMode<MODE> a) 
     }
     if (base > 0x7fffffff) {  // more places than int counts
         if (tid == 0) atomicOr(p.status, PST_ARG);
+        if (a.mode == PAGES_OWN) await_previous();
         return;
     }
     const int N = static_cast<int>(base);
@@ -547,7 +553,10 @@ __global__ void __launch_bounds__(32 * NW, 1) attn_chunks(const InMode<MODE> a) 
     // this CTA's places [c0, c1), this warp's [w0, w1)
     int ctas = N / MIN_PLACES;
     ctas = ctas < 1 ? 1 : (ctas > static_cast<int>(gridDim.x) ? gridDim.x : ctas);
-    if (N == 0 || static_cast<int>(blockIdx.x) >= ctas) return;
+    if (N == 0 || static_cast<int>(blockIdx.x) >= ctas) {
+        if (a.mode == PAGES_OWN) await_previous();
+        return;
+    }
     // (a border inside a short unit goes to its beginning: the wait for the longer share is less than the 4 us
     // that CTAs take to join a unit; up to 128 places where that share is not much over the others.  16 rows of
     // 1024 tokens 14.9 -> 11.9 us, of 2048 19.0 -> 16.0)
@@ -661,7 +670,6 @@ __global__ void __launch_bounds__(32 * NW, 1) attn_chunks(const InMode<MODE> a) 
         for (int k = 0; k < ST; k++) send();
         st.load_q(qw, a, r, u.row0);
         st.reset();
-        if (r.from > 0 && t0 == 0) st.resume(a, r, u.head, u.row0);
         while (done != sent) {
             const int k = done % ST;
             if (!__all_sync(FULL, mbar_wait(&sh.full[warp][k], done / ST & 1, a.wait_ns))) {
@@ -677,6 +685,10 @@ __global__ void __launch_bounds__(32 * NW, 1) attn_chunks(const InMode<MODE> a) 
             __syncwarp();
             send();
         }
+        if (a.mode == PAGES_OWN && r.from > 0 && t0 == 0) {
+            await_previous();
+            st.take_in(a, r, u.head, u.row0);
+        }
         if (t0 == 0 && t1 == u.chunks) st.to_output(a, r, u.head, u.row0);
         else {
             __syncwarp();
@@ -684,6 +696,7 @@ __global__ void __launch_bounds__(32 * NW, 1) attn_chunks(const InMode<MODE> a) 
             if (lane == 0) sh.unit[2 * warp + (t0 == 0)] = u.first;
         }
     }
+    if (a.mode == PAGES_OWN) await_previous();
     __syncthreads();
 
     // The records that warps left, in order: a unit's are neighbours (a run), the first of
@@ -707,7 +720,7 @@ __global__ void __launch_bounds__(32 * NW, 1) attn_chunks(const InMode<MODE> a) 
         const PageRow r = known_row<D, NT, NW>(sh, a, u.i);
         const int n = __popc(run), even = (k0 + 1) & ~1, odd = k0 & 1;
         auto part_of = [&](int k) -> const float * { return k < odd ? sh.record(k0) : sh.rec[(even >> 1) + k - odd]; };
-        float *to = a.records + (2LL * blockIdx.x + begins) * REC;
+        float *to = records + (2LL * blockIdx.x + begins) * REC;
         for (int i = tid % TH; i < ITEMS; i += TH) {
             float acc[4], m, l;
             const int row = i / (D / 4), c = i % (D / 4) * 4;
@@ -734,8 +747,8 @@ __global__ void __launch_bounds__(32 * NW, 1) attn_chunks(const InMode<MODE> a) 
             const Unit u = find_unit<D, NT, NW>(sh, a, first);
             const int cf = share_of(N, ctas, first), others = share_of(N, ctas, first + u.chunks - 1) - cf;
             if (lane == 0) {
-                all = atomic_add_acq_rel_gpu(a.tickets + cf, 1) == others;
-                if (all) a.tickets[cf] = 0;  // for the next call
+                all = atomic_add_acq_rel_gpu(tickets + cf, 1) == others;
+                if (all) tickets[cf] = 0;  // for the next call
             }
         }
         if (lane == 0) sh.last[warp] = all;
@@ -748,7 +761,7 @@ __global__ void __launch_bounds__(32 * NW, 1) attn_chunks(const InMode<MODE> a) 
         const Unit u = find_unit<D, NT, NW>(sh, a, first);
         const PageRow r = known_row<D, NT, NW>(sh, a, u.i);
         const int cf = share_of(N, ctas, first), n = share_of(N, ctas, first + u.chunks - 1) - cf + 1;
-        auto cta_of = [&](int k) -> const float * { return a.records + (2LL * (cf + k) + (k == 0)) * REC; };
+        auto cta_of = [&](int k) -> const float * { return records + (2LL * (cf + k) + (k == 0)) * REC; };
         for (int i = tid; i < ITEMS; i += 32 * NW) {
             float acc[4], m, l;
             const int row = i / (D / 4), c = i % (D / 4) * 4;
@@ -762,6 +775,7 @@ template <int D, int NT, int NW, bool TWO, int MODE>
 int launch_as(const PagesAttnArgs &a, int grid, cudaStream_t st) {
     const int smem = static_cast<int>(sizeof(Shared<D, NT, NW>));
     if (const int e = allow_shared<attn_chunks<D, NT, NW, TWO, MODE>>(smem)) return e;
+    if (MODE == PAGES_OWN) return launch_overlapping(attn_chunks<D, NT, NW, TWO, MODE>, dim3(grid), 32 * NW, smem, st, InMode<MODE>{a});
     attn_chunks<D, NT, NW, TWO, MODE><<<grid, 32 * NW, smem, st>>>(InMode<MODE>{a});
     return static_cast<int>(cudaGetLastError());
 }

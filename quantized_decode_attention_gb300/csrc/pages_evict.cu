@@ -63,7 +63,7 @@ __global__ void __launch_bounds__(CH_THREADS) choose_kernel(PagesEvictArgs a, in
     const PagesView &p = a.p;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int head = blockIdx.y, layer = blockIdx.z, src = a.src[blockIdx.x], dst = a.dst[blockIdx.x];
-    asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
+    let_next_start();
     for (int i = tid; i < BINS; i += CH_THREADS) sh.hist[i] = 0;
     // is dst in order: a row of its own, named once?
     bool bad = src >= p.max_seqs || dst >= p.max_seqs || src == dst;
@@ -210,7 +210,7 @@ __global__ void __launch_bounds__(GA_THREADS, 6) gather_kernel(PagesEvictArgs a)
     const PagesView &p = a.p;
     int4 *pair = reinterpret_cast<int4 *>(dyn);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, head = blockIdx.y, layer = blockIdx.z;
-    asm volatile("griddepcontrol.wait;\n" ::: "memory");
+    await_previous();
     int pages = 0;
     for (int i0 = 0; i0 < a.n; i0 += GA_THREADS) {
         const int i = i0 + tid, keep = i < a.n ? a.keeps[i] : 0, w = (keep + p.P - 1) / p.P;
@@ -449,18 +449,9 @@ __global__ void __launch_bounds__(GA_THREADS, 6) gather_kernel(PagesEvictArgs a)
 
 template <int D, int B>
 int launch_gather(const PagesEvictArgs &a, int num_sms, cudaStream_t st) {
-    cudaLaunchConfig_t cfg{};
     const long long units = static_cast<long long>(a.p.Hkv) * a.p.n_layers, room = 6LL * num_sms;
-    cfg.gridDim = dim3(static_cast<unsigned>(units < room ? room / units : 1), a.p.Hkv, a.p.n_layers);
-    cfg.blockDim = dim3(GA_THREADS);
-    cfg.dynamicSmemBytes = a.n * 16;
-    cfg.stream = st;
-    cudaLaunchAttribute at{};
-    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at.val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = &at;
-    cfg.numAttrs = 1;
-    return static_cast<int>(cudaLaunchKernelEx(&cfg, gather_kernel<D, B>, a));
+    const dim3 grid(static_cast<unsigned>(units < room ? room / units : 1), a.p.Hkv, a.p.n_layers);
+    return launch_overlapping(gather_kernel<D, B>, grid, GA_THREADS, a.n * 16, st, a);
 }
 template <int D>
 int launch_gather_of(const PagesEvictArgs &a, int num_sms, cudaStream_t st) {

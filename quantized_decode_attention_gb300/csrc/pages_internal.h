@@ -53,8 +53,14 @@ constexpr int PAGES_REC_FLOATS = 256 * (128 + 2);
 inline size_t pages_ws_lists(int n_pages) {  // bytes of the lists, a multiple of 16
     return (PAGES_WS_HEAD * 4 + 12 * static_cast<size_t>(n_pages) + 15) / 16 * 16;
 }
-inline size_t pages_ws_bytes(int n_pages) {
+// Then tickets and records (of 16 query rows) of its own for the launch of shared attention over the rows' own pages, which
+// begins while the one over the common pages still runs.
+constexpr int PAGES_OWN_REC_FLOATS = 16 * (128 + 2);
+inline size_t pages_ws_own(int n_pages) {
     return pages_ws_lists(n_pages) + PAGES_MAX_CTAS * 20 + static_cast<size_t>(PAGES_MAX_CTAS) * 2 * PAGES_REC_FLOATS * 4;
+}
+inline size_t pages_ws_bytes(int n_pages) {
+    return pages_ws_own(n_pages) + PAGES_MAX_CTAS * 4 + static_cast<size_t>(PAGES_MAX_CTAS) * 2 * PAGES_OWN_REC_FLOATS * 4;
 }
 
 struct PagesStoreArgs {
@@ -82,6 +88,8 @@ struct PagesAttnArgs {
     const int *groups;    // where each group begins among call_rows rows (NULL: one group of all)
     const int *plan;      // [call_rows][2]: tokens in common, the table row that they are read from
     int call_rows;
+    int *own_tickets;     // workspace: of the launch over the rows' own pages
+    float *own_records;
     float *part;          // the parts of all queries: accumulators [n_tok Hq][d], then [n_tok Hq][2] maximum and sum
     const uint16_t *q;
     long long qt, qh;

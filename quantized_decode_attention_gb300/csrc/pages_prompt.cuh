@@ -39,6 +39,7 @@ constexpr float MOST = 32768.f;   // ... and may grow to 2^15 (a logit 2^8 over 
 constexpr int TILE = 128, ROWS = 2 * TILE;   // query rows of a tile, of a unit
 constexpr int KEYS = 128;                    // keys at a time
 constexpr int UNIT_COST = 512, MIN_SHARE = 1024;  // tokens: of a unit's beginning and end; that make a CTA worth its parts
+constexpr int MIN_SHARE_COMMON = 512;  // of pages in common, whose parts are joined in any case (64 rows over 8192 tokens: 4 % less than 1024)
 constexpr int THREADS = 512;
 
 __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
@@ -229,6 +230,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prompt(const InMode<MODE> a) 
     const PagesView &p = a.p;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int tb = ROWS / p.G;  // tokens of a block
+    let_next_start();
     if (tid == 0) {
 #pragma unroll
         for (int i = 0; i < 2; i++) {
@@ -284,7 +286,10 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prompt(const InMode<MODE> a) 
         if (a.lse)
             for (long long k = tid; k < static_cast<long long>(r.n) * p.Hq; k += THREADS) a.lse[static_cast<long long>(r.q0) * p.Hq + k] = -INFINITY;
     }
-    int ctas = static_cast<int>(N / MIN_SHARE < gridDim.x ? N / MIN_SHARE : gridDim.x);
+    // (the workspace is the launch's before, up to its end)
+    if (a.mode == PAGES_OWN) await_previous();
+    constexpr int worth = MODE == PAGES_COMMON ? MIN_SHARE_COMMON : MIN_SHARE;
+    int ctas = static_cast<int>(N / worth < gridDim.x ? N / worth : gridDim.x);
     if (ctas < 1) ctas = 1;
     int4 *join = reinterpret_cast<int4 *>(a.joins) + blockIdx.x;
     if (N == 0 || static_cast<int>(blockIdx.x) >= ctas) {
@@ -678,9 +683,11 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prompt(const InMode<MODE> a) 
 }
 
 // The units that crossed a share's border: CTA (c, y) adds up the parts of the unit that
-// began in share c and went on, 16 channels of its 256 rows, in CTA order.
+// began in share c and went on, 8 channels of its 256 rows, in CTA order.
 template <int D, int MODE>
 __global__ void __launch_bounds__(ROWS) join_parts(const InMode<MODE> a) {
+    let_next_start();
+    await_previous();
     const int4 what = reinterpret_cast<const int4 *>(a.joins)[blockIdx.x];  // row of the call, KV head, block, parts
     const int n = what.w, row = threadIdx.x, tb = ROWS / a.p.G, c = blockIdx.y;
     const PagesView &p = a.p;
@@ -688,49 +695,51 @@ __global__ void __launch_bounds__(ROWS) join_parts(const InMode<MODE> a) {
     const PageRow r = attn_row(a, what.x);
     const int tok = what.z * tb + row / p.G;
     if (row >= tb * p.G || tok >= r.n) return;
-    constexpr int REC = ROWS * (D + 2);
-    float m = -INFINITY, l = 0.f, acc[16];
-#pragma unroll
-    for (int i = 0; i < 16; i++) acc[i] = 0.f;
-    auto add = [&](const float4 (&v)[4], float2 sums) {
-        float wa, wb;
-        join_sums(m, l, sums, wa, wb);
-#pragma unroll
-        for (int i = 0; i < 4; i++) {
-            acc[4 * i] = acc[4 * i] * wa + v[i].x * wb;
-            acc[4 * i + 1] = acc[4 * i + 1] * wa + v[i].y * wb;
-            acc[4 * i + 2] = acc[4 * i + 2] * wa + v[i].z * wb;
-            acc[4 * i + 3] = acc[4 * i + 3] * wa + v[i].w * wb;
-        }
-    };
-#pragma unroll 2
-    for (int j = 0; j < n; j++) {
-        const float *rec = a.records + (2LL * (blockIdx.x + j) + (j == 0)) * REC;
-        const float mk = rec[ROWS * D + row], lk = rec[ROWS * (D + 1) + row];
-        float4 v[4];
-#pragma unroll
-        for (int i = 0; i < 4; i++) v[i] = *reinterpret_cast<const float4 *>(rec + ((4 * c + i) * ROWS + row) * 4);
-        add(v, make_float2(mk, lk));
-    }
     const long long o = (static_cast<long long>(r.q0) + tok) * p.Hq + what.y * p.G + row % p.G;
-    float4 *part = reinterpret_cast<float4 *>(a.part + o * D + 16 * c);
-    if (a.mode == PAGES_COMMON) {
+    float4 *part = reinterpret_cast<float4 *>(a.part + o * D + 8 * c);
+    constexpr int REC = ROWS * (D + 2);
+    auto rec_of = [&](int k) -> const float * { return a.records + (2LL * (blockIdx.x + k) + (k == 0)) * REC; };
+    // the maximum first: then no part waits for another
+    float m = -INFINITY;
+#pragma unroll 8
+    for (int k = 0; k < n; k++) m = fmaxf(m, rec_of(k)[ROWS * D + row]);
+    float2 before = make_float2(-INFINITY, 0.f);
+    if (a.mode == PAGES_OWN && r.from > 0) before = reinterpret_cast<const float2 *>(part_sums<D>(a))[o];
+    m = fmaxf(m, before.x);
+    const float mu = m == -INFINITY ? 0.f : m;
+    float l = 0.f, acc[8];
 #pragma unroll
-        for (int i = 0; i < 4; i++) part[i] = make_float4(acc[4 * i], acc[4 * i + 1], acc[4 * i + 2], acc[4 * i + 3]);
+    for (int i = 0; i < 8; i++) acc[i] = 0.f;
+    auto add = [&](float4 x, float4 y, float mk, float lk) {
+        const float w = ex2(mk - mu);  // 0 for a part that saw nothing
+        l += lk * w;
+        acc[0] += x.x * w;
+        acc[1] += x.y * w;
+        acc[2] += x.z * w;
+        acc[3] += x.w * w;
+        acc[4] += y.x * w;
+        acc[5] += y.y * w;
+        acc[6] += y.z * w;
+        acc[7] += y.w * w;
+    };
+#pragma unroll 4
+    for (int k = 0; k < n; k++) {
+        const float *rec = rec_of(k);
+        const float4 *v = reinterpret_cast<const float4 *>(rec + (2 * c * ROWS + row) * 4);
+        add(v[0], v[ROWS], rec[ROWS * D + row], rec[ROWS * (D + 1) + row]);
+    }
+    if (a.mode == PAGES_COMMON) {
+        part[0] = make_float4(acc[0], acc[1], acc[2], acc[3]);
+        part[1] = make_float4(acc[4], acc[5], acc[6], acc[7]);
         if (c == 0) reinterpret_cast<float2 *>(part_sums<D>(a))[o] = make_float2(m, l);
         return;
     }
-    if (r.from > 0) {
-        const float4 v[4] = {part[0], part[1], part[2], part[3]};
-        add(v, reinterpret_cast<const float2 *>(part_sums<D>(a))[o]);
-    }
+    if (a.mode == PAGES_OWN && r.from > 0) add(part[0], part[1], before.x, before.y);
     const float by = l == 0.f ? 0.f : a.out_scale / l;
-    uint32_t w[8];
+    uint32_t w[4];
 #pragma unroll
-    for (int i = 0; i < 8; i++) w[i] = pack2(to16(acc[2 * i] * by, p.bf16), to16(acc[2 * i + 1] * by, p.bf16));
-    uint4 *dst = reinterpret_cast<uint4 *>(a.out + o * D + 16 * c);
-    dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
-    dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
+    for (int i = 0; i < 4; i++) w[i] = pack2(to16(acc[2 * i] * by, p.bf16), to16(acc[2 * i + 1] * by, p.bf16));
+    *reinterpret_cast<uint4 *>(a.out + o * D + 8 * c) = make_uint4(w[0], w[1], w[2], w[3]);
     if (c == 0 && a.lse) a.lse[o] = l == 0.f ? -INFINITY : (m - LIFT + log2f(l)) * LN2;
 }
 
@@ -738,11 +747,14 @@ template <int D, int MODE>
 int launch_as(const PagesAttnArgs &a, int grid, cudaStream_t st) {
     const int smem = static_cast<int>(sizeof(Shared<D>)) + 1024;  // room to put it on a 1024-byte boundary
     if (const int e = allow_shared<attn_prompt<D, MODE>>(smem)) return e;
-    attn_prompt<D, MODE><<<grid, THREADS, smem, st>>>(InMode<MODE>{a});
-    const cudaError_t e1 = cudaGetLastError();
-    if (e1 != cudaSuccess) return static_cast<int>(e1);
-    join_parts<D, MODE><<<dim3(grid, D / 16), ROWS, 0, st>>>(InMode<MODE>{a});
-    return static_cast<int>(cudaGetLastError());
+    if (MODE == PAGES_OWN) {
+        if (const int e = launch_overlapping(attn_prompt<D, MODE>, dim3(grid), THREADS, smem, st, InMode<MODE>{a})) return e;
+    } else {
+        attn_prompt<D, MODE><<<grid, THREADS, smem, st>>>(InMode<MODE>{a});
+        const cudaError_t e = cudaGetLastError();
+        if (e != cudaSuccess) return static_cast<int>(e);
+    }
+    return launch_overlapping(join_parts<D, MODE>, dim3(grid, D / 8), ROWS, 0, st, InMode<MODE>{a});
 }
 template <int MODE>
 int launch_many(const PagesAttnArgs &a, int grid, void *stream) {
