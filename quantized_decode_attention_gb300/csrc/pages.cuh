@@ -38,13 +38,20 @@ int allow_shared(int bytes) {
     return static_cast<int>(e);
 }
 
+// How many CTAs the launch over the rows' own pages takes, of `grid`, for n places of UNIT_COST and chunks of 32 tokens: few
+// where they are done with it before the common pages are, which then have the other SMs at the same time.
+__device__ __forceinline__ int own_ctas(int n, int grid) {
+        constexpr int PLACES = 96, MOST = 64;
+    return n <= PLACES * MOST ? MOST : grid;
+}
+
 // A kernel launched by launch_overlapping may start while the one before it in the stream still runs, once all of that
 // one's CTAs have called let_next_start or ended; it waits for its end with await_previous.  Every CTA of it does, so that its
 // own end is behind that one's too.
 __device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory"); }
 __device__ __forceinline__ void await_previous() { asm volatile("griddepcontrol.wait;\n" ::: "memory"); }
-template <class K, class A>
-int launch_overlapping(K kernel, dim3 grid, int threads, int smem, cudaStream_t st, const A &args) {
+template <class K, class... A>
+int launch_overlapping(K kernel, dim3 grid, int threads, int smem, cudaStream_t st, const A &...args) {
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = grid;
     cfg.blockDim = dim3(threads);
@@ -55,7 +62,7 @@ int launch_overlapping(K kernel, dim3 grid, int threads, int smem, cudaStream_t 
     at.val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = &at;
     cfg.numAttrs = 1;
-    return static_cast<int>(cudaLaunchKernelEx(&cfg, kernel, args));
+    return static_cast<int>(cudaLaunchKernelEx(&cfg, kernel, args...));
 }
 
 // ---- rows ----------------------------------------------------------------------------
@@ -190,12 +197,60 @@ __device__ __forceinline__ uint8_t *summary_ptr(const PagesView &p, int id, int 
     return p.summary + (static_cast<long long>(id) * p.Hkv + head) * p.sum_bytes;
 }
 
+// PAGES_COMMON: this thread's part of the places of the launch over the rows' own pages.  The upper half of the CTA's threads
+// look at them, while the lower ones look at the groups.
+template <int T, class A>
+__device__ __forceinline__ long long own_places(const A &a) {
+    long long n = 0;
+    if (a.mode == PAGES_COMMON && a.after_few && threadIdx.x >= T / 2) {
+        const int few = a.own_max_new * a.p.G <= 8 ? 8 : 16;
+        PagesRows rows = a.r;
+        rows.n_rows = a.call_rows;
+        rows.max_new = a.own_max_new;
+        for (int i = threadIdx.x - T / 2; i < a.call_rows; i += T / 2) {
+            const int from = a.plan[2 * i];
+            const PageRow r = page_row(a.p, rows, i);
+            const int keys = r.len - (from > 0 && from <= r.len - r.n && from % a.p.P == 0 ? from : 0);
+            if (r.len > 0) n += static_cast<long long>((r.n * a.p.G + few - 1) / few) * a.p.Hkv * ((keys + 31) / 32 + FEW_UNIT_COST);
+        }
+    }
+    return n;
+}
+// CTAs that the launch has for itself: those that the one over the rows' own pages, which may still run, does not take.
+template <int T, class A>
+__device__ __forceinline__ int sms_left(const A &a, long long n, long long *part) {
+    if (a.mode != PAGES_COMMON || !a.after_few) return gridDim.x;
+    const int tid = threadIdx.x;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) n += __shfl_xor_sync(FULL, n, o);
+    __syncthreads();
+    if ((tid & 31) == 0) part[tid >> 5] = n;
+    __syncthreads();
+    n = 0;
+    for (int k = 0; k < T / 32; k++) n += part[k];
+    const int left = static_cast<int>(gridDim.x) - (n > 1 << 30 ? static_cast<int>(gridDim.x) : own_ctas(static_cast<int>(n), gridDim.x));
+    return left > 0 ? left : gridDim.x;
+}
+
 // ---- conversions -----------------------------------------------------------------------
 __device__ __forceinline__ float from16(uint16_t x, bool bf16) {
     return bf16 ? __uint_as_float(static_cast<uint32_t>(x) << 16) : __half2float(__ushort_as_half(x));
 }
 __device__ __forceinline__ uint16_t to16(float x, bool bf16) {
     return bf16 ? __bfloat16_as_ushort(__float2bfloat16_rn(x)) : __half_as_ushort(__float2half_rn(x));
+}
+// The larger magnitudes (with signs of no meaning), NaN where there is one.
+template <bool BF16>
+__device__ __forceinline__ uint32_t max2_abs(uint32_t a, uint32_t b) {
+    uint32_t r;
+    if (BF16) asm("max.NaN.xorsign.abs.bf16x2 %0, %1, %2;\n" : "=r"(r) : "r"(a), "r"(b));
+    else asm("max.NaN.xorsign.abs.f16x2 %0, %1, %2;\n" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+template <bool BF16>
+__device__ __forceinline__ float2 pair_to_float(uint32_t w) {
+    if (BF16) return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+    return __half22float2(*reinterpret_cast<const __half2 *>(&w));
 }
 // Four bytes of two codes each -> four half2 of code values (low nibble first).
 __device__ __forceinline__ void e2m1x8_to_half(uint32_t w, uint32_t (&h)[4]) {

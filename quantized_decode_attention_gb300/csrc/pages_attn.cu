@@ -11,17 +11,18 @@ constexpr int PROMPT_ROWS = 32;
 
 }  // namespace
 
-int launch_pages_attention(PagesAttnArgs a, int mode, int num_sms, void *stream) {
+// Attention's launches of one kind; mixed: rows with few query rows are likely.
+static int launch_kind(PagesAttnArgs a, int mode, bool mixed, int num_sms, void *stream) {
     const int grid = num_sms < PAGES_MAX_CTAS ? num_sms : PAGES_MAX_CTAS;
-    const int rows = a.r.max_new * a.p.G;
     a.over = 0;
     a.most = 0x7fffffff;
-    if (!a.sel && rows > PROMPT_ROWS) {
+    if (!a.sel && a.r.max_new * a.p.G > PROMPT_ROWS) {
         // rows with many new tokens on the tensor cores; those of a mixed batch with few, which wait
         // for the cache and not for products, by the kernel for few (one row alone: no second launch)
-        a.over = a.r.n_rows == 1 ? 0 : PROMPT_ROWS;
+        a.over = mixed ? PROMPT_ROWS : 0;
         if (const int e = launch_pages_prompt(a, mode, grid, stream)) return e;
-        if (a.r.n_rows == 1) return 0;
+        if (!mixed) return 0;
+        a.after_few = 0;
         a.over = 0;
         a.most = PROMPT_ROWS;
     }
@@ -32,12 +33,22 @@ int launch_pages_attention(PagesAttnArgs a, int mode, int num_sms, void *stream)
     }
 }
 
+int launch_pages_attention(const PagesAttnArgs &a, int mode, int num_sms, void *stream) {
+    return launch_kind(a, mode, a.r.n_rows > 1, num_sms, stream);
+}
+
+// The launch over the rows' own pages, then the one over what groups have in common.  Where rows (groups) have many query rows
+// on average, all go to the kernel for many: an idle launch for few costs 4 to 8 us (32 rows of 9 to 24 tokens).
 int launch_pages_shared(const PagesAttnArgs &a, int n_groups, int max_group, int num_sms, void *stream) {
+    const auto mixed = [&](int rows) { return rows > 1 && static_cast<long long>(a.r.n_tok) * a.p.G <= static_cast<long long>(PROMPT_ROWS) * rows; };
+    const bool few = a.r.max_new * a.p.G <= PROMPT_ROWS || mixed(a.r.n_rows);
+    if (const int e = launch_kind(a, PAGES_OWN, few, num_sms, stream)) return e;
     PagesAttnArgs c = a;
+    c.own_max_new = a.r.max_new;
+    c.after_few = few;
     c.r.n_rows = n_groups;
     c.r.max_new = max_group;
-    if (const int e = launch_pages_attention(c, PAGES_COMMON, num_sms, stream)) return e;
-    return launch_pages_attention(a, PAGES_OWN, num_sms, stream);
+    return launch_kind(c, PAGES_COMMON, mixed(n_groups), num_sms, stream);
 }
 
 }  // namespace dq

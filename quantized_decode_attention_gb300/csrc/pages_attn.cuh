@@ -41,8 +41,10 @@ namespace {
 constexpr float LN2 = 0.69314718055994530942f;
 constexpr float SLACK = 8.f, LIFT = 7.f;   // log2 units
 constexpr int CHUNK = 32;                  // tokens
-constexpr int UNIT_COST = 2;               // chunks that a unit's beginning and end are worth (40 ragged rows: 76 us, with 0 94)
-constexpr int SHORT = 64;                  // places of a unit that CTAs do not share
+constexpr int UNIT_COST = FEW_UNIT_COST;   // (40 ragged rows: 76 us, with 0 94)
+// Places of a unit that CTAs do not share; of common pages, which few units have, fewer (8 rows behind 2000 tokens, 16 units of 64
+// places, four layers: 77 us, with 64 93).
+constexpr int SHORT_ROWS = 64, SHORT_COMMON = 24;
 constexpr int MIN_PLACES = 16;             // places that make a CTA worth its merge (1 row of 500: 8.4 us, with 64 13.4)
 
 __device__ __forceinline__ void mbar_expect(uint32_t bar, unsigned bytes) {
@@ -289,7 +291,7 @@ struct State {
         }
     }
 
-    // What an earlier launch left for the unit's rows, their maxima, sums and accumulators as they were, beside this state.
+    // What the launch over the rows' own pages left for the unit's rows, beside this state.
     template <class A>
     __device__ __forceinline__ void take_in(const A &a, const PageRow &r, int head, int row0) {
         const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
@@ -301,6 +303,7 @@ struct State {
                 if (row >= r.n * a.p.G) continue;
                 const long long o = query_of(a, r, head, row);
                 const float2 ml = reinterpret_cast<const float2 *>(part_sums<D>(a))[o];
+                if (ml.x == INFINITY) continue;  // (its output is 0)
                 const float mx = fmaxf(m[n][e], ml.x), by = mx == -INFINITY ? 0.f : mx;
                 const float keep = ex2(m[n][e] - by), take = ex2(ml.x - by);  // 0 for a part that saw nothing
                 m[n][e] = mx;
@@ -357,13 +360,14 @@ struct State {
                 const int row = row0 + 8 * n + 2 * t + e;
                 if (row >= rows) continue;
                 const long long o = query_of(a, r, head, row);
-                if (a.mode == PAGES_COMMON) {
+                if (a.mode == PAGES_OWN && r.from > 0) {
 #pragma unroll
                     for (int i = 0; i < D / 16; i++)
                         *reinterpret_cast<float2 *>(a.part + o * D + g * (D / 8) + 2 * i) = make_float2(acc[n][i][e], acc[n][i][e + 2]);
                     if (g == 0) reinterpret_cast<float2 *>(part_sums<D>(a))[o] = make_float2(m[n][e], l[n][e]);
                     continue;
                 }
+                if (a.mode == PAGES_COMMON && reinterpret_cast<const float2 *>(part_sums<D>(a))[o].x == INFINITY) l[n][e] = 0.f;
                 const float w = l[n][e] == 0.f ? 0.f : a.out_scale / l[n][e];
                 uint32_t u[D / 16];
 #pragma unroll
@@ -451,6 +455,18 @@ __device__ __forceinline__ int share_of(int n, int m, int x) {
     return static_cast<unsigned>(x) < ahead ? x / (q + 1) : rest + (x - ahead) / q;
 }
 
+// Four channels of a part beside those of others.
+__device__ __forceinline__ void join(float (&acc)[4], float &m, float &l, float mk, float lk, float4 x) {
+    const float mx = fmaxf(m, mk), mu = mx == -INFINITY ? 0.f : mx;
+    const float wa = ex2(m - mu), wb = ex2(mk - mu);  // 0 for a part that saw nothing
+    m = mx;
+    l = l * wa + lk * wb;
+    acc[0] = acc[0] * wa + x.x * wb;
+    acc[1] = acc[1] * wa + x.y * wb;
+    acc[2] = acc[2] * wa + x.z * wb;
+    acc[3] = acc[3] * wa + x.w * wb;
+}
+
 // One thread's 4 channels at c of row `row` over n records, added up in order.
 template <int D, int NT, class F>
 __device__ __forceinline__ void add_records(int n, int row, int c, F rec_of, float (&acc)[4], float &m, float &l) {
@@ -461,26 +477,24 @@ __device__ __forceinline__ void add_records(int n, int row, int c, F rec_of, flo
     for (int k = 0; k < n; k++) {
         const float *r = rec_of(k);
         const float mk = r[8 * NT * D + row], lk = r[8 * NT * (D + 1) + row];
-        const float4 x = *reinterpret_cast<const float4 *>(r + row * D + c);
-        const float mx = fmaxf(m, mk), mu = mx == -INFINITY ? 0.f : mx;
-        const float wa = ex2(m - mu), wb = ex2(mk - mu);  // 0 for a part that saw nothing
-        m = mx;
-        l = l * wa + lk * wb;
-        acc[0] = acc[0] * wa + x.x * wb;
-        acc[1] = acc[1] * wa + x.y * wb;
-        acc[2] = acc[2] * wa + x.z * wb;
-        acc[3] = acc[3] * wa + x.w * wb;
+        join(acc, m, l, mk, lk, *reinterpret_cast<const float4 *>(r + row * D + c));
     }
 }
 
 template <int D, class A>
-__device__ __forceinline__ void write4(const A &a, const PageRow &r, int head, int row, int c, const float (&acc)[4], float m, float l) {
+__device__ __forceinline__ void write4(const A &a, const PageRow &r, int head, int row, int c, float (&acc)[4], float m, float l) {
     if (row >= r.n * a.p.G) return;
     const long long o = query_of(a, r, head, row);
-    if (a.mode == PAGES_COMMON) {
+    if (a.mode == PAGES_OWN && r.from > 0) {
         *reinterpret_cast<float4 *>(a.part + o * D + c) = make_float4(acc[0], acc[1], acc[2], acc[3]);
         if (c == 0) reinterpret_cast<float2 *>(part_sums<D>(a))[o] = make_float2(m, l);
         return;
+    }
+    if (a.mode == PAGES_COMMON) {  // what the launch over the rows' own pages left
+        const float2 own = reinterpret_cast<const float2 *>(part_sums<D>(a))[o];
+        const float4 x = *reinterpret_cast<const float4 *>(a.part + o * D + c);
+        if (own.x == INFINITY) l = 0.f;
+        else join(acc, m, l, own.x, own.y, x);
     }
     const float w = l == 0.f ? 0.f : a.out_scale / l;
     *reinterpret_cast<uint2 *>(a.out + o * D + c) =
@@ -496,11 +510,12 @@ __global__ void __launch_bounds__(32 * NW, 1) attn_chunks(const InMode<MODE> a) 
     const PagesView &p = a.p;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     constexpr int ST = S::ST;
-    if (a.mode == PAGES_COMMON) let_next_start();
+    if (a.mode == PAGES_OWN) let_next_start();
     int *tickets = a.mode == PAGES_OWN ? a.own_tickets : a.tickets;
     float *records = a.mode == PAGES_OWN ? a.own_records : a.records;
     if (lane < ST) mbar_init(&sh.full[warp][lane], 1 + a.owed);
     fence_mbar_init();
+    const long long own = own_places<32 * NW>(a);
     // places before each row: a prefix over the rows, 32 NW at a time
     long long base = 0;
     for (int i0 = 0; i0 < a.r.n_rows; i0 += 32 * NW) {
@@ -533,7 +548,7 @@ __global__ void __launch_bounds__(32 * NW, 1) attn_chunks(const InMode<MODE> a) 
     }
     if (base > 0x7fffffff) {  // more places than int counts
         if (tid == 0) atomicOr(p.status, PST_ARG);
-        if (a.mode == PAGES_OWN) await_previous();
+        if (a.mode == PAGES_COMMON) await_previous();
         return;
     }
     const int N = static_cast<int>(base);
@@ -547,14 +562,18 @@ __global__ void __launch_bounds__(32 * NW, 1) attn_chunks(const InMode<MODE> a) 
         if (!takes(a, r)) continue;
         uint4 *o = reinterpret_cast<uint4 *>(a.out + static_cast<long long>(r.q0) * p.Hq * D);
         for (long long k = tid; k < static_cast<long long>(r.n) * p.Hq * (D / 8); k += 32 * NW) o[k] = make_uint4(0, 0, 0, 0);
+        if (a.mode == PAGES_OWN && a.plan[2 * i] > 0)
+            for (long long k = tid; k < static_cast<long long>(r.n) * p.Hq; k += 32 * NW)
+                reinterpret_cast<float2 *>(part_sums<D>(a))[static_cast<long long>(r.q0) * p.Hq + k] = make_float2(INFINITY, 0.f);
         if (a.lse)
             for (long long k = tid; k < static_cast<long long>(r.n) * p.Hq; k += 32 * NW) a.lse[static_cast<long long>(r.q0) * p.Hq + k] = -INFINITY;
     }
     // this CTA's places [c0, c1), this warp's [w0, w1)
+    const int room = a.mode == PAGES_OWN ? own_ctas(N, gridDim.x) : (a.mode == PAGES_COMMON ? sms_left<32 * NW>(a, own, sh.part) : gridDim.x);
     int ctas = N / MIN_PLACES;
-    ctas = ctas < 1 ? 1 : (ctas > static_cast<int>(gridDim.x) ? gridDim.x : ctas);
+    ctas = ctas < 1 ? 1 : (ctas > room ? room : ctas);
     if (N == 0 || static_cast<int>(blockIdx.x) >= ctas) {
-        if (a.mode == PAGES_OWN) await_previous();
+        if (a.mode == PAGES_COMMON) await_previous();
         return;
     }
     // (a border inside a short unit goes to its beginning: the wait for the longer share is less than the 4 us
@@ -565,6 +584,7 @@ __global__ void __launch_bounds__(32 * NW, 1) attn_chunks(const InMode<MODE> a) 
         if (x <= 0 || x >= N) return x;
         const Unit u = find_unit<D, NT, NW>(sh, a, x);
         const int places = u.chunks + UNIT_COST;
+        constexpr int SHORT = MODE == PAGES_COMMON ? SHORT_COMMON : SHORT_ROWS;
         return places <= SHORT || (places <= 2 * SHORT && 4LL * places * ctas <= 5LL * N) ? u.first - UNIT_COST : x;
     };
     const int c0 = border(blockIdx.x), c1 = border(blockIdx.x + 1);
@@ -685,7 +705,7 @@ __global__ void __launch_bounds__(32 * NW, 1) attn_chunks(const InMode<MODE> a) 
             __syncwarp();
             send();
         }
-        if (a.mode == PAGES_OWN && r.from > 0 && t0 == 0) {
+        if (a.mode == PAGES_COMMON && t0 == 0 && t1 == u.chunks) {
             await_previous();
             st.take_in(a, r, u.head, u.row0);
         }
@@ -696,7 +716,7 @@ __global__ void __launch_bounds__(32 * NW, 1) attn_chunks(const InMode<MODE> a) 
             if (lane == 0) sh.unit[2 * warp + (t0 == 0)] = u.first;
         }
     }
-    if (a.mode == PAGES_OWN) await_previous();
+    if (a.mode == PAGES_COMMON) await_previous();
     __syncthreads();
 
     // The records that warps left, in order: a unit's are neighbours (a run), the first of
@@ -775,7 +795,7 @@ template <int D, int NT, int NW, bool TWO, int MODE>
 int launch_as(const PagesAttnArgs &a, int grid, cudaStream_t st) {
     const int smem = static_cast<int>(sizeof(Shared<D, NT, NW>));
     if (const int e = allow_shared<attn_chunks<D, NT, NW, TWO, MODE>>(smem)) return e;
-    if (MODE == PAGES_OWN) return launch_overlapping(attn_chunks<D, NT, NW, TWO, MODE>, dim3(grid), 32 * NW, smem, st, InMode<MODE>{a});
+    if (MODE == PAGES_COMMON && a.after_few) return launch_overlapping(attn_chunks<D, NT, NW, TWO, MODE>, dim3(grid), 32 * NW, smem, st, InMode<MODE>{a});
     attn_chunks<D, NT, NW, TWO, MODE><<<grid, 32 * NW, smem, st>>>(InMode<MODE>{a});
     return static_cast<int>(cudaGetLastError());
 }

@@ -1,5 +1,5 @@
-// Paged cache: the kernel for few new tokens as shared attention takes it, over what groups of rows
-// have in common and over what is behind it.
+// Paged cache: the kernel for few new tokens as shared attention takes it, over what is behind the
+// pages that groups of rows have in common, and over those.
 #include "pages_attn.cuh"
 
 namespace dq {

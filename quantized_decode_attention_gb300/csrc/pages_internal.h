@@ -74,13 +74,14 @@ struct PagesReadArgs {
     PagesRows r;
     uint16_t *k, *v;
 };
+constexpr int FEW_UNIT_COST = 2;  // the kernel for few tokens: chunks that a unit's beginning and end are worth
 // Which queries an attention launch answers, over which of a row's tokens: a constant of each kernel
 // (as a variable it costs attention of single tokens 7 %).
 enum : int {
     PAGES_NEWEST = 0,  // the call's rows' newest tokens, over what they hold up to them
     PAGES_ALL = 1,     // queries of the call's rows, over all they hold
-    PAGES_COMMON = 2,  // the tokens of groups of rows, over the pages that a group has in common: parts
-    PAGES_OWN = 3      // the call's rows' newest tokens, over what is behind those pages, from their parts on
+    PAGES_OWN = 2,     // the call's rows' newest tokens, over what is behind the pages that their groups have in common: parts
+    PAGES_COMMON = 3   // the tokens of groups of rows, over those pages, and the parts with it
 };
 struct PagesAttnArgs {
     PagesView p;
@@ -90,7 +91,11 @@ struct PagesAttnArgs {
     int call_rows;
     int *own_tickets;     // workspace: of the launch over the rows' own pages
     float *own_records;
-    float *part;          // the parts of all queries: accumulators [n_tok Hq][d], then [n_tok Hq][2] maximum and sum
+    // The parts of the queries whose group has pages in common: accumulators [n_tok Hq][d], then [n_tok Hq][2] maximum and
+    // sum, a maximum of +inf where the row holds nothing.
+    float *part;
+    int own_max_new;      // PAGES_COMMON: max_new of the launch over the rows' own pages
+    int after_few;        // the launch before this one is the kernel for few tokens, whose end need not be waited for at the start
     const uint16_t *q;
     long long qt, qh;
     uint16_t *out;
@@ -151,7 +156,7 @@ int launch_pages_fork(const PagesView &p, const int *src, const int *dst, int n,
 int launch_pages_compact(const PagesView &p, int *ws, int num_sms, void *stream);
 int launch_pages_append(const PagesStoreArgs &a, void *stream);
 int launch_pages_read(const PagesReadArgs &a, void *stream);
-int launch_pages_attention(PagesAttnArgs a, int mode, int num_sms, void *stream);
+int launch_pages_attention(const PagesAttnArgs &a, int mode, int num_sms, void *stream);
 int launch_pages_few_shared(const PagesAttnArgs &a, int mode, int grid, void *stream);
 // many new tokens: the tensor-core kernel on at most `grid` CTAs
 int launch_pages_prompt(const PagesAttnArgs &a, int mode, int grid, void *stream);

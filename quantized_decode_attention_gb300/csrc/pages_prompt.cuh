@@ -122,6 +122,68 @@ __device__ __forceinline__ float top_of(const uint32_t (&s)[32]) {
     return fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3]));
 }
 
+// A warp's 32 query rows of a block of tokens from tok0 on, as binary16 operands in shared memory: each by a power of two
+// below 2^14 and with sm_scale's sign.  Returns this lane's row's logit unit.  A row is D / 8 lanes' 16 bytes, so that whole
+// lines are read; two elements go at a time (where a CTA has few keys this is a good part of its time).
+template <int D, bool BF16, class A>
+__device__ __forceinline__ float put_queries(const A &a, const PageRow &r, int head, int tok0, int tb, uint8_t *to) {
+    constexpr int LANES = D / 8, PER = 32 / LANES, DEEP = 4;
+    const int G = a.p.G, lane = threadIdx.x & 31, warp = threadIdx.x >> 5, piece = lane % LANES, sub = lane / LANES, row0 = (warp & 7) * 32;
+    const unsigned inv = 65536 / G + 1;  // i / G = i inv / 65536 for i below 256
+    const uint16_t *src = a.q + (static_cast<long long>(r.q0) + tok0) * a.qt + head * G * a.qh + 8 * piece;
+    float f = 0.f;
+    // every line of the 32 rows is sent for at once, a row a lane, so that the loads below wait once for all
+    {
+        const unsigned i = row0 + lane, tk = i * inv >> 16, h = i - tk * G;
+        if (static_cast<int>(tk) < tb && tok0 + static_cast<int>(tk) < r.n) {
+            const uint16_t *at = src - 8 * piece + tk * a.qt + h * a.qh;
+#pragma unroll
+            for (int k = 0; k < D / 64; k++) {
+                uint32_t x;
+                asm volatile("ld.global.b32 %0, [%1];\n" : "=r"(x) : "l"(at + 64 * k));
+            }
+        }
+    }
+#pragma unroll 1
+    for (int i0 = 0; i0 < 32; i0 += PER * DEEP) {
+        uint4 w[DEEP];
+#pragma unroll
+        for (int k = 0; k < DEEP; k++) {
+            const unsigned i = row0 + i0 + k * PER + sub, tk = i * inv >> 16, h = i - tk * G;
+            const bool is = static_cast<int>(tk) < tb && tok0 + static_cast<int>(tk) < r.n;
+            w[k] = is ? *reinterpret_cast<const uint4 *>(src + tk * a.qt + h * a.qh) : make_uint4(0, 0, 0, 0);
+        }
+        float top[DEEP];
+#pragma unroll
+        for (int k = 0; k < DEEP; k++) {
+            const uint32_t m = max2_abs<BF16>(max2_abs<BF16>(w[k].x, w[k].y), max2_abs<BF16>(w[k].z, w[k].w));
+            top[k] = fmaxf(from16(static_cast<uint16_t>(m & 0x7fffu), BF16), from16(static_cast<uint16_t>(m >> 16 & 0x7fffu), BF16));
+        }
+#pragma unroll
+        for (int o = 1; o < LANES; o <<= 1)
+#pragma unroll
+            for (int k = 0; k < DEEP; k++) top[k] = fmaxf(top[k], __shfl_xor_sync(FULL, top[k], o));
+#pragma unroll
+        for (int k = 0; k < DEEP; k++) {
+            int up = 13 - (static_cast<int>(__float_as_uint(top[k]) >> 23) - 127);
+            up = top[k] > 0.f ? (up > 126 ? 126 : up) : 0;
+            const float by = a.scale_log2 < 0.f ? -pow2i(up) : pow2i(up);
+            const uint32_t u[4] = {w[k].x, w[k].y, w[k].z, w[k].w};
+            uint32_t h[4];
+#pragma unroll
+            for (int j = 0; j < 4; j++) {
+                const float2 x = pair_to_float<BF16>(u[j]);
+                h[j] = half2_of(x.x * by, x.y * by);
+            }
+            const int i = i0 + k * PER;
+            *reinterpret_cast<uint4 *>(to + (piece >> 3) * (TILE * 128) + swizzled((warp & 3) * 32 + i + sub, piece & 7)) = make_uint4(h[0], h[1], h[2], h[3]);
+            const int mine = __shfl_sync(FULL, up, lane % PER * LANES);  // lane i + s has row i + s, whose lanes begin at s LANES
+            if (lane >= i && lane < i + PER) f = fabsf(a.scale_log2) * pow2i(-mine);
+        }
+    }
+    return f;
+}
+
 // ---- the line of units ---------------------------------------------------------------------
 // Row i's units: blocks of `tb` tokens in order, KV heads within.  Block b is as long as
 // the keys that a full block would see, plus UNIT_COST: base + (b + 1) tb.
@@ -143,6 +205,9 @@ struct Shared {
     uint32_t tmem;
 };
 
+__device__ __forceinline__ long long over(long long n, long long m) {  // n / m, both positive: 32 bits where they are enough
+    return (n | m) >> 32 ? n / m : static_cast<unsigned>(n) / static_cast<unsigned>(m);
+}
 __device__ __forceinline__ long long blocks_before(long long base, int more, int b) {  // places of blocks 0 .. b - 1 of one head
     return b * (base + UNIT_COST) + static_cast<long long>(more) * b * (b + 1) / 2;
 }
@@ -173,18 +238,18 @@ __device__ Unit find_unit(const Shared<D> &sh, const A &a, int tb, long long x) 
     }
     u.b = b0;
     const long long before = a.p.Hkv * blocks_before(base, more, b0), w = base + UNIT_COST + static_cast<long long>(b0 + 1) * more;
-    u.head = static_cast<int>((in - before) / w);
+    u.head = static_cast<int>(over(in - before, w));
     u.start = sh.first[lo] + before + u.head * w;
     u.end = u.start + w;
     return u;
 }
 __device__ __forceinline__ long long share(long long n, int m, int k) {
-    const long long q = n / m, rest = n - q * m;
+    const long long q = over(n, m), rest = n - q * m;
     return k * q + (k < rest ? k : rest);
 }
 __device__ __forceinline__ int share_of(long long n, int m, long long x) {
-    const long long q = n / m, rest = n - q * m, ahead = rest * (q + 1);
-    return static_cast<int>(x < ahead ? x / (q + 1) : rest + (x - ahead) / q);
+    const long long q = over(n, m), rest = n - q * m, ahead = rest * (q + 1);
+    return static_cast<int>(x < ahead ? over(x, q + 1) : rest + over(x - ahead, q));
 }
 
 // Maximum m and sum l of a part take another's in: the accumulators go by `keep` and `take`.
@@ -200,7 +265,7 @@ __device__ __forceinline__ void join_sums(float &m, float &l, float2 other, floa
 struct Segment {
     Unit u;
     int t0, t1;
-    bool begins, ends;
+    bool begins, ends, two;  // two: the block has query rows in its second tile
 };
 template <int D, class A>
 __device__ Segment find_segment(const Shared<D> &sh, const A &a, int tb, long long x, long long c1) {
@@ -215,6 +280,7 @@ __device__ Segment find_segment(const Shared<D> &sh, const A &a, int tb, long lo
         const long long t = (at - s.u.start - UNIT_COST + KEYS - 1) / KEYS;
         return at - s.u.start <= UNIT_COST ? 0 : (t < tiles ? static_cast<int>(t) : tiles);
     };
+    s.two = (last - s.u.b * tb) * a.p.G > TILE;
     s.t0 = s.begins ? 0 : tile_at(x);
     s.t1 = s.ends ? tiles : tile_at(c1);
     return s;
@@ -246,6 +312,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prompt(const InMode<MODE> a) 
         mbar_init(&sh.drained, 1);
         fence_mbar_init();
     }
+    const long long own = own_places<THREADS>(a);
     // places before each row
     long long base = 0;
     for (int i0 = 0; i0 < a.r.n_rows; i0 += THREADS) {
@@ -285,22 +352,27 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prompt(const InMode<MODE> a) 
         for (long long k = tid; k < static_cast<long long>(r.n) * p.Hq * (D / 8); k += THREADS) o[k] = make_uint4(0, 0, 0, 0);
         if (a.lse)
             for (long long k = tid; k < static_cast<long long>(r.n) * p.Hq; k += THREADS) a.lse[static_cast<long long>(r.q0) * p.Hq + k] = -INFINITY;
+        if (a.mode == PAGES_OWN && a.plan[2 * i] > 0)
+            for (long long k = tid; k < static_cast<long long>(r.n) * p.Hq; k += THREADS)
+                reinterpret_cast<float2 *>(part_sums<D>(a))[static_cast<long long>(r.q0) * p.Hq + k] = make_float2(INFINITY, 0.f);
     }
-    // (the workspace is the launch's before, up to its end)
-    if (a.mode == PAGES_OWN) await_previous();
     constexpr int worth = MODE == PAGES_COMMON ? MIN_SHARE_COMMON : MIN_SHARE;
-    int ctas = static_cast<int>(N / worth < gridDim.x ? N / worth : gridDim.x);
+    const int room = sms_left<THREADS>(a, own, sh.part);
+    int ctas = static_cast<int>(N / worth < room ? N / worth : room);
     if (ctas < 1) ctas = 1;
     int4 *join = reinterpret_cast<int4 *>(a.joins) + blockIdx.x;
     if (N == 0 || static_cast<int>(blockIdx.x) >= ctas) {
         if (tid == 0) *join = make_int4(0, 0, 0, 0);
+        if (a.mode == PAGES_COMMON) await_previous();
         return;
     }
     const long long c0 = share(N, ctas, blockIdx.x), c1 = share(N, ctas, blockIdx.x + 1);
     if (tid == 0) {  // the unit that begins here and goes on in other CTAs, if any
         const Unit u = find_unit<D>(sh, a, tb, c1 - 1);
         const bool on = u.start >= c0 && u.end > c1;
-        *join = on ? make_int4(u.i, u.head, u.b, share_of(N, ctas, u.end - 1) - static_cast<int>(blockIdx.x) + 1) : make_int4(0, 0, 0, 0);
+        const int t0 = u.b * tb, n = u.r.n - t0 < tb ? u.r.n - t0 : tb;
+        *join = on ? make_int4(u.r.q0 + t0, u.head | (u.r.from > 0) << 16, n * p.G, share_of(N, ctas, u.end - 1) - static_cast<int>(blockIdx.x) + 1)
+                   : make_int4(0, 0, 0, 0);
     }
     if (warp == 12) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;\n" ::"r"(smem_u32(&sh.tmem)) : "memory");
@@ -327,7 +399,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prompt(const InMode<MODE> a) 
 
     if (warp < 8) {
         // ---- softmax: a thread a query row --------------------------------------------------
-        const int t = warp >> 2, mine = tid & (TILE - 1), row = tid;  // tile, row of the tile, row of the unit
+        const int t = warp >> 2, row = tid;  // tile, row of the unit
         const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;  // 32 lanes of tensor memory
         const uint32_t s_at = tmem + lanes + t * KEYS, o_at = tmem + lanes + 2 * KEYS + t * D;
         unsigned runs = 0, it = 0;
@@ -335,38 +407,16 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prompt(const InMode<MODE> a) 
             const Segment g = find_segment<D>(sh, a, tb, x, c1);
             const PageRow &r = g.u.r;
             x = g.u.end;
+            if (t == 1 && !g.two) continue;
             const int tok = g.u.b * tb + row / p.G, gq = row % p.G;
             const bool real = row < tb * p.G && tok < r.n;
             const int pos = real ? first_sees(a, r) + tok * a.step : 0x7fffffff;  // no row: nothing to mask
             // the query, by a power of two below 2^14 and with sm_scale's sign, as binary16
             RowState row_s{0.f, -INFINITY, {0, 0}};
             if (g.t0 < g.t1) {
-                const uint16_t *src = a.q + (static_cast<long long>(r.q0) + tok) * a.qt + (g.u.head * p.G + gq) * a.qh;
-                uint4 w[D / 8];
-#pragma unroll
-                for (int i = 0; i < D / 8; i++) w[i] = real ? *reinterpret_cast<const uint4 *>(src + 8 * i) : make_uint4(0, 0, 0, 0);
-                float top = 0.f;
-#pragma unroll
-                for (int i = 0; i < D / 8; i++) {
-                    const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
-#pragma unroll
-                    for (int j = 0; j < 4; j++)
-                        top = fmaxf(top, fmaxf(fabsf(from16(static_cast<uint16_t>(u[j] & 0xffffu), p.bf16)), fabsf(from16(static_cast<uint16_t>(u[j] >> 16), p.bf16))));
-                }
-                int up = 13 - (static_cast<int>(__float_as_uint(top) >> 23) - 127);
-                up = top > 0.f ? (up > 126 ? 126 : up) : 0;
-                const float by = a.scale_log2 < 0.f ? -pow2i(up) : pow2i(up);
+                const float f = p.bf16 ? put_queries<D, true>(a, r, g.u.head, g.u.b * tb, tb, sh.q[t]) : put_queries<D, false>(a, r, g.u.head, g.u.b * tb, tb, sh.q[t]);
                 // (never 0: a hidden key's -inf stays one)
-                row_s.f = fmaxf(fabsf(a.scale_log2) * pow2i(-up), 1e-37f);
-#pragma unroll
-                for (int i = 0; i < D / 8; i++) {
-                    const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
-                    uint32_t h[4];
-#pragma unroll
-                    for (int j = 0; j < 4; j++)
-                        h[j] = half2_of(from16(static_cast<uint16_t>(u[j] & 0xffffu), p.bf16) * by, from16(static_cast<uint16_t>(u[j] >> 16), p.bf16) * by);
-                    *reinterpret_cast<uint4 *>(sh.q[t] + (i >> 3) * (TILE * 128) + swizzled(mine, i & 7)) = make_uint4(h[0], h[1], h[2], h[3]);
-                }
+                row_s.f = fmaxf(f, 1e-37f);
                 fence_proxy_async();
                 mbar_arrive(&sh.q_full[t]);
             }
@@ -442,7 +492,14 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prompt(const InMode<MODE> a) 
             const bool whole = g.begins && g.ends;
             float *rec = a.records + (2LL * blockIdx.x + g.begins) * REC;
             float l = row_s.sum(), m = row_s.m, keep = 1.f, take = 0.f;
-            if (whole && real && r.from > 0) join_sums(m, l, reinterpret_cast<const float2 *>(part_sums<D>(a))[o], keep, take);
+            if (a.mode == PAGES_COMMON && whole) {
+                await_previous();
+                if (real) {
+                    const float2 own = reinterpret_cast<const float2 *>(part_sums<D>(a))[o];
+                    if (own.x == INFINITY) l = 0.f;
+                    else join_sums(m, l, own, keep, take);
+                }
+            }
             const float by = l == 0.f ? 0.f : a.out_scale / l;
 #pragma unroll 1
             for (int c = 0; c < D / 32; c++) {
@@ -458,12 +515,12 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prompt(const InMode<MODE> a) 
 #pragma unroll
                     for (int i = 0; i < 8; i++)
                         *reinterpret_cast<uint4 *>(rec + ((8 * c + i) * ROWS + row) * 4) = make_uint4(s[4 * i], s[4 * i + 1], s[4 * i + 2], s[4 * i + 3]);
-                } else if (real && a.mode == PAGES_COMMON) {
+                } else if (real && a.mode == PAGES_OWN && r.from > 0) {
 #pragma unroll
                     for (int i = 0; i < 8; i++)
                         *reinterpret_cast<uint4 *>(a.part + o * D + 32 * c + 4 * i) = make_uint4(s[4 * i], s[4 * i + 1], s[4 * i + 2], s[4 * i + 3]);
                 } else if (real) {
-                    if (r.from > 0) {
+                    if (a.mode == PAGES_COMMON) {
 #pragma unroll
                         for (int i = 0; i < 32; i++) s[i] = __float_as_uint(__uint_as_float(s[i]) * keep + a.part[o * D + 32 * c + i] * take);
                     }
@@ -480,7 +537,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prompt(const InMode<MODE> a) 
             if (!whole) {
                 rec[ROWS * D + row] = m;
                 rec[ROWS * (D + 1) + row] = l;
-            } else if (real && a.mode == PAGES_COMMON) {
+            } else if (real && a.mode == PAGES_OWN && r.from > 0) {
                 reinterpret_cast<float2 *>(part_sums<D>(a))[o] = make_float2(m, l);
             } else if (real && a.lse) {
                 a.lse[o] = l == 0.f ? -INFINITY : (m - LIFT + log2f(l)) * LN2;
@@ -605,7 +662,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prompt(const InMode<MODE> a) 
         // ---- products -----------------------------------------------------------------------------
         // The warp goes through them together and one lane issues them: a branch of one lane's own keeps the descriptors out
         // of the uniform registers that the instruction takes (2048 tokens over 16384: 404 us, so 433).
-        unsigned runs = 0, it = 0;
+        unsigned runs[2] = {0, 0}, done[2] = {0, 0}, it = 0;  // of each tile: units, keys' tiles
         uint32_t q_at[2], s_at[2], o_at[2];
 #pragma unroll
         for (int t = 0; t < 2; t++) {
@@ -636,32 +693,34 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prompt(const InMode<MODE> a) 
             wait(&sh.k_full[it & 1], it >> 1 & 1);
 #pragma unroll
             for (int t = 0; t < 2; t++) {
-                wait(&sh.q_full[t], runs & 1);
+                if (t == 1 && !g.two) break;
+                wait(&sh.q_full[t], runs[t]++ & 1);
                 tc_fence_after();
                 scores(t, it & 1);
             }
             commit(&sh.k_empty[it & 1]);
-            runs++;
             for (int k = g.t0; k < g.t1; k++, it++) {
                 const int st = it & 1, next = (it + 1) & 1;
                 const uint32_t vb = v_at + st * STAGE;
 #pragma unroll
                 for (int t = 0; t < 2; t++) {
-                    wait(&sh.p_full[t], it & 1);
+                    if (t == 1 && !g.two) break;
+                    const bool last = t == 1 || !g.two;
+                    wait(&sh.p_full[t], done[t]++ & 1);
                     if (t == 0) wait(&sh.v_full[st], it >> 1 & 1);
                     tc_fence_after();
                     if (elect_one()) {
 #pragma unroll
                         for (int i = 0; i < KEYS / 16; i++)
                             mma_tmem(o_at[t], s_at[t] + 8 * i, vb + (i >> 2) * (D * 8) + (i & 3) * 2, product(D), k > g.t0 || i > 0);
-                        if (t == 1) tc_commit(&sh.v_empty[st]);
+                        if (last) tc_commit(&sh.v_empty[st]);
                     }
                     __syncwarp();
                     if (k + 1 < g.t1) {
                         if (t == 0) wait(&sh.k_full[next], (it + 1) >> 1 & 1);
                         if (t == 0) tc_fence_after();
                         scores(t, next);
-                        if (t == 1) commit(&sh.k_empty[next]);
+                        if (last) commit(&sh.k_empty[next]);
                     } else {
                         commit(&sh.o_full[t]);
                     }
@@ -672,6 +731,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prompt(const InMode<MODE> a) 
         commit(&sh.drained);
         if (!mbar_spin(&sh.drained, 0, a.wait_ns)) atomicOr(p.status, PST_TIMEOUT);
     }
+    if (a.mode == PAGES_COMMON) await_previous();
     __syncwarp();
     tc_fence_before();
     __syncthreads();
@@ -682,79 +742,163 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prompt(const InMode<MODE> a) 
 
 }
 
-// The units that crossed a share's border: CTA (c, y) adds up the parts of the unit that
-// began in share c and went on, 8 channels of its 256 rows, in CTA order.
+// The units that crossed a share's border, where there may be many of a few parts each: CTA (c, y) adds up the parts of the
+// unit that began in share c and went on, 8 channels of its 256 rows, in CTA order.
+// (joins: first token, KV head and whether there are pages in common, query rows, parts)
 template <int D, int MODE>
-__global__ void __launch_bounds__(ROWS) join_parts(const InMode<MODE> a) {
+__global__ void __launch_bounds__(ROWS) join_many(const InMode<MODE> a) {
     let_next_start();
     await_previous();
-    const int4 what = reinterpret_cast<const int4 *>(a.joins)[blockIdx.x];  // row of the call, KV head, block, parts
-    const int n = what.w, row = threadIdx.x, tb = ROWS / a.p.G, c = blockIdx.y;
+    const int4 what = reinterpret_cast<const int4 *>(a.joins)[blockIdx.x];
     const PagesView &p = a.p;
-    if (n == 0) return;
-    const PageRow r = attn_row(a, what.x);
-    const int tok = what.z * tb + row / p.G;
-    if (row >= tb * p.G || tok >= r.n) return;
-    const long long o = (static_cast<long long>(r.q0) + tok) * p.Hq + what.y * p.G + row % p.G;
-    float4 *part = reinterpret_cast<float4 *>(a.part + o * D + 8 * c);
+    const int n = what.w, row = threadIdx.x, c = blockIdx.y, tok = row / p.G;
+    if (n == 0 || row >= what.z) return;
+    const long long o = (static_cast<long long>(what.x) + tok) * p.Hq + (what.y & 0xffff) * p.G + row - tok * p.G;
     constexpr int REC = ROWS * (D + 2);
-    auto rec_of = [&](int k) -> const float * { return a.records + (2LL * (blockIdx.x + k) + (k == 0)) * REC; };
-    // the maximum first: then no part waits for another
-    float m = -INFINITY;
-#pragma unroll 8
-    for (int k = 0; k < n; k++) m = fmaxf(m, rec_of(k)[ROWS * D + row]);
-    float2 before = make_float2(-INFINITY, 0.f);
-    if (a.mode == PAGES_OWN && r.from > 0) before = reinterpret_cast<const float2 *>(part_sums<D>(a))[o];
-    m = fmaxf(m, before.x);
-    const float mu = m == -INFINITY ? 0.f : m;
-    float l = 0.f, acc[8];
-#pragma unroll
-    for (int i = 0; i < 8; i++) acc[i] = 0.f;
-    auto add = [&](float4 x, float4 y, float mk, float lk) {
-        const float w = ex2(mk - mu);  // 0 for a part that saw nothing
-        l += lk * w;
-        acc[0] += x.x * w;
-        acc[1] += x.y * w;
-        acc[2] += x.z * w;
-        acc[3] += x.w * w;
-        acc[4] += y.x * w;
-        acc[5] += y.y * w;
-        acc[6] += y.z * w;
-        acc[7] += y.w * w;
+    float2 own = make_float2(-INFINITY, 0.f);
+    if (a.mode == PAGES_COMMON) own = reinterpret_cast<const float2 *>(part_sums<D>(a))[o];
+    float m = -INFINITY, l = 0.f;
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
+    auto add = [&](float mk, float lk, float4 xk, float4 yk) {
+        float keep, take;
+        join_sums(m, l, make_float2(mk, lk), keep, take);
+        x = make_float4(x.x * keep + xk.x * take, x.y * keep + xk.y * take, x.z * keep + xk.z * take, x.w * keep + xk.w * take);
+        y = make_float4(y.x * keep + yk.x * take, y.y * keep + yk.y * take, y.z * keep + yk.z * take, y.w * keep + yk.w * take);
     };
 #pragma unroll 4
     for (int k = 0; k < n; k++) {
-        const float *rec = rec_of(k);
+        const float *rec = a.records + (2LL * (blockIdx.x + k) + (k == 0)) * REC;
         const float4 *v = reinterpret_cast<const float4 *>(rec + (2 * c * ROWS + row) * 4);
-        add(v[0], v[ROWS], rec[ROWS * D + row], rec[ROWS * (D + 1) + row]);
+        add(rec[ROWS * D + row], rec[ROWS * (D + 1) + row], v[0], v[ROWS]);
     }
-    if (a.mode == PAGES_COMMON) {
-        part[0] = make_float4(acc[0], acc[1], acc[2], acc[3]);
-        part[1] = make_float4(acc[4], acc[5], acc[6], acc[7]);
+    float4 *part = reinterpret_cast<float4 *>(a.part + o * D + 8 * c);
+    if (a.mode == PAGES_OWN && what.y >> 16) {
+        part[0] = x;
+        part[1] = y;
         if (c == 0) reinterpret_cast<float2 *>(part_sums<D>(a))[o] = make_float2(m, l);
         return;
     }
-    if (a.mode == PAGES_OWN && r.from > 0) add(part[0], part[1], before.x, before.y);
+    if (own.x == INFINITY) l = 0.f;  // the row holds nothing
+    else if (a.mode == PAGES_COMMON) add(own.x, own.y, part[0], part[1]);
     const float by = l == 0.f ? 0.f : a.out_scale / l;
-    uint32_t w[4];
-#pragma unroll
-    for (int i = 0; i < 4; i++) w[i] = pack2(to16(acc[2 * i] * by, p.bf16), to16(acc[2 * i + 1] * by, p.bf16));
-    *reinterpret_cast<uint4 *>(a.out + o * D + 8 * c) = make_uint4(w[0], w[1], w[2], w[3]);
+    *reinterpret_cast<uint4 *>(a.out + o * D + 8 * c) =
+        make_uint4(pack2(to16(x.x * by, p.bf16), to16(x.y * by, p.bf16)), pack2(to16(x.z * by, p.bf16), to16(x.w * by, p.bf16)),
+                   pack2(to16(y.x * by, p.bf16), to16(y.y * by, p.bf16)), pack2(to16(y.z * by, p.bf16), to16(y.w * by, p.bf16)));
     if (c == 0 && a.lse) a.lse[o] = l == 0.f ? -INFINITY : (m - LIFT + log2f(l)) * LN2;
+}
+
+// The same where there are few units of many parts (64 rows behind 8192 tokens: 8 of 11, 9 us; 12 with the kernel above): a CTA
+// adds up 4 channels of 128 rows of a unit, a quarter of the parts in each quarter of its threads, so that all are on their
+// way at once, always in the same order.
+constexpr int JOIN_WAYS = 4, JOIN_THREADS = TILE * JOIN_WAYS, JOIN_FEW = 16;
+template <int D, int MODE>
+__global__ void __launch_bounds__(JOIN_THREADS) join_few(const InMode<MODE> a, int ctas) {
+    __shared__ int4 todo[PAGES_MAX_CTAS];
+    __shared__ int owner[PAGES_MAX_CTAS], n_todo;
+    __shared__ float4 acc_s[JOIN_WAYS - 1][TILE];
+    __shared__ float2 ml_s[JOIN_WAYS - 1][TILE];
+    let_next_start();
+    await_previous();
+    const PagesView &p = a.p;
+    const int tid = threadIdx.x, lane = tid & 31, way = tid / TILE;
+    if (tid < 32) {
+        int n = 0;
+        int4 what[PAGES_MAX_CTAS / 32];
+#pragma unroll
+        for (int k = 0; k < PAGES_MAX_CTAS / 32; k++)
+            what[k] = 32 * k + lane < ctas ? reinterpret_cast<const int4 *>(a.joins)[32 * k + lane] : make_int4(0, 0, 0, 0);
+#pragma unroll
+        for (int k = 0; k < PAGES_MAX_CTAS / 32; k++) {
+            const unsigned some = __ballot_sync(FULL, what[k].w > 0);
+            if (what[k].w > 0) {
+                const int at = n + __popc(some & ((1u << lane) - 1u));
+                todo[at] = what[k];
+                owner[at] = 32 * k + lane;
+            }
+            n += __popc(some);
+        }
+        if (lane == 0) n_todo = n;
+    }
+    __syncthreads();
+    constexpr int REC = ROWS * (D + 2), SLICES = D / 4 * 2, DEEP = 5;
+    const int items = n_todo * SLICES;
+    for (int item = blockIdx.x; item < items; item += gridDim.x) {
+        const int which = item / SLICES, c = item % (D / 4), row0 = item % SLICES / (D / 4) * TILE, row = row0 + tid % TILE;
+        const int4 what = todo[which];
+        if (row0 >= what.z) continue;  // no rows in the second tile
+        const bool real = row < what.z, first = real && way == 0;
+        const int tok = row / p.G;
+        const long long o = (static_cast<long long>(what.x) + tok) * p.Hq + (what.y & 0xffff) * p.G + row - tok * p.G;
+        float4 *part = reinterpret_cast<float4 *>(a.part + o * D + 4 * c);
+        float2 own = make_float2(-INFINITY, 0.f);
+        float4 own_acc = make_float4(0.f, 0.f, 0.f, 0.f), acc = own_acc;
+        if (a.mode == PAGES_COMMON && first) {
+            own = reinterpret_cast<const float2 *>(part_sums<D>(a))[o];
+            own_acc = *part;
+        }
+        float m = -INFINITY, l = 0.f;
+        auto add = [&](float mk, float lk, float4 x) {
+            float keep, take;
+            join_sums(m, l, make_float2(mk, lk), keep, take);
+            acc = make_float4(acc.x * keep + x.x * take, acc.y * keep + x.y * take, acc.z * keep + x.z * take, acc.w * keep + x.w * take);
+        };
+        for (int k0 = way; k0 < what.w; k0 += DEEP * JOIN_WAYS) {
+            float mk[DEEP], lk[DEEP];
+            float4 x[DEEP];
+#pragma unroll
+            for (int e = 0; e < DEEP; e++) {
+                const int k = k0 + e * JOIN_WAYS;
+                mk[e] = -INFINITY;
+                lk[e] = 0.f;
+                x[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (k >= what.w || !real) continue;
+                const float *rec = a.records + (2LL * (owner[which] + k) + (k == 0)) * REC;
+                mk[e] = rec[ROWS * D + row];
+                lk[e] = rec[ROWS * (D + 1) + row];
+                x[e] = *reinterpret_cast<const float4 *>(rec + (c * ROWS + row) * 4);
+            }
+#pragma unroll
+            for (int e = 0; e < DEEP; e++) add(mk[e], lk[e], x[e]);
+        }
+        if (way > 0) {
+            acc_s[way - 1][tid % TILE] = acc;
+            ml_s[way - 1][tid % TILE] = make_float2(m, l);
+        }
+        __syncthreads();
+        if (first) {
+#pragma unroll
+            for (int w = 0; w < JOIN_WAYS - 1; w++) add(ml_s[w][tid].x, ml_s[w][tid].y, acc_s[w][tid]);
+            if (a.mode == PAGES_OWN && what.y >> 16) {
+                *part = acc;
+                if (c == 0) reinterpret_cast<float2 *>(part_sums<D>(a))[o] = make_float2(m, l);
+            } else {
+                if (own.x == INFINITY) l = 0.f;
+                else if (a.mode == PAGES_COMMON) add(own.x, own.y, own_acc);
+                const float by = l == 0.f ? 0.f : a.out_scale / l;
+                *reinterpret_cast<uint2 *>(a.out + o * D + 4 * c) =
+                    make_uint2(pack2(to16(acc.x * by, p.bf16), to16(acc.y * by, p.bf16)), pack2(to16(acc.z * by, p.bf16), to16(acc.w * by, p.bf16)));
+                if (c == 0 && a.lse) a.lse[o] = l == 0.f ? -INFINITY : (m - LIFT + log2f(l)) * LN2;
+            }
+        }
+        __syncthreads();
+    }
 }
 
 template <int D, int MODE>
 int launch_as(const PagesAttnArgs &a, int grid, cudaStream_t st) {
     const int smem = static_cast<int>(sizeof(Shared<D>)) + 1024;  // room to put it on a 1024-byte boundary
     if (const int e = allow_shared<attn_prompt<D, MODE>>(smem)) return e;
-    if (MODE == PAGES_OWN) {
+    if (MODE == PAGES_COMMON && a.after_few) {
         if (const int e = launch_overlapping(attn_prompt<D, MODE>, dim3(grid), THREADS, smem, st, InMode<MODE>{a})) return e;
     } else {
         attn_prompt<D, MODE><<<grid, THREADS, smem, st>>>(InMode<MODE>{a});
         const cudaError_t e = cudaGetLastError();
         if (e != cudaSuccess) return static_cast<int>(e);
     }
-    return launch_overlapping(join_parts<D, MODE>, dim3(grid, D / 8), ROWS, 0, st, InMode<MODE>{a});
+    // (as many units at most: whole blocks of query rows, and one begun in each row)
+    const long long units = (static_cast<long long>(a.r.n_tok) * a.p.G / ROWS + a.r.n_rows) * a.p.Hkv;
+    if (units <= JOIN_FEW) return launch_overlapping(join_few<D, MODE>, dim3(3 * grid), JOIN_THREADS, 0, st, InMode<MODE>{a}, grid);
+    return launch_overlapping(join_many<D, MODE>, dim3(grid, D / 8), ROWS, 0, st, InMode<MODE>{a});
 }
 template <int MODE>
 int launch_many(const PagesAttnArgs &a, int grid, void *stream) {

@@ -23,14 +23,6 @@ namespace {
 
 constexpr int ST_THREADS = 128, ST_WARPS = ST_THREADS / 32;
 
-// The larger magnitudes (with signs of no meaning), NaN where there is one.
-template <bool BF16>
-__device__ __forceinline__ uint32_t max2_abs(uint32_t a, uint32_t b) {
-    uint32_t r;
-    if (BF16) asm("max.NaN.xorsign.abs.bf16x2 %0, %1, %2;\n" : "=r"(r) : "r"(a), "r"(b));
-    else asm("max.NaN.xorsign.abs.f16x2 %0, %1, %2;\n" : "=r"(r) : "r"(a), "r"(b));
-    return r;
-}
 __device__ __forceinline__ uint32_t hmax2(uint32_t a, uint32_t b) {
     uint32_t r;
     asm("max.f16x2 %0, %1, %2;\n" : "=r"(r) : "r"(a), "r"(b));
@@ -46,12 +38,6 @@ __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
     asm("mul.rn.f16x2 %0, %1, %2;\n" : "=r"(r) : "r"(a), "r"(b));
     return r;
 }
-template <bool BF16>
-__device__ __forceinline__ float2 pair_to_float(uint32_t w) {
-    if (BF16) return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
-    return __half22float2(*reinterpret_cast<const __half2 *>(&w));
-}
-
 // 16 channels of one token.
 struct Block16 {
     uint32_t w[8];  // the values, two a word
