@@ -25,7 +25,7 @@
 // 8-11: a unit's keys into tensor memory, the next one's codes on their way.  Warps 12, 13 and 15: queries
 // into shared memory, a block in turn, four deep.  Warp 14: one thread issues all products, tile by tile
 // in turn, so that one tile's exponentials run beside the other's products.
-// Tensor memory: three products (128 columns each), then the two tiles' keys (D / 2 columns).
+// Tensor memory: two products (128 columns each), then two units' keys (2 tiles of D / 2 columns each).
 #include <type_traits>
 
 #include <cuda_runtime.h>
@@ -38,12 +38,17 @@ namespace {
 
 constexpr int TILE = 128, KEYS = 2 * TILE;  // keys of a tile, of a unit
 constexpr int COLS = 128;                   // query rows of a block, at most
-constexpr int RING = 3;                     // products in tensor memory: a tile's next one is there when its last is weighed
 constexpr int ST = 4;                       // blocks of queries in shared memory
+constexpr int RING = 2, KB = 2;             // products and units' keys in tensor memory (three and one: 3 % slower at 2048 tokens)
 constexpr int THREADS = 512;
 constexpr int UNIT_COST = 32;               // tokens that a unit's beginning and end are worth
 constexpr int MIN_SHARE = 64;               // tokens that make a CTA worth its parts
 
+// A unit that this CTA shares with others: the one that its share begins within, and the one that goes on behind it.
+struct Joint {
+    int first, others;  // the CTA that it begins in, and how many more there are; others < 0: none
+    int row, head, key0, len, old;
+};
 template <int D>
 struct Shared {
     __align__(1024) uint8_t q[ST][COLS * D * 2];
@@ -53,9 +58,10 @@ struct Shared {
     long long first[DQ_PAGES_MAX_ROWS + 1];
     int row[DQ_PAGES_MAX_ROWS], keys[DQ_PAGES_MAX_ROWS];
     long long part[THREADS / 32];
-    uint64_t q_full[ST], q_empty[ST], k_full, k_empty, s_full[RING], s_empty[RING], drained;
+    uint64_t q_full[ST], q_empty[ST], k_full[KB], k_empty[KB], s_full[RING], s_empty[RING], drained;
     uint32_t tmem;
     int last[2];
+    Joint joint[2];
 };
 
 // Unit j of a row and KV head: places UNIT_COST + n - skipped(j); the tokens before that one see none of its keys.
@@ -69,13 +75,16 @@ __device__ __forceinline__ long long units_before(const PageRow &r, int j) {  //
 }
 __device__ __forceinline__ int units_of(const PageRow &r) { return (r.len + KEYS - 1) / KEYS; }
 
+__device__ __forceinline__ long long over(long long n, long long m) {  // n / m, both positive: 32 bits where they are enough
+    return (n | m) >> 32 ? n / m : static_cast<unsigned>(n) / static_cast<unsigned>(m);
+}
 __device__ __forceinline__ long long share(long long n, int m, int k) {
-    const long long q = n / m, rest = n - q * m;
+    const long long q = over(n, m), rest = n - q * m;
     return k * q + (k < rest ? k : rest);
 }
 __device__ __forceinline__ int share_of(long long n, int m, long long x) {
-    const long long q = n / m, rest = n - q * m, ahead = rest * (q + 1);
-    return static_cast<int>(x < ahead ? x / (q + 1) : rest + (x - ahead) / q);
+    const long long q = over(n, m), rest = n - q * m, ahead = rest * (q + 1);
+    return static_cast<int>(x < ahead ? over(x, q + 1) : rest + over(x - ahead, q));
 }
 
 // A CTA's way along its share [c0, c1) of the line: unit by unit, with the blocks [b0, b1) of query rows that are its.
@@ -93,7 +102,7 @@ struct Walk {
         r = weigh_row_at(a, sh.row, sh.keys, sh.first, x, i);
         units = units_of(r);
         const long long all = units_before(r, units), in = x - sh.first[i];
-        head = static_cast<int>(in / all);
+        head = static_cast<int>(over(in, all));
         const long long at = in - head * all;
         int lo = 0, hi = units - 1;
         while (lo < hi) {
@@ -168,8 +177,10 @@ __global__ void __launch_bounds__(THREADS, 1) weigh_many(const PagesWeighArgs a)
             mbar_init(&sh.q_full[i], 1 + 32);  // a warp's stores, 32 threads' copies
             mbar_init(&sh.q_empty[i], 9);
         }
-        mbar_init(&sh.k_full, 4);
-        mbar_init(&sh.k_empty, 1);
+        for (int i = 0; i < KB; i++) {
+            mbar_init(&sh.k_full[i], 4);
+            mbar_init(&sh.k_empty[i], 1);
+        }
         for (int i = 0; i < RING; i++) {
             mbar_init(&sh.s_full[i], 1);
             mbar_init(&sh.s_empty[i], 4);
@@ -314,11 +325,12 @@ __global__ void __launch_bounds__(THREADS, 1) weigh_many(const PagesWeighArgs a)
         auto unpack = [&](const Packed &from) {
             const uint4 (&w)[2][D / 32] = from.w;
             const uint2 (&ks)[2] = from.ks;
-            if (units >= 1) wait(&sh.k_empty, (units + 1) & 1);
+            const int kb = units % KB;
+            if (units >= KB) wait(&sh.k_empty[kb], (units / KB + 1) & 1);
             tc_fence_after();
 #pragma unroll
             for (int t = 0; t < 2; t++) {
-                const uint32_t to = k_tmem + lanes + t * (D / 2);
+                const uint32_t to = k_tmem + lanes + (kb * 2 + t) * (D / 2);
 #pragma unroll
                 for (int i = 0; i < D / 32; i++) {  // 32 channels: two scale blocks, 16 words
                     uint32_t o[16];
@@ -341,7 +353,7 @@ __global__ void __launch_bounds__(THREADS, 1) weigh_many(const PagesWeighArgs a)
             }
             tmem_wait_st();
             tc_fence_before();
-            mbar_arrive(&sh.k_full);
+            mbar_arrive(&sh.k_full[kb]);
             units++;
         };
         // codes one unit ahead, page numbers two
@@ -364,6 +376,13 @@ __global__ void __launch_bounds__(THREADS, 1) weigh_many(const PagesWeighArgs a)
             if (now) unpack(cur);
             if (!more) break;
             cur = nxt;
+        }
+        if (dt < 2) {  // (here, where there is time for it)
+            Walk h(a);
+            h.find(sh, a, dt == 0 ? c0 : c1 - 1, c0, c1);
+            const bool mine = dt == 0 ? h.start < c0 : h.start >= c0 && h.end > c1;
+            const int first = share_of(N, ctas, h.start);
+            sh.joint[dt] = Joint{first, mine ? share_of(N, ctas, h.end - 1) - first : -1, h.r.row, h.head, h.j * KEYS, h.r.len, h.r.len - h.r.n};
         }
     } else if (warp != 14) {
         // ---- queries: three warps take the blocks in turn ----------------------------------------------
@@ -435,7 +454,8 @@ __global__ void __launch_bounds__(THREADS, 1) weigh_many(const PagesWeighArgs a)
         unsigned it = 0, units = 0;
         for (g.find(sh, a, c0, c0, c1); g.start < c1; g.next(sh, a, c0, c1)) {
             if (g.b0 >= g.b1) continue;
-            wait(&sh.k_full, units & 1);
+            const int kb = units % KB;
+            wait(&sh.k_full[kb], units / KB & 1);
             for (int b = g.b0; b < g.b1; b++, it++) {
                 const int st = it % ST;
                 wait(&sh.q_full[st], it / ST & 1);
@@ -445,7 +465,7 @@ __global__ void __launch_bounds__(THREADS, 1) weigh_many(const PagesWeighArgs a)
                     const unsigned n = 2 * it + t, buf = n % RING;
                     if (n >= RING) wait(&sh.s_empty[buf], (n / RING + 1) & 1);
                     tc_fence_after();
-                    const uint32_t ka = k_tmem + t * (D / 2), qb = q_at + st * (COLS * D * 2 / 16);
+                    const uint32_t ka = k_tmem + (kb * 2 + t) * (D / 2), qb = q_at + st * (COLS * D * 2 / 16);
                     if (elect_one()) {
 #pragma unroll
                         for (int i = 0; i < D / 16; i++)
@@ -457,7 +477,7 @@ __global__ void __launch_bounds__(THREADS, 1) weigh_many(const PagesWeighArgs a)
                 if (elect_one()) tc_commit(&sh.q_empty[st]);
                 __syncwarp();
             }
-            if (elect_one()) tc_commit(&sh.k_empty);
+            if (elect_one()) tc_commit(&sh.k_empty[kb]);
             __syncwarp();
             units++;
         }
@@ -473,31 +493,24 @@ __global__ void __launch_bounds__(THREADS, 1) weigh_many(const PagesWeighArgs a)
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;\n" ::"r"(tmem) : "memory");
     }
     // Units that CTAs share: the last one to bring its part (the count releases and acquires the parts) adds all up.
-    // This CTA has at most two: the one that its share begins within, and the one that goes on behind it.
-    if (tid < 64) {
-        const int k = tid >> 5;
+    if (tid < 64 && lane == 0) {
+        const Joint &u = sh.joint[tid >> 5];
         int all = 0;
-        if (lane == 0) {
-            g.find(sh, a, k == 0 ? c0 : c1 - 1, c0, c1);
-            const bool mine = k == 0 ? g.start < c0 : g.start >= c0 && g.end > c1;
-            if (mine) {
-                const int cf = share_of(N, ctas, g.start), others = share_of(N, ctas, g.end - 1) - cf;
-                all = atomic_add_acq_rel_gpu(a.tickets + cf, 1) == others;
-                if (all) a.tickets[cf] = 0;  // for the next call
-            }
-            sh.last[k] = all;
+        if (u.others >= 0) {
+            all = atomic_add_acq_rel_gpu(a.tickets + u.first, 1) == u.others;
+            if (all) a.tickets[u.first] = 0;  // for the next call
         }
+        sh.last[tid >> 5] = all;
     }
     __syncthreads();
     for (int k = 0; k < 2; k++) {
-        if (!sh.last[k] || tid >= KEYS) continue;
-        g.find(sh, a, k == 0 ? c0 : c1 - 1, c0, c1);
-        const int cf = share_of(N, ctas, g.start), n = share_of(N, ctas, g.end - 1) - cf + 1, key = g.j * KEYS + tid;
-        if (key >= g.r.len) continue;
+        const Joint &u = sh.joint[k];
+        const int key = u.key0 + tid;
+        if (!sh.last[k] || tid >= KEYS || key >= u.len) continue;
         float sum = 0.f;
-        for (int i = 0; i < n; i++) sum += __ldcg(a.records + (2LL * (cf + i) + (i == 0)) * KEYS + tid);
-        float *score = scores_of(a, g.r.row, g.head) + key;
-        *score = (key < g.r.len - g.r.n ? *score : 0.f) + sum;
+        for (int i = 0; i <= u.others; i++) sum += __ldcg(a.records + (2LL * (u.first + i) + (i == 0)) * KEYS + tid);
+        float *score = scores_of(a, u.row, u.head) + key;
+        *score = (key < u.old ? *score : 0.f) + sum;
     }
 }
 
