@@ -194,19 +194,20 @@ __global__ void __launch_bounds__(CH_THREADS) choose_kernel(PagesEvictArgs a, in
     }
 }
 
-constexpr int GA_THREADS = 128, GA_WARPS = GA_THREADS / 32;
+constexpr int GA_THREADS = 128, GA_WARPS = GA_THREADS / 32, GA_CTAS = 8;  // CTAs of an SM (6: 2 % slower, 10, with spills: 30 %)
 
 // One CTA row of the grid per (KV head, layer), which walks the pages of all pairs, a block of B = min(P, 64) tokens
 // at a time.  Two blocks ahead the positions are on their way, one ahead the page numbers and scores.
 template <int D, int B>
-__global__ void __launch_bounds__(GA_THREADS, 6) gather_kernel(PagesEvictArgs a) {
+__global__ void __launch_bounds__(GA_THREADS, GA_CTAS) gather_kernel(PagesEvictArgs a) {
     using L = PageBlock<D>;
     constexpr int C = D / 16;
     extern __shared__ __align__(16) uint8_t dyn[];         // [n] src, dst, keep, pages before the pair
     __shared__ __align__(16) uint8_t img[B * D * 9 / 16];  // a block's key codes, then their scales
     __shared__ float red[GA_WARPS];
     __shared__ long long from_s[B];                        // where a token's block is in the pool: -1 none
-    __shared__ int place_s[B], part[GA_WARPS];             // its place there
+    __shared__ int2 place_s[B];                            // its place there, and that of its values' first scale in the block's
+    __shared__ int part[GA_WARPS];
     const PagesView &p = a.p;
     int4 *pair = reinterpret_cast<int4 *>(dyn);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, head = blockIdx.y, layer = blockIdx.z;
@@ -320,7 +321,8 @@ __global__ void __launch_bounds__(GA_THREADS, 6) gather_kernel(PagesEvictArgs a)
         if (tid < B) {
             if (f.id == -2) atomicOr(p.status, PST_TABLE);
             from_s[tid] = f.id < 0 ? -1 : ((pool + f.id) * p.Hkv + head) * p.page_bytes + f.place / B * L::size(B);
-            place_s[tid] = f.place % B;
+            const int t = f.place % B;
+            place_s[tid] = make_int2(t, L::vscale(t, 0));
             if (f.id != -1) scores_of(now.dst)[(now.ord << shift) + now.b0 + tid] = f.score;
         }
         __syncthreads();
@@ -334,26 +336,27 @@ __global__ void __launch_bounds__(GA_THREADS, 6) gather_kernel(PagesEvictArgs a)
             s0[e] = s1[e] = 0;
             if (i >= PAIRS) continue;
             const long long f0 = from_s[2 * pr], f1 = from_s[2 * pr + 1];
+            // (a scale block further on is 8 scales and 4 x 16 bytes of codes)
             if (f0 >= 0) {
-                const int t0 = place_s[2 * pr];
-                v[e] = *reinterpret_cast<const uint4 *>(p.pages + f0 + L::vc(B) + L::vcode(t0, c));
-                s0[e] = p.pages[f0 + L::vs(B) + L::vscale(t0, c)];
+                const int at = place_s[2 * pr].y;
+                v[e] = *reinterpret_cast<const uint4 *>(p.pages + f0 + (L::vc(B) + (at >> 1) * 16 + c * 64));
+                s0[e] = p.pages[f0 + (L::vs(B) + at + c * 8)];
             }
             if (f1 >= 0) {
-                const int t1 = place_s[2 * pr + 1];
-                w[e] = *reinterpret_cast<const uint4 *>(p.pages + f1 + L::vc(B) + L::vcode(t1, c));
-                s1[e] = p.pages[f1 + L::vs(B) + L::vscale(t1, c)];
+                const int at = place_s[2 * pr + 1].y;
+                w[e] = *reinterpret_cast<const uint4 *>(p.pages + f1 + (L::vc(B) + (at >> 1) * 16 + c * 64));
+                s1[e] = p.pages[f1 + (L::vs(B) + at + c * 8)];
             }
         }
 #pragma unroll
         for (int e = 0; e < NK; e++) {
             const int i = tid + e * GA_THREADS, u = i / (D / 32);
             k[e] = make_uint4(0, 0, 0, 0);
-            if (i < KEYS && from_s[u] >= 0) k[e] = *reinterpret_cast<const uint4 *>(p.pages + from_s[u] + place_s[u] * (D / 2) + 16 * (i % (D / 32)));
+            if (i < KEYS && from_s[u] >= 0) k[e] = *reinterpret_cast<const uint4 *>(p.pages + from_s[u] + (place_s[u].x * (D / 2) + 16 * (i % (D / 32))));
         }
         if (tid < SCALES) {  // four scales
             const int u = tid / (D / 64);
-            if (from_s[u] >= 0) ks = *reinterpret_cast<const uint32_t *>(p.pages + from_s[u] + L::ks(B) + place_s[u] * C + 4 * (tid % (D / 64)));
+            if (from_s[u] >= 0) ks = *reinterpret_cast<const uint32_t *>(p.pages + from_s[u] + (L::ks(B) + place_s[u].x * C + 4 * (tid % (D / 64))));
         }
         const bool last = left <= B;
         look(next, j, page_next, f);
@@ -363,17 +366,18 @@ __global__ void __launch_bounds__(GA_THREADS, 6) gather_kernel(PagesEvictArgs a)
         page_next = number(next);
 #pragma unroll
         for (int e = 0; e < NV; e++) {
-            const int i = tid + e * GA_THREADS, in = i % (4 * C), c = in >> 2, pr = 4 * (i / (4 * C)) + (in & 3);
+            const int i = tid + e * GA_THREADS, pr = 4 * (i / (4 * C)) + (i & 3);
             if (i >= PAIRS || 2 * pr >= n || !blk) continue;
-            uint4 *to = reinterpret_cast<uint4 *>(blk + L::vc(B) + L::vcode(2 * pr, c));
-            uint8_t *to_s = blk + L::vs(B) + L::vscale(2 * pr, c);
-            int odd = place_s[2 * pr + 1] & 1;
+            // (the bytes' order is the items')
+            uint4 *to = reinterpret_cast<uint4 *>(blk + L::vc(B)) + i;
+            uint8_t *to_s = blk + L::vs(B) + 2 * i;
+            int odd = place_s[2 * pr + 1].y & 1;
             if (2 * pr + 1 >= n) {  // the place behind the last token stays as it is
                 w[e] = *to;
                 s1[e] = to_s[1];
                 odd = 1;
             }
-            const int sv = 4 * (place_s[2 * pr] & 1), sw = 4 * odd;
+            const int sv = 4 * (place_s[2 * pr].y & 1), sw = 4 * odd;
             auto both = [&](uint32_t x, uint32_t y) { return (x >> sv & 0x0f0f0f0fu) | (y >> sw & 0x0f0f0f0fu) << 4; };
             *to = make_uint4(both(v[e].x, w[e].x), both(v[e].y, w[e].y), both(v[e].z, w[e].z), both(v[e].w, w[e].w));
             *reinterpret_cast<uint16_t *>(to_s) = static_cast<uint16_t>(s0[e] | s1[e] << 8);
@@ -449,7 +453,7 @@ __global__ void __launch_bounds__(GA_THREADS, 6) gather_kernel(PagesEvictArgs a)
 
 template <int D, int B>
 int launch_gather(const PagesEvictArgs &a, int num_sms, cudaStream_t st) {
-    const long long units = static_cast<long long>(a.p.Hkv) * a.p.n_layers, room = 6LL * num_sms;
+    const long long units = static_cast<long long>(a.p.Hkv) * a.p.n_layers, room = static_cast<long long>(GA_CTAS) * num_sms;
     const dim3 grid(static_cast<unsigned>(units < room ? room / units : 1), a.p.Hkv, a.p.n_layers);
     return launch_overlapping(gather_kernel<D, B>, grid, GA_THREADS, a.n * 16, st, a);
 }
