@@ -21,7 +21,9 @@ namespace dq {
 namespace {
 
 constexpr int CHUNK = 32;
-constexpr int MANY_ROWS = 32;  // query rows of a row and KV head beyond which the tensor-core kernel takes over
+// Query rows of a row and KV head beyond which the tensor-core kernel takes over (8 rows of 32768 tokens, 8 KV heads; this kernel
+// against that: 32 query rows 128 / 210 us, 48 187 / 210, 64 246 / 209; 1 row of 8192: 48 14.0 / 15.6, 64 17.2 / 15.6).
+constexpr int MANY_ROWS = 48;
 
 __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
     uint32_t r;
@@ -200,8 +202,6 @@ __global__ void __launch_bounds__(32 * WARPS) weigh_chunks(PagesWeighArgs a) {
         float *scores = scores_of(a, r.row, head);
         const int rows = r.n * p.G, old = r.len - r.n, mine = (lane >> 2) + 8 * (lane & 3);
         for (int row0 = 0; row0 < rows; row0 += 8 * NT) {
-            Queries<D, NT> q;
-            q.load(a, r, head, row0);
             const int least = old + row0 / p.G;
             auto load = [&](Keys<D> &k, float &s, int c) {
                 const int at = c * CHUNK;
@@ -231,7 +231,9 @@ __global__ void __launch_bounds__(32 * WARPS) weigh_chunks(PagesWeighArgs a) {
             };
             Keys<D> cur, nxt;
             float was, next_was;
-            load(cur, was, t0);
+            load(cur, was, t0);  // (on its way while the queries are put together)
+            Queries<D, NT> q;
+            q.load(a, r, head, row0);
             for (int c = t0; c < t1; c++) {
                 if (c + 1 < t1) load(nxt, next_was, c + 1);
                 const float got = weigh_chunk<D, NT>(cur, q, c * CHUNK, least);
@@ -263,6 +265,7 @@ int launch_pages_weigh(PagesWeighArgs a, int num_sms, void *stream) {
         a.over = 0;
         a.most = MANY_ROWS;
     }
+    // two n tiles share the conversions of a chunk (16 query rows: 67 us, with one tile 116; four tiles: no less at 32 than two)
     if (rows <= 8) return a.p.d == 128 ? launch_as<128, 1>(a, num_sms, st) : launch_as<64, 1>(a, num_sms, st);
     return a.p.d == 128 ? launch_as<128, 2>(a, num_sms, st) : launch_as<64, 2>(a, num_sms, st);
 }
