@@ -222,7 +222,9 @@ dq_status dq_pages_cross(const dq_pages_config *cfg, const dq_pages_buffers *buf
  *            each row the tokens that its group has in common and a table row that holds
  *            them.  Common are the whole leading pages that the tables of all rows of the
  *            group name alike and that every new token sees all of; none in a group of one
- *            row, or for a row in no group.  Rows that hold or bring nothing do not count.
+ *            row, or for a row in no group, and, where `always` is 0, none where reading them
+ *            once would save less time than it costs (an estimate from the group's rows, new
+ *            tokens and common tokens).  Rows that hold or bring nothing do not count.
  *            It stays true until a row of the call is resized, forked into, moved by
  *            dq_pages_compact or brings other tokens: one plan serves all layers.
  * dq_pages_shared gives what dq_pages_attention of the same rows does (to rounding: the
@@ -235,7 +237,7 @@ dq_status dq_pages_cross(const dq_pages_config *cfg, const dq_pages_buffers *buf
  * Errors: DQ_EINVAL, DQ_EALIGN, DQ_ECUDA.
  */
 dq_status dq_pages_common(const dq_pages_config *cfg, const dq_pages_buffers *bufs, const int *rows, const int *cu, int n_rows,
-                          const int *groups, int n_groups, int *plan, void *stream);
+                          const int *groups, int n_groups, int always, int *plan, void *stream);
 dq_status dq_pages_shared_bytes(const dq_pages_config *cfg, int n_tok, size_t *bytes); /* host only */
 dq_status dq_pages_shared(const dq_pages_config *cfg, const dq_pages_buffers *bufs, int layer, const void *q, long long q_tok_stride,
                           long long q_head_stride, void *out, float *lse, const int *rows, const int *cu, int n_rows, int n_tok,

@@ -276,7 +276,7 @@ dq_status dq_pages_cross(const dq_pages_config *cfg, const dq_pages_buffers *buf
 }
 
 dq_status dq_pages_common(const dq_pages_config *cfg, const dq_pages_buffers *bufs, const int *rows, const int *cu, int n_rows,
-                          const int *groups, int n_groups, int *plan, void *stream) {
+                          const int *groups, int n_groups, int always, int *plan, void *stream) {
     dq::PagesCommonArgs a{};
     dq_status s = view(cfg, bufs, -1, false, a.p);
     if (s != DQ_OK) return s;
@@ -285,6 +285,7 @@ dq_status dq_pages_common(const dq_pages_config *cfg, const dq_pages_buffers *bu
     if ((s = check_groups(groups, n_groups, n_rows, plan)) != DQ_OK) return s;
     a.groups = groups;
     a.n_groups = n_groups;
+    a.always = always;
     a.plan = plan;
     return launched(dq::launch_pages_common(a, stream), "common launch");
 }

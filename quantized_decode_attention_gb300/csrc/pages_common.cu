@@ -12,10 +12,28 @@
 namespace dq {
 namespace {
 
-constexpr int CO_THREADS = 512, CO_WARPS = CO_THREADS / 32;
+constexpr float BYTES_US = 5e6f, UNIT_US = 1.9f, COST_US = 20.f, SMS = 152.f;
+constexpr int CO_THREADS = 1024, CO_WARPS = CO_THREADS / 32;
+
+// Whether a group's `keys` common tokens, for `rows` rows with `tokens` new ones, are worth a launch of their own: the
+// time of each row's reading them (the cache at 5 TB/s; for many query rows the products, 1.9 us a unit of 256 query
+// rows and 128 keys on an SM), less that of one reading, against the launch's and the join's, which the groups share.
+// A choice of speed alone: it takes all groups to be like this one.  Measured, attention with nothing common / in
+// common, us (8 KV heads of 128, 4 query heads each): 8 rows behind 2048 tokens 17.3 / 22.2, 8192 25.8 / 29.4, 32768
+// 61 / 53.5; 64 rows behind 512 21.8 / 27.2, 1024 28.7 / 27.4, 2048 42.8 / 28.8, 8192 112 / 38; 8 groups of 8 behind
+// 512 19.7 / 19.7, 2048 40.6 / 37.7, 8192 110 / 87; rows of 16 tokens: 4 behind 8192 45 / 55.6, 8 behind 2048
+// 36.5 / 54, 32 behind 2048 80 / 70, 16384 383 / 154.
+__device__ __forceinline__ bool pays(const PagesCommonArgs &a, int rows, int tokens, int keys) {
+    const PagesView &p = a.p;
+    const float q = static_cast<float>(tokens) * p.G, heads = static_cast<float>(p.Hkv) * keys;  // query rows; keys of all heads
+    float saved;  // us
+    if (q <= 32.f * rows) saved = (rows - 1) * heads * (p.d * 9 / 8) / BYTES_US;
+    else saved = (rows * ceilf(q / rows / 256.f) - ceilf(q / 256.f)) * (heads / 128.f) * UNIT_US / SMS;
+    return saved * a.n_groups > COST_US;
+}
 
 __global__ void __launch_bounds__(CO_THREADS) common_kernel(PagesCommonArgs a) {
-    __shared__ int least, leader, count, row_s[DQ_PAGES_MAX_ROWS];
+    __shared__ int least, leader, count, tokens, row_s[DQ_PAGES_MAX_ROWS];
     const PagesView &p = a.p;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, n_rows = a.r.n_rows;
     const int g0 = a.groups ? a.groups[blockIdx.x] : 0, g1 = a.groups ? a.groups[blockIdx.x + 1] : n_rows;
@@ -27,7 +45,7 @@ __global__ void __launch_bounds__(CO_THREADS) common_kernel(PagesCommonArgs a) {
     if (tid == 0) {
         least = p.M;
         leader = n_rows;
-        count = 0;
+        count = tokens = 0;
     }
     __syncthreads();
     // (places of the group that hold nothing or bring nothing do not count)
@@ -39,6 +57,7 @@ __global__ void __launch_bounds__(CO_THREADS) common_kernel(PagesCommonArgs a) {
             atomicMin(&least, r.len > r.n ? (r.len - r.n) / p.P : 0);
             atomicMin(&leader, i);
             atomicAdd(&count, 1);
+            atomicAdd(&tokens, r.n);
         }
     }
     __syncthreads();
@@ -65,7 +84,8 @@ __global__ void __launch_bounds__(CO_THREADS) common_kernel(PagesCommonArgs a) {
         }
         __syncthreads();
     }
-    const int2 what = count > 1 ? make_int2(least * p.P, first) : make_int2(0, 0);
+    const bool share = count > 1 && (a.always || pays(a, count, tokens, least * p.P));
+    const int2 what = share ? make_int2(least * p.P, first) : make_int2(0, 0);
     for (int i = g0 + tid; i < g1; i += CO_THREADS) plan[i] = what;
     // rows of the call that are in no group
     if (blockIdx.x == 0)

@@ -116,6 +116,7 @@ struct PagesCommonArgs {
     PagesRows r;
     const int *groups;
     int n_groups;
+    int always;           // also where it does not pay
     int *plan;
 };
 struct PagesWeighArgs {

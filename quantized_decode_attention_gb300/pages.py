@@ -40,7 +40,7 @@ def _load():
         L.dq_pages_attention.argtypes = [cfg, buf, I, P, LL, LL, P, P, P, P, I, I, I, P, I, C.c_float, P]
         L.dq_pages_select.argtypes = [cfg, buf, I, P, LL, LL, P, I, P, I, I, I, P]
         L.dq_pages_cross.argtypes = [cfg, buf, I, P, LL, LL, P, P, P, P, I, I, I, C.c_float, P]
-        L.dq_pages_common.argtypes = [cfg, buf, P, P, I, P, I, P, P]
+        L.dq_pages_common.argtypes = [cfg, buf, P, P, I, P, I, I, P, P]
         L.dq_pages_shared_bytes.argtypes = [cfg, I, C.POINTER(C.c_size_t)]
         L.dq_pages_shared.argtypes = [cfg, buf, I, P, LL, LL, P, P, P, P, I, I, I, P, I, I, P, P, C.c_float, P]
         L.dq_pages_weigh.argtypes = [cfg, buf, I, P, LL, LL, P, P, I, P, P, I, I, I, C.c_float, P]
@@ -252,13 +252,14 @@ class PagePool:
         self._call("cross", stream, layer, qp, qt, qh, op, None if lse is None else self._lse(lse, n), *self._rows(rows, cu, n, max_new),
                    self._scale if sm_scale is None else sm_scale)
 
-    def common(self, plan, groups=None, rows=None, cu=None, stream=None):
+    def common(self, plan, groups=None, rows=None, cu=None, always=False, stream=None):
         """What the rows of each group have in common (whole leading pages that all of them hold and all their new tokens
         see), into plan int32 [n_rows, 2] for shared(), in every layer.  groups: int32 [n_groups + 1], where each group's
-        rows begin among the call's (None: one group of all)."""
+        rows begin among the call's (None: one group of all).  Where reading it once would cost more time than it saves,
+        nothing is taken to be common, unless always is set."""
         n = plan.shape[0]
         g, n_groups, pp = self._groups(groups, plan, n)
-        self._call("common", stream, self._ints(rows, "rows", n), None if cu is None else self._ints(cu, "cu", n + 1), n, g, n_groups, pp)
+        self._call("common", stream, self._ints(rows, "rows", n), None if cu is None else self._ints(cu, "cu", n + 1), n, g, n_groups, int(always), pp)
 
     def shared_scratch(self, n_tok):
         """The buffer that shared() takes for calls of up to n_tok tokens."""

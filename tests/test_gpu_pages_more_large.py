@@ -154,7 +154,7 @@ def test_calls_on_another_device_are_refused_and_streams_are_taken_as_numbers():
     q = f.queries([1, 1])
     out, plan, scratch = torch.empty_like(q), torch.empty(2, 2, dtype=torch.int32, device="cuda"), f.pool.shared_scratch(2)
     torch.cuda.synchronize()
-    f.pool.common(plan, stream=s.cuda_stream)
+    f.pool.common(plan, always=True, stream=s.cuda_stream)
     f.pool.shared(0, q, out, plan, scratch, stream=s.cuda_stream)
     f.pool.check(s.cuda_stream)
     want, _, tol, _ = f.expect(q, [1, 1])

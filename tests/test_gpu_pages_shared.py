@@ -69,6 +69,8 @@ class Forked(Filled):
             at += n
         return out, lse, tol * (1 + torch.finfo(_dt(self.dtype)).eps / 2), ltol
 
+    always = True
+
     def plan(self, counts, rows=None, bounds=None):
         """What common() found, as a list of (tokens, row)."""
         import torch
@@ -76,7 +78,7 @@ class Forked(Filled):
         plan = torch.full((n, 2), 77, dtype=torch.int32, device="cuda")
         one = all(x == 1 for x in counts)
         self.pool.common(plan, groups=None if bounds is None else _i32(bounds), rows=None if rows is None else _i32(rows),
-                         cu=None if one else _cu(counts))
+                         cu=None if one else _cu(counts), always=self.always)
         return plan
 
     def attend(self, q, counts, rows=None, sel=None, scale=None, stream=None, pool=None):
@@ -122,6 +124,21 @@ def test_several_tokens(d, G, P, dtype):
     for counts in ([3, 2, 1, 5, 0, 3, 2, 1, 1, 4, 7, 1, 2, 2], [9, 80, 70, 130, 1, 2, 5, 2, 3, 1, 90, 1, 40, 30],
                    [2, 80 + P, 1, 150, 150, 3, 5, 2, 1, 1, 0, 1, 33, 34]):
         f.verify(f.queries(counts), counts)
+
+
+def test_common_only_where_it_pays():
+    """Left to itself, common() takes much that many rows share and leaves little that few do: its estimate is far from its
+    limit of 20 us on both sides (8 KV heads of 128, 144 bytes each of a key and value: 63 x 8 x 4096 x 144 / 5e6 us = 59, twice
+    for two groups; 2 x 8 x 640 x 144 / 5e6 = 0.3)."""
+    f = Forked([(4096, [1 + i % 5 for i in range(64)]), (640, [3, 9, 1])], n_kv_heads=8, n_q_heads=32, n_pages=300, max_pages_per_seq=70)
+    n = [1] * 67
+    assert f.plan(n, None, f.bounds)[:, 0].tolist() == [4096] * 64 + [640] * 3
+    f.always = False
+    assert f.plan(n, None, f.bounds)[:, 0].tolist() == [4096] * 64 + [0] * 3
+    f.verify(f.queries(n), n)
+    n = [1 + i % 5 for i in range(64)] + [2, 9, 1]
+    assert f.plan(n, None, f.bounds)[:, 0].tolist() == [4096] * 64 + [0] * 3
+    f.verify(f.queries(n), n)
 
 
 def test_a_big_group_over_a_long_beginning():
@@ -227,7 +244,7 @@ def test_the_same_every_time_and_in_graphs_on_two_streams():
         o, plan, scratch = torch.empty_like(q[i]), torch.empty(n, 2, dtype=torch.int32, device="cuda"), f.pool.shared_scratch(n)
         g = torch.cuda.CUDAGraph()
         with torch.cuda.graph(g, stream=s[i]):
-            handles[i].common(plan)
+            handles[i].common(plan, always=True)
             for _ in range(3):
                 handles[i].shared(0, q[i], o, plan, scratch)
         graphs.append(g)

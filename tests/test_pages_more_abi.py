@@ -6,7 +6,7 @@ import pytest
 from test_pages_abi import EALIGN, EINVAL, EUNSUPPORTED, Q, bufs, cfg, lib, refused, with_  # noqa: F401
 
 CROSS = (0, Q, 4096, 128, Q, None, None, None, 2, 2, 1, 0.1, None)
-COMMON = (None, None, 2, None, 1, Q, None)
+COMMON = (None, None, 2, None, 1, 0, Q, None)
 SHARED = (0, Q, 4096, 128, Q, None, None, None, 2, 2, 1, None, 1, 2, Q, Q, 0.1, None)
 WEIGH = (0, Q, 4096, 128, Q, Q, 64, None, None, 2, 2, 1, 0.1, None)
 EVICT = (Q, 64, Q, Q, 2, 1, 1, None)
@@ -34,7 +34,7 @@ def test_refused_pools(lib, name, args):  # noqa: F811
     ("dq_pages_common", with_(COMMON, _2=0), EINVAL), ("dq_pages_common", with_(COMMON, _2=7), EINVAL),
     ("dq_pages_common", with_(COMMON, _4=0), EINVAL), ("dq_pages_common", with_(COMMON, _4=2), EINVAL),       # two groups, and no groups
     ("dq_pages_common", with_(COMMON, _3=Q, _4=3), EINVAL), ("dq_pages_common", with_(COMMON, _3=Q + 2), EALIGN),
-    ("dq_pages_common", with_(COMMON, _5=None), EINVAL), ("dq_pages_common", with_(COMMON, _5=Q + 4), EALIGN),
+    ("dq_pages_common", with_(COMMON, _6=None), EINVAL), ("dq_pages_common", with_(COMMON, _6=Q + 4), EALIGN),
     ("dq_pages_common", with_(COMMON, _1=Q + 1), EALIGN), ("dq_pages_common", with_(COMMON, _0=Q + 1), EALIGN),
     ("dq_pages_shared", with_(SHARED, _0=-1), EINVAL), ("dq_pages_shared", with_(SHARED, _1=None), EINVAL),
     ("dq_pages_shared", with_(SHARED, _2=4100), EALIGN), ("dq_pages_shared", with_(SHARED, _4=Q + 8), EALIGN),
