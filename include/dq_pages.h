@@ -21,6 +21,10 @@
  *   dq_pages_resize   each row gets room for its new token(s)
  *   per layer: dq_pages_append, then dq_pages_attention (or dq_pages_select and
  *   dq_pages_attention over what it chose)
+ * Beside it: dq_pages_cross attends to rows that the queries are no tokens of (an
+ * encoder's states), dq_pages_common and dq_pages_shared are for rows that begin with
+ * the same pages (one prompt, many answers), dq_pages_weigh and dq_pages_evict hold rows
+ * to a number of tokens by what attention makes of them.
  *
  * Conventions (beside those of dq.h: device pointers, 16-byte alignment, status
  * codes, work enqueued on `stream`, argument errors found on the host before
@@ -95,9 +99,9 @@ typedef struct {
  * seq_len int32 [max_seqs], 0 at the start.
  * refs    int32 [n_pages]: rows that hold the page; 0 = free.  0 at the start.
  * status  16 bytes, 0 at the start.
- * workspace: 0 at the start, used by every call but dq_pages_append, _read, _fork
- *         and _select: 12 bytes a page and some 43 MB for the parts that attention's
- *         CTAs join.  Every call leaves it fit for the next one, a call whose wait
+ * workspace: 0 at the start, used by every call but dq_pages_append, _read, _fork,
+ *         _select and _common: 12 bytes a page and some 45 MB for the parts that CTAs
+ *         of attention (of every kind) and of dq_pages_weigh join.  Every call leaves it fit for the next one, a call whose wait
  *         ran out too.
  */
 typedef struct {
@@ -293,7 +297,9 @@ dq_status dq_pages_select(const dq_pages_config *cfg, const dq_pages_buffers *bu
  * Scores behind seq_len are left as they are, those of rows that bring nothing too.  A query
  * whose lse is -inf adds nothing.  `rows` names a row that brings tokens once: otherwise its
  * scores are left as they are (DQ_EINVAL from dq_pages_check).  Precision: as
- * dq_pages_attention's logits; the sums are fp32 in an order that is the same every time.
+ * dq_pages_attention's logits (more than 48 query rows of a row and KV head are multiplied as
+ * they are, without a scaling by a power of two: exact for bf16 channels of 2^-100 to 2^100);
+ * the sums are fp32 in an order that is the same every time.
  *
  * dq_pages_evict, for all layers at once: row dst[i], of k = its seq_len tokens, which a
  * dq_pages_resize has given room, receives for each layer and KV head k tokens of row

@@ -569,9 +569,14 @@ __global__ void __launch_bounds__(32 * NW, 1) attn_chunks(const InMode<MODE> a) 
             for (long long k = tid; k < static_cast<long long>(r.n) * p.Hq; k += 32 * NW) a.lse[static_cast<long long>(r.q0) * p.Hq + k] = -INFINITY;
     }
     // this CTA's places [c0, c1), this warp's [w0, w1)
-    const int room = a.mode == PAGES_OWN ? own_ctas(N, gridDim.x) : (a.mode == PAGES_COMMON ? sms_left<32 * NW>(a, own, sh.part) : gridDim.x);
+    // (the compiler's schedule of the loop below hangs on this: with one bound for all kinds of launch 8 rows of 4 to 8 tokens
+    // over 32768 take 5 % longer)
     int ctas = N / MIN_PLACES;
-    ctas = ctas < 1 ? 1 : (ctas > room ? room : ctas);
+    ctas = ctas < 1 ? 1 : (ctas > static_cast<int>(gridDim.x) ? gridDim.x : ctas);
+    if (a.mode == PAGES_OWN || a.mode == PAGES_COMMON) {
+        const int room = a.mode == PAGES_OWN ? own_ctas(N, gridDim.x) : sms_left<32 * NW>(a, own, sh.part);
+        ctas = ctas > room ? room : ctas;
+    }
     if (N == 0 || static_cast<int>(blockIdx.x) >= ctas) {
         if (a.mode == PAGES_COMMON) await_previous();
         return;

@@ -12,8 +12,12 @@
 // gather_kernel, a CTA a page of dst at a time: positions, page numbers, then 16-byte
 // pieces straight from the source pages to the destination's (keys and scales as they are,
 // values two tokens a byte), the scores over the positions, and the page's summary.  The
-// pages are independent, so that it is bound by memory: what it reads is scattered, two
-// tokens' halves of a 16-byte piece of values often in different sectors.
+// pages are independent.  What it reads is scattered: kept tokens are rarely neighbours, and a
+// value's sector of 32 bytes holds 4 tokens' channels (keeping an eighth reads 289 MB where 145 are kept); where
+// nearly all are kept it is instructions, the nibbles of values and the summaries, that count (60 % of the issue slots).
+//
+// 16 rows of 4160 tokens to 4096, two layers of 8 KV heads, head_dim 128: 14 us to choose, 70 to gather (the resizes of a
+// caller beside them: 105 in all); four prompts of 9 to 16 k to 2048, eight layers: 28 and 55 (128 in all).
 #include <cuda_runtime.h>
 
 #include "pages.cuh"

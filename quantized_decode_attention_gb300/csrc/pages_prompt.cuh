@@ -5,7 +5,7 @@
 // out = (sum p v) / (sum p).  4 D products and one exponential for each (query, key)
 // pair: the kernel is bound by the tensor cores and, nearly as much, by the exponentials
 // and their conversions.  2048 new tokens over 16384 (32 / 8 heads, head_dim 128) take
-// 404 us, 1.28 PFLOP/s.
+// 400 us, 1.29 PFLOP/s.
 //
 // Work.  A unit is 256 query rows (256 / G tokens with their G query heads) of one row and
 // KV head, in two tiles of 128.  It walks the keys that its last token sees, 128 at a

@@ -6,8 +6,8 @@
 // products and one exponential for each (query, key) pair: bound by the tensor cores and
 // the exponentials alike.
 //
-// 2048 new tokens over 16384 (32 / 8 heads, head_dim 128) take 218 us, 1.18 PFLOP/s; the last 64 queries of
-// four prompts of 9 to 16 k tokens 50 us.
+// 2048 new tokens over 16384 (32 / 8 heads, head_dim 128) take 208 us, 1.24 PFLOP/s; the last 64 queries of
+// four prompts of 9 to 16 k tokens 48 us.
 //
 // Keys are the rows of the product, so that a key's sum is one thread's: nothing is summed
 // over lanes.  Their operand lies in tensor memory (a thread unpacks a key's codes and
