@@ -262,10 +262,12 @@ int launch_pages_weigh(PagesWeighArgs a, int num_sms, void *stream) {
     const int rows = a.r.max_new * a.p.G;
     a.over = 0;
     a.most = 0x7fffffff;
-    if (rows > MANY_ROWS) {  // rows with many query rows on the tensor cores, the others of a mixed batch here
-        a.over = a.r.n_rows == 1 ? 0 : MANY_ROWS;
+    if (rows > MANY_ROWS) {  // rows with many query rows on the tensor cores, the others of a mixed batch here (where rows have
+        // many on average, all there: an idle launch costs 3 us)
+        const bool mixed = a.r.n_rows > 1 && static_cast<long long>(a.r.n_tok) * a.p.G <= static_cast<long long>(MANY_ROWS) * a.r.n_rows;
+        a.over = mixed ? MANY_ROWS : 0;
         if (const int e = launch_pages_weigh_many(a, num_sms < PAGES_MAX_CTAS ? num_sms : PAGES_MAX_CTAS, stream)) return e;
-        if (a.r.n_rows == 1) return 0;
+        if (!mixed) return 0;
         a.over = 0;
         a.most = MANY_ROWS;
     }

@@ -44,6 +44,8 @@ def test_many_queries(d, G, P, dtype):
     f = Encoded(lens, seed=G, n_kv_heads=2, n_q_heads=2 * G, head_dim=d, page_size=P, dtype=dtype, n_pages=120, max_pages_per_seq=45)
     counts = [150, 90, 70, 33, 1, 0, 64]
     f.verify(f.queries(counts), counts)
+    more = [70 if G == 1 else 33, 1, 0, 2, 1, 3, 1, 1, 0, 1, 1, 1, 2, 1]  # few on average: they have a launch of their own
+    f.verify(f.queries(more), more, [1, 0, 6, 2, 5, 3, 4, 6, 1, 1, 0, 5, 6, 2])
     f.verify(f.queries([300]), [300], [1])
     f.verify(f.queries([65]), [65], [2])
     f.verify(f.queries([40, 66]), [40, 66], [1, 1])

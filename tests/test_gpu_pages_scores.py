@@ -79,6 +79,7 @@ def test_weights_of_several_tokens(d, G, P, dtype):
     f.verify_weights([2, 1, 3, 1, 1, 2, 4], amp=2.0)
     f.verify_weights([200, 3, 64, 130, 1, 77, 257], scale=-0.05)
     f.verify_weights([33, 0, 0, 40], [6, 0, 1, 3])
+    f.verify_weights([1, 2, 0, 1, 0, 1, max(60, 48 // G + 1)])  # G 1 and 2: few on average, with a launch of their own
 
 
 def test_weights_of_long_rows():
