@@ -10,13 +10,13 @@
 // equal shares, one for each warp.  A lane (g, t) = (lane / 4, lane % 4) loads its operands of
 // mma.sync m16n8k16 straight from the page (D / 4 channels at t D / 4 of tokens g and g + 8,
 // K [16 tokens x 16 channels] . Q^T, 8 query rows in the n of 8), the next chunk's while it
-// works on this one's.  Every score is one thread's: nothing is joined, and the order of its
-// sum is fixed.  More than 8 NT query rows go by blocks, the later ones adding to what the
-// first stored.
+// works on this one's, and the page number after that (16 rows of 4160: 15.3 -> 13.8 us).
+// Every score is one thread's: nothing is joined, and the order of its sum is fixed.  More
+// than 8 NT query rows go by blocks, the later ones adding to what the first stored.
 //
 // Bound by the lengths, the table and the first codes one after the other where rows are short, by
 // mma.sync and the conversions of codes where they are long (16 rows of 4160 tokens, 32 / 8 heads, head_dim 128,
-// one query each: 15.3 us, 43 MB; 8 of 32768 with 2: 67 us, 2.5 TB/s).
+// one query each: 13.8 us, 43 MB; 8 of 32768 with 4: 65 us, 2.6 TB/s).
 #include <cuda_runtime.h>
 
 #include "pages_weigh.cuh"
@@ -26,7 +26,7 @@ namespace {
 
 constexpr int CHUNK = 32;
 // Query rows of a row and KV head beyond which the tensor-core kernel takes over (8 rows of 32768 tokens, 8 KV heads; this kernel
-// against that: 32 query rows 128 / 210 us, 48 187 / 210, 64 246 / 209; 1 row of 8192: 48 14.0 / 15.6, 64 17.2 / 15.6).
+// against that: 32 query rows 124 / 208 us, 48 181 / 208, 64 238 / 208; 1 row of 8192: 48 14.2 / 15.6, 64 17.3 / 15.6).
 constexpr int MANY_ROWS = 48;
 
 __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
@@ -185,7 +185,7 @@ __device__ __forceinline__ float weigh_chunk(const Keys<D> &k, const Queries<D, 
 constexpr int WARPS = 8;
 
 template <int D, int NT>
-__global__ void __launch_bounds__(32 * WARPS) weigh_chunks(PagesWeighArgs a) {
+__global__ void __launch_bounds__(32 * WARPS, 2) weigh_chunks(PagesWeighArgs a) {
     __shared__ long long first[DQ_PAGES_MAX_ROWS + 1], part[WARPS];
     __shared__ int row_s[DQ_PAGES_MAX_ROWS], keys_s[DQ_PAGES_MAX_ROWS];
     const PagesView &p = a.p;
@@ -196,6 +196,7 @@ __global__ void __launch_bounds__(32 * WARPS) weigh_chunks(PagesWeighArgs a) {
     __syncthreads();
     const long long all = static_cast<long long>(gridDim.x) * WARPS, me = static_cast<long long>(blockIdx.x) * WARPS + warp;
     const long long x0 = base * me / all, x1 = base * (me + 1) / all;
+    const int shift = 31 - __clz(p.P);  // (a power of two)
     for (long long x = x0; x < x1;) {
         int i;
         const PageRow r = weigh_row_at(a, row_s, keys_s, first, x, i);
@@ -204,25 +205,36 @@ __global__ void __launch_bounds__(32 * WARPS) weigh_chunks(PagesWeighArgs a) {
         const int t1 = x1 - x < chunks - t0 ? t0 + static_cast<int>(x1 - x) : chunks;
         x += t1 - t0;
         float *scores = scores_of(a, r.row, head);
+        const int *table = p.table + static_cast<long long>(r.row) * p.M;
         const int rows = r.n * p.G, old = r.len - r.n, mine = (lane >> 2) + 8 * (lane & 3);
         for (int row0 = 0; row0 < rows; row0 += 8 * NT) {
             const int least = old + row0 / p.G;
-            auto load = [&](Keys<D> &k, float &s, int c) {
+            // what the table has for a chunk's page (pages of 16: its two)
+            auto entry = [&](int c) {
+                const int *e = table + (c * CHUNK >> shift);
+                return make_int2(e[0], p.P < CHUNK && c * CHUNK + 16 < r.len ? e[1] : 0);
+            };
+            auto checked = [&](int id) {
+                if (id >= 0 && id < p.n_pages) return id;
+                atomicOr(p.status, PST_TABLE);
+                return -1;
+            };
+            auto load = [&](Keys<D> &k, float &s, int c, int2 e) {
                 const int at = c * CHUNK;
                 if (p.P >= CHUNK) {
-                    const int id = page_of(p, r.row, at / p.P);
+                    const int id = checked(e.x);
                     if (id < 0) {
                         k.none(0);
                         k.none(1);
                     } else {
-                        k.load(p, page_ptr(p, id, head), at % p.P);
+                        k.load(p, page_ptr(p, id, head), at & (p.P - 1));
                     }
                 } else {
                     using B = PageBlock<D>;
                     const int g = lane >> 2, t = lane & 3;
 #pragma unroll
                     for (int h = 0; h < 2; h++) {
-                        const int id = at + 16 * h < r.len ? page_of(p, r.row, at / 16 + h) : -1;
+                        const int id = at + 16 * h < r.len ? checked(h ? e.y : e.x) : -1;
                         if (id < 0) {
                             k.none(h);
                             continue;
@@ -235,11 +247,13 @@ __global__ void __launch_bounds__(32 * WARPS) weigh_chunks(PagesWeighArgs a) {
             };
             Keys<D> cur, nxt;
             float was, next_was;
-            load(cur, was, t0);  // (on its way while the queries are put together)
+            load(cur, was, t0, entry(t0));  // (on its way while the queries are put together)
+            int2 ahead = t0 + 1 < t1 ? entry(t0 + 1) : make_int2(0, 0);
             Queries<D, NT> q;
             q.load(a, r, head, row0);
             for (int c = t0; c < t1; c++) {
-                if (c + 1 < t1) load(nxt, next_was, c + 1);
+                if (c + 1 < t1) load(nxt, next_was, c + 1, ahead);
+                if (c + 2 < t1) ahead = entry(c + 2);
                 const float got = weigh_chunk<D, NT>(cur, q, c * CHUNK, least);
                 if (c * CHUNK + mine < r.len) scores[c * CHUNK + mine] = was + got;
                 cur = nxt;
@@ -271,7 +285,7 @@ int launch_pages_weigh(PagesWeighArgs a, int num_sms, void *stream) {
         a.over = 0;
         a.most = MANY_ROWS;
     }
-    // two n tiles share the conversions of a chunk (16 query rows: 67 us, with one tile 116; four tiles: no less at 32 than two)
+    // two n tiles share the conversions of a chunk (16 query rows: 65 us, with one tile 116; four tiles: no less at 32 than two)
     if (rows <= 8) return a.p.d == 128 ? launch_as<128, 1>(a, num_sms, st) : launch_as<64, 1>(a, num_sms, st);
     return a.p.d == 128 ? launch_as<128, 2>(a, num_sms, st) : launch_as<64, 2>(a, num_sms, st);
 }
