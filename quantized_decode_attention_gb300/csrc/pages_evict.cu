@@ -16,8 +16,8 @@
 // value's sector of 32 bytes holds 4 tokens' channels (keeping an eighth reads 289 MB where 145 are kept); where
 // nearly all are kept it is instructions, the nibbles of values and the summaries, that count (60 % of the issue slots).
 //
-// 16 rows of 4160 tokens to 4096, two layers of 8 KV heads, head_dim 128: 14 us to choose, 70 to gather (the resizes of a
-// caller beside them: 105 in all); four prompts of 9 to 16 k to 2048, eight layers: 28 and 55 (128 in all).
+// 16 rows of 4160 tokens to 4096, two layers of 8 KV heads, head_dim 128: 91 us, some 14 of them to choose; four
+// prompts of 16384 to 2048, eight layers: 92, 28 to choose.
 #include <cuda_runtime.h>
 
 #include "pages.cuh"
@@ -25,8 +25,15 @@
 namespace dq {
 namespace {
 
-constexpr int CH_THREADS = 512, CH_WARPS = CH_THREADS / 32;
 constexpr int CH_HELD = 48 << 10;  // keys of scores that shared memory holds, at most
+// Longest rows (at most `cap` tokens) that 512 threads choose from, 1024 for longer ones.  512 / 1024, the whole eviction in us: 16 rows
+// of 1024 tokens, two layers, 28 / 36, of 4160 91 / 97; 4 of 16384, eight layers, 92 / 98; 1 of 32768, two layers, 34 to 38 / 35, of
+// 65536 112 / 66 to 75.  (256: 4 % less at 64 rows of 1024, more elsewhere.)
+constexpr int CH_LONG = 32768;
+// Keys held for which the gather's CTAs may come in while scores are chosen from: beside more shared memory their L1 is too
+// small for the sectors that two tokens share.  Beside / after, us: 16 rows of 4160 tokens 91 / 93, of 6144 98 / 99; 4 of 8192 74 / 70,
+// of 16384 121 / 92; 1 of 131072 183 / 170.
+constexpr int CH_BESIDE = 6144;
 constexpr int BIN_BITS = 11, BINS = 1 << BIN_BITS;
 
 // Keys that order like the scores, as unsigned: NaN lowest, -0 as 0.
@@ -52,26 +59,30 @@ __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
     return r;
 }
 
+template <int T>
 struct ChooseShared {
     int hist[BINS];
-    int above[CH_WARPS], equal[CH_WARPS];
+    int above[T / 32], equal[T / 32];
     uint32_t digit;
     int digit_above, digit_count;
 };
 
 // `held`: keys that the dynamic shared memory has room for behind the struct.
-__global__ void __launch_bounds__(CH_THREADS) choose_kernel(PagesEvictArgs a, int held) {
+template <int T>
+__global__ void __launch_bounds__(T, 2048 / T) choose_kernel(PagesEvictArgs a, int held) {
+    constexpr int CH_WARPS = T / 32;
     extern __shared__ __align__(16) uint8_t raw[];
-    ChooseShared &sh = *reinterpret_cast<ChooseShared *>(raw);
-    uint32_t *key = reinterpret_cast<uint32_t *>(raw + sizeof(ChooseShared));
+    using S = ChooseShared<T>;
+    S &sh = *reinterpret_cast<S *>(raw);
+    uint32_t *key = reinterpret_cast<uint32_t *>(raw + sizeof(S));
     const PagesView &p = a.p;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int head = blockIdx.y, layer = blockIdx.z, src = a.src[blockIdx.x], dst = a.dst[blockIdx.x];
-    let_next_start();
-    for (int i = tid; i < BINS; i += CH_THREADS) sh.hist[i] = 0;
+    if (held <= CH_BESIDE) let_next_start();
+    for (int i = tid; i < BINS; i += T) sh.hist[i] = 0;
     // is dst in order: a row of its own, named once?
     bool bad = src >= p.max_seqs || dst >= p.max_seqs || src == dst;
-    for (int i = tid; i < a.n; i += CH_THREADS) {
+    for (int i = tid; i < a.n; i += T) {
         if (a.src[i] < 0 || a.dst[i] < 0) continue;
         bad |= a.src[i] == dst || (a.dst[i] == dst && i != static_cast<int>(blockIdx.x));
     }
@@ -94,7 +105,7 @@ __global__ void __launch_bounds__(CH_THREADS) choose_kernel(PagesEvictArgs a, in
     const float *scores = a.scores + ((at + src) * p.Hkv + head) * a.cap;
     int *out = reinterpret_cast<int *>(a.scores) + ((at + dst) * p.Hkv + head) * a.cap;
     if (keep == len) {
-        for (int j = tid; j < len; j += CH_THREADS) out[j] = j;
+        for (int j = tid; j < len; j += T) out[j] = j;
         return;
     }
     // the tokens between the ones that are kept anyway
@@ -107,21 +118,21 @@ __global__ void __launch_bounds__(CH_THREADS) choose_kernel(PagesEvictArgs a, in
     for (int shift = 32 - BIN_BITS; take > 0 && take < count;) {
         if (range == 0xffffffffu) {  // the first digit, as the scores come in
 #pragma unroll 8
-            for (int j = tid; j < n; j += CH_THREADS) {
+            for (int j = tid; j < n; j += T) {
                 const uint32_t k = order_key(mid[j]);
                 if (j < held) key[j] = k;
                 atomicAdd(&sh.hist[k >> shift], 1);
             }
         } else {
 #pragma unroll 4
-            for (int j = tid; j < n; j += CH_THREADS) {
+            for (int j = tid; j < n; j += T) {
                 const uint32_t k = key_at(j) - least;
                 if (k <= range) atomicAdd(&sh.hist[k >> shift], 1);
             }
         }
         __syncthreads();
         // thread t: bins BINS - 1 - 4 t and the three below it
-        constexpr int PER = BINS / CH_THREADS;
+        constexpr int PER = BINS / T;
         int c[PER], sum = 0;
 #pragma unroll
         for (int i = 0; i < PER; i++) sum += c[i] = sh.hist[BINS - 1 - PER * tid - i];
@@ -466,15 +477,19 @@ int launch_gather_of(const PagesEvictArgs &a, int num_sms, cudaStream_t st) {
     return a.p.blk == 64 ? launch_gather<D, 64>(a, num_sms, st) : (a.p.blk == 32 ? launch_gather<D, 32>(a, num_sms, st) : launch_gather<D, 16>(a, num_sms, st));
 }
 
+template <int T>
+int launch_choose(const PagesEvictArgs &a, cudaStream_t st) {
+    const int held = a.cap < CH_HELD ? a.cap : CH_HELD, smem = static_cast<int>(sizeof(ChooseShared<T>));
+    if (const int e = allow_shared<choose_kernel<T>>(smem + CH_HELD * 4)) return e;
+    choose_kernel<T><<<dim3(a.n, a.p.Hkv, a.p.n_layers), T, smem + held * 4, st>>>(a, held);
+    return static_cast<int>(cudaGetLastError());
+}
+
 }  // namespace
 
 int launch_pages_evict(const PagesEvictArgs &a, int num_sms, void *stream) {
     auto st = static_cast<cudaStream_t>(stream);
-    const int held = a.cap < CH_HELD ? a.cap : CH_HELD, smem = static_cast<int>(sizeof(ChooseShared));
-    if (const int e = allow_shared<choose_kernel>(smem + CH_HELD * 4)) return e;
-    choose_kernel<<<dim3(a.n, a.p.Hkv, a.p.n_layers), CH_THREADS, smem + held * 4, st>>>(a, held);
-    const cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess) return static_cast<int>(e);
+    if (const int e = a.cap > CH_LONG ? launch_choose<1024>(a, st) : launch_choose<512>(a, st)) return e;
     return a.p.d == 128 ? launch_gather_of<128>(a, num_sms, st) : launch_gather_of<64>(a, num_sms, st);
 }
 
