@@ -128,9 +128,9 @@ def test_several_tokens(d, G, P, dtype):
 
 def test_common_only_where_it_pays():
     """Left to itself, common() takes much that many rows share and leaves little that few do: its estimate is far from its
-    limit of 20 us on both sides (8 KV heads of 128, 144 bytes each of a key and value: 63 x 8 x 4096 x 144 / 5e6 us = 59, twice
-    for two groups; 2 x 8 x 640 x 144 / 5e6 = 0.3)."""
-    f = Forked([(4096, [1 + i % 5 for i in range(64)]), (640, [3, 9, 1])], n_kv_heads=8, n_q_heads=32, n_pages=300, max_pages_per_seq=70)
+    limit of 20 us on both sides (4 KV heads of 128, 144 bytes each of a key and value: 63 x 4 x 4096 x 144 / 5e6 us = 30, twice
+    for two groups; 2 x 4 x 640 x 144 / 5e6 = 0.15)."""
+    f = Forked([(4096, [1 + i % 5 for i in range(64)]), (640, [3, 9, 1])], n_kv_heads=4, n_q_heads=8, n_pages=300, max_pages_per_seq=70)
     n = [1] * 67
     assert f.plan(n, None, f.bounds)[:, 0].tolist() == [4096] * 64 + [640] * 3
     f.always = False
@@ -267,6 +267,34 @@ def test_the_same_every_time_and_in_graphs_on_two_streams():
     f.pool.check()
     exp, _, tol, _ = f.expect(q[0], [1] * n)
     assert (np.abs(_np(outs[0]) - exp) <= tol).all()
+
+
+@pytest.mark.parametrize("n", [1, 3])
+def test_a_captured_plan_that_stops_to_pay(n):
+    """A replay after a row was shortened to little: what is left in common is no longer worth it, and the launches that the graph
+    holds attend without it (2^12 tokens, 63 x 4 x 4096 x 144 / 5e6 us = 30 saved; then 64 tokens, 0.5; the limit is 20)."""
+    import torch
+    f = Forked([(4096, [n + i % 5 for i in range(64)])], n_kv_heads=4, n_q_heads=4, n_pages=300, max_pages_per_seq=70)
+    counts = [n] * 64
+    q = f.queries(counts)
+    out, plan, scratch = torch.empty_like(q), torch.empty(64, 2, dtype=torch.int32, device="cuda"), f.pool.shared_scratch(64 * n)
+    cu = None if n == 1 else _cu(counts)
+    g, s = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    with torch.cuda.graph(g, stream=s):
+        f.pool.common(plan, cu=cu)
+        f.pool.shared(0, q, out, plan, scratch, cu=cu, max_new=n)
+    for tokens in (4096, 64):
+        out.fill_(float("nan"))
+        torch.cuda.synchronize()
+        g.replay()
+        torch.cuda.synchronize()
+        f.pool.check()
+        assert plan[:, 0].tolist() == [tokens if tokens > 64 else 0] * 64
+        want, _, tol, _ = f.expect(q, counts)
+        assert (np.abs(_np(out) - want) <= tol).all()
+        f.pool.resize(_i32([5]), _i32([100]))
+        f.lens[5] = 100
+        f.hk[5], f.hv[5] = f.hk[5][:100], f.hv[5][:100]
 
 
 def test_tokens_of_no_row_are_left_alone():
