@@ -135,7 +135,7 @@ __device__ __forceinline__ PageRow attn_row(const A &a, int i) {
         return PageRow{what.y, what.x, q0, n, 0};
     }
     o = page_row(a.p, a.r, i);
-    if (a.mode == PAGES_OWN && o.len > 0) {
+    if (a.mode == PAGES_OWN && o.len > 0 && o.n > 0) {  // (a row that brings nothing may be shorter than what the others share)
         o.from = a.plan[2 * i];
         if (o.from < 0 || o.from % a.p.P || (o.from > 0 && o.from > o.len - o.n)) {
             atomicOr(a.p.status, PST_ARG);

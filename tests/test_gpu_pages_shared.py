@@ -308,3 +308,21 @@ def test_tokens_of_no_row_are_left_alone():
         f.pool.shared(0, q, out, plan, f.pool.shared_scratch(n + 5), cu=_cu(counts), max_new=max(counts), lse=lse)
         f.pool.check()
         assert (out[n:] == 9).all() and (lse[n:] == 9).all() and torch.isfinite(out[:n]).all()
+
+
+@pytest.mark.parametrize("counts", [[1, 0, 1, 1, 0], [2, 0, 3, 1, 0], [40, 0, 9, 70, 0], [0, 0, 1, 300, 0]])
+def test_short_rows_that_bring_nothing(counts):
+    """Rows of the group that hold less than the others have in common, and bring nothing: they do not count, and they are in
+    order.  One of them is of the same beginning, one a stranger; each is at the group's front, middle and end once."""
+    f = Forked([(320, [60, None, 9, 300]), (70, [30])], n_pages=60, page_size=32, max_pages_per_seq=24)
+    f.bounds = [0, 5]
+    f.pool.fork(_i32([0]), _i32([1]))
+    f.pool.resize(_i32([1]), _i32([100]))
+    f.lens[1], f.hk[1], f.hv[1] = 100, f.hk[0][:100], f.hv[0][:100]
+    for rows in (None, [1, 4, 0, 3, 2], [2, 4, 0, 1, 3]):
+        c = counts if rows is None else [counts[r] for r in rows]
+        there = [r for r, n in enumerate(counts) if n]
+        want = min([320] + [(f.lens[r] - counts[r]) // 32 * 32 for r in there])
+        assert f.plan(c, rows, [0, 5])[:, 0].tolist() == [want] * 5
+        f.pool.check()
+        f.verify(f.queries(c), c, rows)
