@@ -41,7 +41,7 @@ int allow_shared(int bytes) {
 // How many CTAs the launch over the rows' own pages takes, of `grid`, for n places of UNIT_COST and chunks of 32 tokens: few
 // where they are done with it before the common pages are, which then have the other SMs at the same time.
 __device__ __forceinline__ int own_ctas(int n, int grid) {
-        constexpr int PLACES = 96, MOST = 64;
+    constexpr int PLACES = 96, MOST = 64;
     return n <= PLACES * MOST ? MOST : grid;
 }
 

@@ -574,7 +574,14 @@ __global__ void __launch_bounds__(32 * NW, 1) attn_chunks(const InMode<MODE> a) 
     int ctas = N / MIN_PLACES;
     ctas = ctas < 1 ? 1 : (ctas > static_cast<int>(gridDim.x) ? gridDim.x : ctas);
     if (a.mode == PAGES_OWN || a.mode == PAGES_COMMON) {
-        const int room = a.mode == PAGES_OWN ? own_ctas(N, gridDim.x) : sms_left<32 * NW>(a, own, sh.part);
+        int room = a.mode == PAGES_OWN ? own_ctas(N, gridDim.x) : sms_left<32 * NW>(a, own, sh.part);
+        if (a.mode == PAGES_OWN) {
+            // nothing in common: all SMs (16 rows of 1364 tokens 21.4 -> 16.8 us, 32 of 664 22.4 -> 17.0).  Each warp looks for
+            // itself: with a barrier's vote the loop below spills (64 rows of 8256 113 -> 115)
+            bool shares = false;
+            for (int i = lane; i < a.r.n_rows; i += 32) shares |= a.plan[2 * i] > 0;
+            if (!__any_sync(FULL, shares)) room = gridDim.x;
+        }
         ctas = ctas > room ? room : ctas;
     }
     if (N == 0 || static_cast<int>(blockIdx.x) >= ctas) {

@@ -326,3 +326,19 @@ def test_short_rows_that_bring_nothing(counts):
         assert f.plan(c, rows, [0, 5])[:, 0].tolist() == [want] * 5
         f.pool.check()
         f.verify(f.queries(c), c, rows)
+
+
+def test_nothing_in_common_is_attention():
+    """Where the plan is empty the rows' own pages are all there is, and the launch over them has the whole card, as attention's has:
+    the same shares, and so the same bits."""
+    import torch
+    f = Filled([2040, 2048, 1990, 2041, 2015, 2000, 2048, 1985], n_kv_heads=4, n_q_heads=16, n_pages=300, max_pages_per_seq=33)
+    n = [1] * 8
+    q = f.queries(n)
+    want = f.attend(q, n)
+    out, lse, plan = torch.empty_like(q), torch.empty_like(want[1]), torch.empty(8, 2, dtype=torch.int32, device="cuda")
+    f.pool.common(plan, always=True)
+    assert plan[:, 0].tolist() == [0] * 8
+    f.pool.shared(0, q, out, plan, f.pool.shared_scratch(8), lse=lse)
+    f.pool.check()
+    assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
