@@ -41,6 +41,15 @@ struct PagesRows {
     int n_rows, n_tok, max_new;
 };
 
+// Whether rows with few query rows (`few` at most, tokens times G) are likely beside those with many, so that they are worth a
+// launch of their own: few on average in all rows but one that has as many tokens as a row may have.  With such a launch / all in the
+// one for many, us: 16 rows of 1 token over 32768 beside one of 2048: weights 530 / 1632, cross 941 / 1151; 4 rows of 64 over 16384,
+// where it has nothing to do: weights 57.8 / 54.2, cross 71.8 / 71.0, shared 82.4 / 78.0; 3 rows of 2 over 8192 beside one of 64, where
+// each of the launches is short: weights 26.7 / 41.6, cross 56.1 / 44.4.
+inline bool few_beside_most(const PagesRows &r, int G, int few) {
+    return r.n_rows > 1 && (static_cast<long long>(r.n_tok) - r.max_new) * G <= static_cast<long long>(few) * (r.n_rows - 1);
+}
+
 constexpr int PAGES_SELECT_MAX = 16384;  // pages of a row that a choice is made among (a key of each in shared memory)
 
 // The int part of the workspace: [0] copies or moves of the last plan, [1] live pages

@@ -276,9 +276,8 @@ int launch_pages_weigh(PagesWeighArgs a, int num_sms, void *stream) {
     const int rows = a.r.max_new * a.p.G;
     a.over = 0;
     a.most = 0x7fffffff;
-    if (rows > MANY_ROWS) {  // rows with many query rows on the tensor cores, the others of a mixed batch here (where rows have
-        // many on average, all there: an idle launch costs 3 us)
-        const bool mixed = a.r.n_rows > 1 && static_cast<long long>(a.r.n_tok) * a.p.G <= static_cast<long long>(MANY_ROWS) * a.r.n_rows;
+    if (rows > MANY_ROWS) {  // rows with many query rows on the tensor cores, the others of a mixed batch here
+        const bool mixed = few_beside_most(a.r, a.p.G, MANY_ROWS);
         a.over = mixed ? MANY_ROWS : 0;
         if (const int e = launch_pages_weigh_many(a, num_sms < PAGES_MAX_CTAS ? num_sms : PAGES_MAX_CTAS, stream)) return e;
         if (!mixed) return 0;

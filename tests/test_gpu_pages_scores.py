@@ -446,3 +446,19 @@ def test_weigh_evict_and_select_on_other_streams():
         held = f.codes[0][0][4][pick, h]
         sums = [R.summary(held[j * 16:(j + 1) * 16]) for j in range(13)]
         assert sel[0, h].tolist() == R.choose(_np(q[0, h:h + 1]), sums, 13, 4, 1, 1)
+
+
+def test_weights_of_single_tokens_beside_a_chunk():
+    """One row brings a chunk and the others a token: theirs are weighed by the kernel for few, every score by one thread in an order
+    of its own, and so with the bits of a call without the chunk."""
+    import torch
+    f = Weighed([300 - 7 * i for i in range(16)] + [300], n_pages=100)
+    counts = [1] * 16 + [200]
+    f.verify_weights(counts)
+    q = f.queries(counts)
+    _, lse = f.attend(q, counts)
+    a, b = f.scores(value=0.5), f.scores(value=0.5)
+    f.pool.weigh(0, q, lse, a, cu=_cu(counts), max_new=200)
+    f.pool.weigh(0, q[:16], lse[:16].contiguous(), b)
+    f.pool.check()
+    assert torch.equal(a[:16], b[:16])
