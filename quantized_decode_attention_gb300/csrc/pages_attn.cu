@@ -11,12 +11,6 @@ constexpr int PROMPT_ROWS = 32;
 
 }  // namespace
 
-// Whether rows with few query rows are likely: where rows (groups) have many on average, all go to the kernel for many, for an idle
-// launch of the other costs 4 to 8 us (shared attention, 32 rows of 9 to 24 tokens).
-static bool few_likely(const PagesAttnArgs &a, int rows) {
-    return rows > 1 && static_cast<long long>(a.r.n_tok) * a.p.G <= static_cast<long long>(PROMPT_ROWS) * rows;
-}
-
 // Attention's launches of one kind; mixed: rows with few query rows have a launch of their own.
 static int launch_kind(PagesAttnArgs a, int mode, bool mixed, int num_sms, void *stream) {
     const int grid = num_sms < PAGES_MAX_CTAS ? num_sms : PAGES_MAX_CTAS;
@@ -40,19 +34,19 @@ static int launch_kind(PagesAttnArgs a, int mode, bool mixed, int num_sms, void 
 }
 
 int launch_pages_attention(const PagesAttnArgs &a, int mode, int num_sms, void *stream) {
-    return launch_kind(a, mode, mode == PAGES_ALL ? few_likely(a, a.r.n_rows) : a.r.n_rows > 1, num_sms, stream);
+    return launch_kind(a, mode, mode == PAGES_ALL ? few_beside_most(a.r, a.p.G, PROMPT_ROWS) : a.r.n_rows > 1, num_sms, stream);
 }
 
 // The launch over the rows' own pages, then the one over what groups have in common.
 int launch_pages_shared(const PagesAttnArgs &a, int n_groups, int max_group, int num_sms, void *stream) {
-    const bool few = a.r.max_new * a.p.G <= PROMPT_ROWS || few_likely(a, a.r.n_rows);
+    const bool few = a.r.max_new * a.p.G <= PROMPT_ROWS || few_beside_most(a.r, a.p.G, PROMPT_ROWS);
     if (const int e = launch_kind(a, PAGES_OWN, few, num_sms, stream)) return e;
     PagesAttnArgs c = a;
     c.own_max_new = a.r.max_new;
     c.after_few = few;
     c.r.n_rows = n_groups;
     c.r.max_new = max_group;
-    return launch_kind(c, PAGES_COMMON, few_likely(a, n_groups), num_sms, stream);
+    return launch_kind(c, PAGES_COMMON, few_beside_most(c.r, c.p.G, PROMPT_ROWS), num_sms, stream);
 }
 
 }  // namespace dq

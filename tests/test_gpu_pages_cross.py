@@ -130,3 +130,20 @@ def test_captured_with_states_that_change(counts):
         f.pool.check()
         want, _, tol, _ = f.expect(q, counts)
         assert (np.abs(_np(out) - want) <= tol).all()
+
+
+def test_single_queries_beside_many():
+    """One row brings many queries and the others few: those of few have the kernel for few, and the bits that a call of theirs
+    alone gives (32 states are one step of it, whatever share they are in; max_new 5 as a bound takes the same tile)."""
+    import torch
+    f = Encoded([1 + 2 * i % 32 for i in range(16)] + [300], n_q_heads=8, n_pages=64)
+    counts = [1 + i % 3 for i in range(16)] + [300]
+    n = sum(counts[:16])
+    q = f.queries(counts)
+    out, lse = f.attend(q, counts)
+    alone, lse_alone = torch.empty_like(q[:n]), torch.empty_like(lse[:n])
+    f.pool.cross(0, q[:n], alone, cu=_cu(counts[:16]), max_new=5, lse=lse_alone)
+    f.pool.check()
+    assert torch.equal(lse[:n], lse_alone) and torch.equal(out[:n], alone)
+    want, _, tol, _ = f.expect(q, counts)
+    assert (np.abs(_np(out) - want) <= tol).all()

@@ -342,3 +342,25 @@ def test_nothing_in_common_is_attention():
     f.pool.shared(0, q, out, plan, f.pool.shared_scratch(8), lse=lse)
     f.pool.check()
     assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+
+
+def test_few_tokens_beside_a_chunk_are_attention():
+    """Rows with few new tokens beside one with many: each goes to the kernel that its number asks for, as in attention, so that with
+    nothing in common the bits are attention's."""
+    import torch
+    f = Filled([300, 77, 150, 512, 64, 700], n_q_heads=8, n_pages=64)
+    counts = [1, 2, 1, 1, 3, 500]
+    q = f.queries(counts)
+    want = f.attend(q, counts)
+    out, lse, plan = torch.empty_like(q), torch.empty_like(want[1]), torch.empty(6, 2, dtype=torch.int32, device="cuda")
+    f.pool.common(plan, cu=_cu(counts), always=True)
+    f.pool.shared(0, q, out, plan, f.pool.shared_scratch(sum(counts)), cu=_cu(counts), max_new=500, lse=lse)
+    f.pool.check()
+    assert torch.equal(lse, want[1]) and torch.equal(out, want[0])
+
+
+def test_groups_with_few_tokens_beside_one_with_many():
+    """Groups of which one brings a chunk: the common pages of each by the kernel that its number of query rows asks for."""
+    f = Forked([(640, [9, 30]), (256, [5, 1, 2]), (1024, [400, 20]), (320, [1, 1])], n_q_heads=8, n_pages=100, max_pages_per_seq=24)
+    counts = [1, 2, 1, 1, 1, 390, 2, 1, 1]
+    f.verify(f.queries(counts), counts)
