@@ -8,6 +8,11 @@ namespace {
 // Query rows of a row and KV head beyond which the tensor-core kernel takes over (8 rows of 32768 tokens, 4 query
 // heads a KV head: 16 query rows 88 us, 32 160, 48 232, 64 304; that kernel 200 at up to 128).
 constexpr int PROMPT_ROWS = 32;
+// Groups of rows from which those with few query rows have a launch over their common pages beside one group with many (fewer only
+// where all have few on average).  Such a launch / all in the one for many, us: 64 rows behind 4096 tokens and one group of 8 behind
+// 2048 51 / 34, 4 groups of 2 behind 8192 84 / 73, 8 of 4 behind 8192 81 / 137, 8 of 2 behind 16384 98 / 238, 8 of 3 behind 32768
+// 134 / 650.
+constexpr int SOME_GROUPS = 4;
 
 }  // namespace
 
@@ -46,7 +51,8 @@ int launch_pages_shared(const PagesAttnArgs &a, int n_groups, int max_group, int
     c.after_few = few;
     c.r.n_rows = n_groups;
     c.r.max_new = max_group;
-    return launch_kind(c, PAGES_COMMON, few_beside_most(c.r, c.p.G, PROMPT_ROWS), num_sms, stream);
+    const bool few_all = n_groups > 1 && static_cast<long long>(a.r.n_tok) * a.p.G <= static_cast<long long>(PROMPT_ROWS) * n_groups;
+    return launch_kind(c, PAGES_COMMON, few_all || (n_groups > SOME_GROUPS && few_beside_most(c.r, c.p.G, PROMPT_ROWS)), num_sms, stream);
 }
 
 }  // namespace dq

@@ -364,3 +364,12 @@ def test_groups_with_few_tokens_beside_one_with_many():
     f = Forked([(640, [9, 30]), (256, [5, 1, 2]), (1024, [400, 20]), (320, [1, 1])], n_q_heads=8, n_pages=100, max_pages_per_seq=24)
     counts = [1, 2, 1, 1, 1, 390, 2, 1, 1]
     f.verify(f.queries(counts), counts)
+
+
+def test_many_groups_with_few_tokens_beside_one_with_many():
+    """The same with more groups, so that those of few have a launch over their common pages; a group without a row that brings
+    anything, and one of a single row."""
+    f = Forked([(256, [5, 1]), (640, [9, 30, 2]), (320, [400, 20]), (128, [1, 1]), (200, [3]), (512, [7, 1, 60]), (384, [None, 2])], n_q_heads=8,
+               n_pages=120, max_pages_per_seq=24)
+    counts = [1, 1, 2, 1, 1, 390, 1, 0, 0, 1, 2, 1, 3, 1, 1]
+    f.verify(f.queries(counts), counts)
