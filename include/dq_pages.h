@@ -227,8 +227,9 @@ dq_status dq_pages_cross(const dq_pages_config *cfg, const dq_pages_buffers *buf
  *            them.  Common are the whole leading pages that the tables of all rows of the
  *            group name alike and that every new token sees all of; none in a group of one
  *            row, or for a row in no group, and, where `always` is 0, none where reading them
- *            once would save less time than it costs (an estimate from the group's rows, new
- *            tokens and common tokens).  Rows that hold or bring nothing do not count.
+ *            once would save less time than it costs (an estimate from the rows, new tokens
+ *            and common tokens of all groups, which share the launch).  Rows that hold or bring
+ *            nothing do not count.
  *            It stays true until a row of the call is resized, forked into, moved by
  *            dq_pages_compact or brings other tokens: one plan serves all layers.
  * dq_pages_shared gives what dq_pages_attention of the same rows does (to rounding: the

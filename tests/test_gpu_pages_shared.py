@@ -373,3 +373,75 @@ def test_many_groups_with_few_tokens_beside_one_with_many():
                n_pages=120, max_pages_per_seq=24)
     counts = [1, 1, 2, 1, 1, 390, 1, 0, 0, 1, 2, 1, 3, 1, 1]
     f.verify(f.queries(counts), counts)
+
+
+def test_savings_of_unlike_groups_add_up():
+    """The launch over common pages costs the call once: groups that would not pay for it alone, however many groups the call has,
+    are taken beside one that does.  Reading once saves, at 4 KV heads of 128, 63 x 4 x 4096 x 144 / 5e6 us = 30 for the first group,
+    11 x 4 x 2048 x 144 / 5e6 = 2.6 for the second, and 0.15 for the third, which is less than a group's own place in the launch takes (1.5)."""
+    f = Forked([(4096, [1 + i % 5 for i in range(64)]), (2048, [1 + i % 3 for i in range(12)]), (640, [3, 9, 1]), (640, [2])], n_kv_heads=4,
+               n_q_heads=8, n_pages=400, max_pages_per_seq=70)
+    f.always = False
+    n = [1] * 80
+    assert f.plan(n, None, f.bounds)[:, 0].tolist() == [4096] * 64 + [2048] * 12 + [0] * 4
+    f.verify(f.queries(n), n)
+    assert f.plan([1] * 16, list(range(64, 80)), [0, 12, 15, 16])[:, 0].tolist() == [0] * 16  # (2.6 and 0.15, of 20)
+    f.pool.check()
+
+
+def test_groups_of_one_row_save_nothing():
+    """One pair behind 2048 tokens saves 8 x 2048 x 144 / 5e6 us = 0.5 of the 20 that the launch costs, beside 62 rows in groups of
+    their own as it does alone."""
+    f = Forked([(2048, [1, 2])] + [(60 + i, [1]) for i in range(62)], n_kv_heads=8, n_q_heads=8, n_pages=160, max_pages_per_seq=34)
+    f.always = False
+    n = [1] * 64
+    assert f.plan(n, None, f.bounds)[:, 0].tolist() == [0] * 64
+    f.always = True
+    assert f.plan(n, None, f.bounds)[:, 0].tolist() == [2048] * 2 + [0] * 62
+    f.verify(f.queries(n), n)
+
+
+def test_many_small_savings_and_groups_out_of_order():
+    """Twenty groups that save 1.2 us each pay for the launch together (2 x 8 x 2560 x 144 / 5e6; 23.6 in all), of which none is
+    worth its place beside others; with half of them nothing is taken.  Groups out of order are reported, whatever is beside them."""
+    from quantized_decode_attention_gb300 import DQError
+    f = Forked([(2560, [1, 2, 3])] * 20, n_kv_heads=8, n_q_heads=8, n_pages=900, max_pages_per_seq=42)
+    f.always = False
+    n = [1] * 60
+    assert f.plan(n, None, f.bounds)[:, 0].tolist() == [2560] * 60
+    f.verify(f.queries(n), n)
+    assert f.plan([1] * 30, None, f.bounds[:11])[:, 0].tolist() == [0] * 30
+    f.pool.check()
+    for b in ([0, 3, 2, 6], [0, 40, 61], [-1, 3, 60]):
+        f.plan(n, None, b)
+        with pytest.raises(DQError, match="out of range"):
+            f.pool.check()
+
+
+def test_a_captured_choice_among_groups():
+    """The choice among groups in a graph, beside the attention that follows it: a replay after rows of the group that pays were
+    shortened takes nothing, one after they are empty the same."""
+    import torch
+    f = Forked([(4096, [1 + i % 5 for i in range(64)]), (2048, [1 + i % 3 for i in range(12)])], n_kv_heads=4, n_q_heads=4, n_pages=400,
+               max_pages_per_seq=70)
+    n = [1] * 76
+    q = f.queries(n)
+    out, plan, scratch, b = torch.empty_like(q), torch.empty(76, 2, dtype=torch.int32, device="cuda"), f.pool.shared_scratch(76), _i32(f.bounds)
+    g, s = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    with torch.cuda.graph(g, stream=s):
+        for _ in range(2):
+            f.pool.common(plan, groups=b)
+            f.pool.shared(0, q, out, plan, scratch, groups=b, max_group=64)
+    for length, want in ((None, [4096] * 64 + [2048] * 12), (100, [0] * 76), (0, [0] * 76)):
+        if length is not None:
+            f.pool.resize(_i32(range(60)), _i32([length] * 60))
+            for r in range(60):
+                f.lens[r], f.hk[r], f.hv[r] = length, f.hk[r][:length], f.hv[r][:length]
+        out.fill_(float("nan"))
+        torch.cuda.synchronize()
+        g.replay()
+        torch.cuda.synchronize()
+        f.pool.check()
+        assert plan[:, 0].tolist() == want
+        exp, _, tol, _ = f.expect(q, n)
+        assert (np.abs(_np(out) - exp) <= tol).all()
