@@ -286,6 +286,7 @@ dq_status dq_pages_common(const dq_pages_config *cfg, const dq_pages_buffers *bu
     a.groups = groups;
     a.n_groups = n_groups;
     a.always = always;
+    a.num_sms = device_sms();
     a.plan = plan;
     return launched(dq::launch_pages_common(a, stream), "common launch");
 }

@@ -14,16 +14,17 @@
 namespace dq {
 namespace {
 
-constexpr float BYTES_US = 5e6f, UNIT_US = 1.9f, COST_US = 20.f, GROUP_US = 1.5f, SMS = 152.f;
+constexpr float BYTES_US = 5e6f, UNIT_US = 1.9f, COST_US = 20.f, GROUP_US = 1.5f;
 constexpr int CO_THREADS = 1024, CO_WARPS = CO_THREADS / 32;
 
 // What one reading of a group's `keys` common tokens saves, in us, for `rows` rows with `tokens` new ones: the time of each
 // row's reading them (the cache at 5 TB/s; for many query rows the products, 1.9 us a unit of 256 query rows and 128 keys on
 // an SM), less that of one reading.
-__device__ __forceinline__ float saved_us(const PagesView &p, int rows, int tokens, int keys) {
+__device__ __forceinline__ float saved_us(const PagesCommonArgs &a, int rows, int tokens, int keys) {
+    const PagesView &p = a.p;
     const float q = static_cast<float>(tokens) * p.G, heads = static_cast<float>(p.Hkv) * keys;  // query rows; keys of all heads
     if (q <= 32.f * rows) return (rows - 1) * heads * (p.d * 9 / 8) / BYTES_US;
-    return (rows * ceilf(q / rows / 256.f) - ceilf(q / 256.f)) * (heads / 128.f) * UNIT_US / SMS;
+    return (rows * ceilf(q / rows / 256.f) - ceilf(q / 256.f)) * (heads / 128.f) * UNIT_US / a.num_sms;
 }
 
 // Which groups' common pages are taken, a choice of speed alone: all together save more than the launch over them and its join
@@ -95,7 +96,7 @@ __global__ void __launch_bounds__(CO_THREADS) common_kernel(PagesCommonArgs a) {
         }
         __syncthreads();
     }
-    const float us = count > 1 ? saved_us(p, count, tokens, least * p.P) : 0.f;
+    const float us = count > 1 ? saved_us(a, count, tokens, least * p.P) : 0.f;
     const bool share = count > 1 && (a.always || a.n_groups > 1 || Choice{us, 1}.takes(us));
     const int2 what = share ? make_int2(least * p.P, first) : make_int2(0, 0);
     // (where the groups' choice is still to come, the group's second place has what it saves)

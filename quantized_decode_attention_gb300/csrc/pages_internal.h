@@ -126,6 +126,7 @@ struct PagesCommonArgs {
     const int *groups;
     int n_groups;
     int always;           // also where it does not pay
+    int num_sms;
     int *plan;
 };
 struct PagesWeighArgs {
