@@ -421,7 +421,7 @@ dq_status dq_pages_check(const dq_pages_buffers *bufs, void *stream) {
         {dq::PST_FULL, DQ_ENOMEM, "resize: too few free pages; nothing was changed"},
         {dq::PST_ARG, DQ_EINVAL, "a row, length or count is out of range, or a row was named twice"},
         {dq::PST_TABLE, DQ_EINVAL, "a table names no page of the pool"},
-        {dq::PST_SHARED, DQ_EINVAL, "an append met a page that several rows hold: resize after a fork"},
+        {dq::PST_SHARED, DQ_EINVAL, "an append or an eviction met a page that several rows hold: resize after a fork"},
         {dq::PST_NONFINITE, DQ_ENONFINITE, "non-finite K/V input"}};
     unsigned w = 0;
     cudaError_t e = cudaMemcpyAsync(&w, bufs->status, sizeof w, cudaMemcpyDeviceToHost, st);

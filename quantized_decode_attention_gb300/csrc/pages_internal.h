@@ -16,7 +16,7 @@ enum : unsigned {
     PST_FULL = 64u,    // resize: too few free pages
     PST_ARG = 128u,    // a row, length or count out of range, or a row named twice
     PST_TABLE = 256u,  // a page number out of range
-    PST_SHARED = 512u  // an append to a page that several rows hold
+    PST_SHARED = 512u  // an append or an eviction to a page that several rows hold
 };
 
 // Pool geometry and pointers, passed to every kernel by value.

@@ -462,3 +462,15 @@ def test_weights_of_single_tokens_beside_a_chunk():
     f.pool.weigh(0, q[:16], lse[:16].contiguous(), b)
     f.pool.check()
     assert torch.equal(a[:16], b[:16])
+
+
+def test_a_destination_that_another_row_holds_is_reported_as_such():
+    from quantized_decode_attention_gb300 import DQError
+    f = Pool2([100], 3, seed=3)
+    f.resize([1], [64])
+    f.pool.fork(_i32([1]), _i32([2]))
+    f.pool.check()
+    f.pool.evict(f.scores, _i32([0]), _i32([2]))
+    with pytest.raises(DQError, match="eviction met a page that several rows hold"):
+        f.pool.check()
+    f.pool.check()
