@@ -260,6 +260,22 @@ dq_status dq_pages_test_expire_wait(const dq_pages_config *cfg, const dq_pages_b
                                     int n_tok, int max_new, unsigned long long limit_ns, void *stream);
 
 /*
+ * The same for the calls below and above that wait: cross attention, shared attention and weighing over rows 0 .. n_rows - 1.
+ * (dq_pages_weigh of at most 48 query rows a row and KV head waits for nothing: it is carried out.)
+ * Errors: as those calls.
+ */
+dq_status dq_pages_test_expire_cross(const dq_pages_config *cfg, const dq_pages_buffers *bufs, int layer, const void *q,
+                                     long long q_tok_stride, long long q_head_stride, void *out, const int *cu, int n_rows,
+                                     int n_tok, int max_new, unsigned long long limit_ns, void *stream);
+dq_status dq_pages_test_expire_shared(const dq_pages_config *cfg, const dq_pages_buffers *bufs, int layer, const void *q,
+                                      long long q_tok_stride, long long q_head_stride, void *out, const int *cu, int n_rows,
+                                      int n_tok, int max_new, const int *groups, int n_groups, int max_group, const int *plan,
+                                      void *scratch, unsigned long long limit_ns, void *stream);
+dq_status dq_pages_test_expire_weigh(const dq_pages_config *cfg, const dq_pages_buffers *bufs, int layer, const void *q,
+                                     long long q_tok_stride, long long q_head_stride, const float *lse, float *scores, int cap,
+                                     const int *cu, int n_rows, int n_tok, int max_new, unsigned long long limit_ns, void *stream);
+
+/*
  * Choose pages for each row's one query token and KV head.  With the group's
  * query heads q_h, Q+ = sum_h max(q_h, 0) and Q- = sum_h min(q_h, 0) a page's score
  *   sum_c Q+_c largest_c + Q-_c smallest_c

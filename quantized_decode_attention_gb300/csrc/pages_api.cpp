@@ -172,6 +172,58 @@ dq_status attention_args(dq::PagesAttnArgs &a, const dq_pages_config *cfg, const
     return DQ_OK;
 }
 
+// The same of a call of shared attention.
+dq_status shared_args(dq::PagesAttnArgs &a, const dq_pages_config *cfg, const dq_pages_buffers *bufs, int layer, const void *q,
+                      long long q_tok_stride, long long q_head_stride, void *out, float *lse, const int *rows, const int *cu, int n_rows,
+                      int n_tok, int max_new, const int *groups, int n_groups, int max_group, const int *plan, void *scratch,
+                      float sm_scale) {
+    dq_status s = attention_args(a, cfg, bufs, layer, q, q_tok_stride, q_head_stride, out, lse, rows, cu, n_rows, n_tok, max_new,
+                                 nullptr, 0, sm_scale);
+    if (s != DQ_OK) return s;
+    if ((s = check_groups(groups, n_groups, n_rows, plan)) != DQ_OK) return s;
+    if (max_group < 1 || max_group > n_tok) return fail(DQ_EINVAL, "max_group outside [1, n_tok]");
+    if (!scratch) return fail(DQ_EINVAL, "scratch is NULL");
+    if (!aligned16(scratch)) return fail(DQ_EALIGN, "scratch not 16-byte aligned");
+    a.groups = groups;
+    a.plan = plan;
+    a.call_rows = n_rows;
+    a.part = static_cast<float *>(scratch);
+    uint8_t *ws = static_cast<uint8_t *>(bufs->workspace) + dq::pages_ws_own(cfg->n_pages);
+    a.own_tickets = reinterpret_cast<int *>(ws);
+    a.own_records = reinterpret_cast<float *>(ws + dq::PAGES_MAX_CTAS * 4);
+    return DQ_OK;
+}
+
+// Checked arguments of a call that weighs.
+dq_status weigh_args(dq::PagesWeighArgs &a, const dq_pages_config *cfg, const dq_pages_buffers *bufs, int layer, const void *q,
+                     long long q_tok_stride, long long q_head_stride, const float *lse, float *scores, int cap, const int *rows,
+                     const int *cu, int n_rows, int n_tok, int max_new, float sm_scale) {
+    dq_status s = view(cfg, bufs, layer, true, a.p);
+    if (s != DQ_OK) return s;
+    if ((s = call_rows(cfg, layer, rows, cu, n_rows, n_tok, max_new, a.r)) != DQ_OK) return s;
+    if (!q || !lse || !scores) return fail(DQ_EINVAL, "q / lse / scores is NULL");
+    if (!aligned16(q) || (q_tok_stride | q_head_stride) & 7)
+        return fail(DQ_EALIGN, "q not 16-byte aligned, or a stride is no multiple of 8 elements");
+    if (!aligned4(lse) || !aligned4(scores)) return fail(DQ_EALIGN, "lse / scores not aligned to 4 bytes");
+    if ((s = check_cap(cap)) != DQ_OK) return s;
+    if (!std::isfinite(sm_scale)) return fail(DQ_EINVAL, "sm_scale is not finite");
+    a.q = static_cast<const uint16_t *>(q);
+    a.qt = q_tok_stride;
+    a.qh = q_head_stride;
+    a.lse = lse;
+    a.scores = scores;
+    a.cap = cap;
+    a.scale_log2 = logit_scale(cfg, sm_scale);
+    uint8_t *ws = static_cast<uint8_t *>(bufs->workspace) + dq::pages_ws_lists(cfg->n_pages);
+    a.tickets = reinterpret_cast<int *>(ws);
+    a.records = reinterpret_cast<float *>(ws + dq::PAGES_MAX_CTAS * 20);
+    a.wait_ns = dq::PAGES_WAIT_NS;
+    a.owed = 0;
+    return DQ_OK;
+}
+
+unsigned long long expire_limit(unsigned long long ns) { return ns < 1000ULL ? 1000ULL : (ns > 1000000000ULL ? 1000000000ULL : ns); }
+
 }  // namespace
 
 extern "C" {
@@ -305,20 +357,9 @@ dq_status dq_pages_shared(const dq_pages_config *cfg, const dq_pages_buffers *bu
                           int max_new, const int *groups, int n_groups, int max_group, const int *plan, void *scratch,
                           float sm_scale, void *stream) {
     dq::PagesAttnArgs a{};
-    dq_status s = attention_args(a, cfg, bufs, layer, q, q_tok_stride, q_head_stride, out, lse, rows, cu, n_rows, n_tok, max_new,
-                                 nullptr, 0, sm_scale);
+    const dq_status s = shared_args(a, cfg, bufs, layer, q, q_tok_stride, q_head_stride, out, lse, rows, cu, n_rows, n_tok, max_new,
+                                    groups, n_groups, max_group, plan, scratch, sm_scale);
     if (s != DQ_OK) return s;
-    if ((s = check_groups(groups, n_groups, n_rows, plan)) != DQ_OK) return s;
-    if (max_group < 1 || max_group > n_tok) return fail(DQ_EINVAL, "max_group outside [1, n_tok]");
-    if (!scratch) return fail(DQ_EINVAL, "scratch is NULL");
-    if (!aligned16(scratch)) return fail(DQ_EALIGN, "scratch not 16-byte aligned");
-    a.groups = groups;
-    a.plan = plan;
-    a.call_rows = n_rows;
-    a.part = static_cast<float *>(scratch);
-    uint8_t *ws = static_cast<uint8_t *>(bufs->workspace) + dq::pages_ws_own(cfg->n_pages);
-    a.own_tickets = reinterpret_cast<int *>(ws);
-    a.own_records = reinterpret_cast<float *>(ws + dq::PAGES_MAX_CTAS * 4);
     return launched(dq::launch_pages_shared(a, n_groups, max_group, device_sms(), stream), "shared attention launch");
 }
 
@@ -326,26 +367,9 @@ dq_status dq_pages_weigh(const dq_pages_config *cfg, const dq_pages_buffers *buf
                          long long q_head_stride, const float *lse, float *scores, int cap, const int *rows, const int *cu,
                          int n_rows, int n_tok, int max_new, float sm_scale, void *stream) {
     dq::PagesWeighArgs a{};
-    dq_status s = view(cfg, bufs, layer, true, a.p);
+    const dq_status s = weigh_args(a, cfg, bufs, layer, q, q_tok_stride, q_head_stride, lse, scores, cap, rows, cu, n_rows, n_tok,
+                                   max_new, sm_scale);
     if (s != DQ_OK) return s;
-    if ((s = call_rows(cfg, layer, rows, cu, n_rows, n_tok, max_new, a.r)) != DQ_OK) return s;
-    if (!q || !lse || !scores) return fail(DQ_EINVAL, "q / lse / scores is NULL");
-    if (!aligned16(q) || (q_tok_stride | q_head_stride) & 7)
-        return fail(DQ_EALIGN, "q not 16-byte aligned, or a stride is no multiple of 8 elements");
-    if (!aligned4(lse) || !aligned4(scores)) return fail(DQ_EALIGN, "lse / scores not aligned to 4 bytes");
-    if ((s = check_cap(cap)) != DQ_OK) return s;
-    if (!std::isfinite(sm_scale)) return fail(DQ_EINVAL, "sm_scale is not finite");
-    a.q = static_cast<const uint16_t *>(q);
-    a.qt = q_tok_stride;
-    a.qh = q_head_stride;
-    a.lse = lse;
-    a.scores = scores;
-    a.cap = cap;
-    a.scale_log2 = logit_scale(cfg, sm_scale);
-    uint8_t *ws = static_cast<uint8_t *>(bufs->workspace) + dq::pages_ws_lists(cfg->n_pages);
-    a.tickets = reinterpret_cast<int *>(ws);
-    a.records = reinterpret_cast<float *>(ws + dq::PAGES_MAX_CTAS * 20);
-    a.wait_ns = dq::PAGES_WAIT_NS;
     return launched(dq::launch_pages_weigh(a, device_sms(), stream), "weigh launch");
 }
 
@@ -379,8 +403,45 @@ dq_status dq_pages_test_expire_wait(const dq_pages_config *cfg, const dq_pages_b
                                        n_tok, max_new, nullptr, 0, 1.0f);
     if (s != DQ_OK) return s;
     a.owed = 1;
-    a.wait_ns = limit_ns < 1000ULL ? 1000ULL : (limit_ns > 1000000000ULL ? 1000000000ULL : limit_ns);
+    a.wait_ns = expire_limit(limit_ns);
     return launched(dq::launch_pages_attention(a, dq::PAGES_NEWEST, device_sms(), stream), "expire-wait launch");
+}
+
+dq_status dq_pages_test_expire_cross(const dq_pages_config *cfg, const dq_pages_buffers *bufs, int layer, const void *q,
+                                     long long q_tok_stride, long long q_head_stride, void *out, const int *cu, int n_rows,
+                                     int n_tok, int max_new, unsigned long long limit_ns, void *stream) {
+    dq::PagesAttnArgs a{};
+    const dq_status s = attention_args(a, cfg, bufs, layer, q, q_tok_stride, q_head_stride, out, nullptr, nullptr, cu, n_rows,
+                                       n_tok, max_new, nullptr, 0, 1.0f);
+    if (s != DQ_OK) return s;
+    a.owed = 1;
+    a.wait_ns = expire_limit(limit_ns);
+    return launched(dq::launch_pages_attention(a, dq::PAGES_ALL, device_sms(), stream), "expire-cross launch");
+}
+
+dq_status dq_pages_test_expire_shared(const dq_pages_config *cfg, const dq_pages_buffers *bufs, int layer, const void *q,
+                                      long long q_tok_stride, long long q_head_stride, void *out, const int *cu, int n_rows,
+                                      int n_tok, int max_new, const int *groups, int n_groups, int max_group, const int *plan,
+                                      void *scratch, unsigned long long limit_ns, void *stream) {
+    dq::PagesAttnArgs a{};
+    const dq_status s = shared_args(a, cfg, bufs, layer, q, q_tok_stride, q_head_stride, out, nullptr, nullptr, cu, n_rows, n_tok,
+                                    max_new, groups, n_groups, max_group, plan, scratch, 1.0f);
+    if (s != DQ_OK) return s;
+    a.owed = 1;
+    a.wait_ns = expire_limit(limit_ns);
+    return launched(dq::launch_pages_shared(a, n_groups, max_group, device_sms(), stream), "expire-shared launch");
+}
+
+dq_status dq_pages_test_expire_weigh(const dq_pages_config *cfg, const dq_pages_buffers *bufs, int layer, const void *q,
+                                     long long q_tok_stride, long long q_head_stride, const float *lse, float *scores, int cap,
+                                     const int *cu, int n_rows, int n_tok, int max_new, unsigned long long limit_ns, void *stream) {
+    dq::PagesWeighArgs a{};
+    const dq_status s = weigh_args(a, cfg, bufs, layer, q, q_tok_stride, q_head_stride, lse, scores, cap, nullptr, cu, n_rows, n_tok,
+                                   max_new, 1.0f);
+    if (s != DQ_OK) return s;
+    a.owed = 1;
+    a.wait_ns = expire_limit(limit_ns);
+    return launched(dq::launch_pages_weigh(a, device_sms(), stream), "expire-weigh launch");
 }
 
 dq_status dq_pages_select(const dq_pages_config *cfg, const dq_pages_buffers *bufs, int layer, const void *q,

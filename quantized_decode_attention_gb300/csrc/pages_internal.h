@@ -142,6 +142,7 @@ struct PagesWeighArgs {
     int *tickets;         // workspace, as attention has them
     float *records;       // workspace: [PAGES_MAX_CTAS][2][256]
     unsigned long long wait_ns;
+    unsigned owed;        // as attention's
 };
 struct PagesEvictArgs {
     PagesView p;          // of the pool

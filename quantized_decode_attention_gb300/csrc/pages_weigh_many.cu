@@ -178,7 +178,7 @@ __global__ void __launch_bounds__(THREADS, 1) weigh_many(const PagesWeighArgs a)
             mbar_init(&sh.q_empty[i], 9);
         }
         for (int i = 0; i < KB; i++) {
-            mbar_init(&sh.k_full[i], 4);
+            mbar_init(&sh.k_full[i], 4 + a.owed);
             mbar_init(&sh.k_empty[i], 1);
         }
         for (int i = 0; i < RING; i++) {

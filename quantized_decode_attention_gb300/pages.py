@@ -47,8 +47,11 @@ def _load():
         L.dq_pages_evict.argtypes = [cfg, buf, P, I, P, P, I, I, I, P]
         L.dq_pages_check.argtypes = [buf, P]
         L.dq_pages_test_expire_wait.argtypes = [cfg, buf, I, P, LL, LL, P, P, I, I, I, C.c_ulonglong, P]
+        L.dq_pages_test_expire_cross.argtypes = L.dq_pages_test_expire_wait.argtypes
+        L.dq_pages_test_expire_shared.argtypes = [cfg, buf, I, P, LL, LL, P, P, I, I, I, P, I, I, P, P, C.c_ulonglong, P]
+        L.dq_pages_test_expire_weigh.argtypes = [cfg, buf, I, P, LL, LL, P, P, I, P, I, I, I, C.c_ulonglong, P]
         for f in ("sizes", "resize", "fork", "compact", "append", "read", "attention", "cross", "common", "shared_bytes", "shared",
-                  "select", "weigh", "evict", "check", "test_expire_wait"):
+                  "select", "weigh", "evict", "check", "test_expire_wait", "test_expire_cross", "test_expire_shared", "test_expire_weigh"):
             getattr(L, "dq_pages_" + f).restype = C.c_int
         _ready = L
     return _ready

@@ -71,3 +71,17 @@ def test_shared_bytes(lib, d, hq):  # noqa: F811
         assert lib.dq_pages_shared_bytes(C.byref(c), bad, C.byref(n)) == EINVAL
     assert lib.dq_pages_shared_bytes(None, 5, C.byref(n)) == EINVAL and lib.dq_pages_shared_bytes(C.byref(c), 5, None) == EINVAL
     assert lib.dq_pages_shared_bytes(C.byref(cfg(head_dim=96)), 5, C.byref(n)) == EUNSUPPORTED
+
+
+def test_refused_calls_whose_waits_run_out(lib):  # noqa: F811
+    cross = (0, Q, 4096, 128, Q, None, 2, 2, 1, 1000, None)
+    shared = (0, Q, 4096, 128, Q, None, 2, 2, 1, None, 1, 2, Q, Q, 1000, None)
+    weigh = (0, Q, 4096, 128, Q, Q, 64, None, 2, 2, 1, 1000, None)
+    for name, args in (("cross", cross), ("shared", shared), ("weigh", weigh)):
+        name = "dq_pages_test_expire_" + name
+        refused(lib, name, EINVAL, args=with_(args, _0=2))
+        refused(lib, name, EINVAL, args=with_(args, _1=None))
+        refused(lib, name, EALIGN, args=with_(args, _1=Q + 8))
+        refused(lib, name, EINVAL, b=bufs(workspace=None), args=args)
+    refused(lib, "dq_pages_test_expire_shared", EINVAL, args=with_(shared, _13=None))
+    refused(lib, "dq_pages_test_expire_weigh", EINVAL, args=with_(weigh, _6=0))
