@@ -39,7 +39,11 @@ int allow_shared(int bytes) {
 }
 
 // How many CTAs the launch over the rows' own pages takes, of `grid`, for n places of UNIT_COST and chunks of 32 tokens: few
-// where they are done with it before the common pages are, which then have the other SMs at the same time.
+// where they are done with it before the common pages are, which then have the other SMs at the same time.  With 32 / 48 / 64 / 96 CTAs
+// for up to 6144 places, us (8 KV heads of 128, 4 query heads each): 64 rows of 64 own tokens behind 8192 common ones
+// 36.5 / - / 38.8 / 43.3, behind 2048 29.3 / - / 29.5 / 31.2, of 250 behind 1536 30.0 / 32.0 / 28.8 / -; 16 of 1300 behind 6144
+// 37.9 / 32.8 / 31.1 / -; 128 of 100 behind 1024 34.0 / 31.9 / 29.4 / -; 8 behind 32768 44.8 / - / 53.3 / 68.8; 8 groups of 8 behind 8192
+// 68.9 / - / 85.5 / 126: few where the common pages are many, more where the own ones are; 64 loses least at either end.
 __device__ __forceinline__ int own_ctas(int n, int grid) {
     constexpr int PLACES = 96, MOST = 64;
     return n <= PLACES * MOST ? MOST : grid;

@@ -42,8 +42,9 @@ constexpr float LN2 = 0.69314718055994530942f;
 constexpr float SLACK = 8.f, LIFT = 7.f;   // log2 units
 constexpr int CHUNK = 32;                  // tokens
 constexpr int UNIT_COST = FEW_UNIT_COST;   // (40 ragged rows: 76 us, with 0 94)
-// Places of a unit that CTAs do not share; of common pages, which few units have, fewer (8 rows behind 2000 tokens, 16 units of 64
-// places, four layers: 77 us, with 64 93).
+// Places of a unit that CTAs do not share; of common pages, which few units have, fewer (8 rows behind 2000 tokens, which are shared
+// only where the caller asks for it always, four layers: 77 us, with 64 93; 8 groups of 8 behind 2048 37.7 / 36.1, 20 of 3 behind 2560
+// 45.2 / 41.2; with 8 places 16 groups of 8 behind 1024 40.1 for 33.2).
 constexpr int SHORT_ROWS = 64, SHORT_COMMON = 24;
 constexpr int MIN_PLACES = 16;             // places that make a CTA worth its merge (1 row of 500: 8.4 us, with 64 13.4)
 

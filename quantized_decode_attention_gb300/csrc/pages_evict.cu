@@ -25,6 +25,9 @@
 namespace dq {
 namespace {
 
+// The variants below go by `cap`, the length of the caller's scores, for which the host knows no better: rows much shorter than it
+// pay for one that could be long.  16 rows of 4160 tokens, two layers, with cap 4160 91 us, 32768 97, 131072 105; 64 of 1024 to 512 with
+// cap 1024 63, 32768 80, 131072 104; 4 of 16384 to 2048, eight layers, with 16384 92, 131072 105.  (Below, cap is the rows' length.)
 constexpr int CH_HELD = 48 << 10;  // keys of scores that shared memory holds, at most
 // Longest rows (at most `cap` tokens) that 512 threads choose from, 1024 for longer ones.  512 / 1024, the whole eviction in us: 16 rows
 // of 1024 tokens, two layers, 28 / 36, of 4160 91 / 97; 4 of 16384, eight layers, 92 / 98; 1 of 32768, two layers, 34 to 38 / 35, of
